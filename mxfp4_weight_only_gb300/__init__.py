@@ -17,10 +17,14 @@ from . import _native
 from ._native import (MOE_ACT_SWIGLU, MOE_AQ_FP8, MOE_AQ_MXFP4, MOE_AQ_NONE,  # noqa: F401
                       MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL, MOE_STATUS_BAD_INDEX,
                       MOE_STATUS_NAN_SCALE, MOE_STATUS_WAIT_TIMEOUT, MoeDims, MoeError, MoeOptions, use_checked)
+from .kv_cache import (KvCacheMxfp4, PageTables, attention_kv_mxfp4, attention_read_status,  # noqa: F401
+                       attention_workspace_bytes, kv_append_mxfp4, kv_gather_mxfp4, kv_page_tables)
 
 __all__ = [
     "moe_workspace_bytes", "moe_a16w4_mxfp4", "moe_a16w4_int4g32", "requant_mxfp4_to_int4g32",
     "moe_route", "moe_router_topk", "moe_read_status", "moe_quantize_act", "dims", "MoeError",
+    "KvCacheMxfp4", "PageTables", "kv_page_tables", "kv_append_mxfp4", "kv_gather_mxfp4", "attention_kv_mxfp4",
+    "attention_workspace_bytes", "attention_read_status",
 ]
 
 _AQ = {None: MOE_AQ_NONE, "bf16": MOE_AQ_NONE, "mxfp4": MOE_AQ_MXFP4, "fp8": MOE_AQ_FP8}

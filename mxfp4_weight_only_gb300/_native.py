@@ -1,4 +1,4 @@
-"""ctypes view of ``libmoe_a16w4.so`` (declarations of include/moe_a16w4.h)."""
+"""ctypes view of ``libmoe_a16w4.so`` (declarations of include/moe_a16w4.h and include/kv_mxfp4.h)."""
 
 from __future__ import annotations
 
@@ -42,6 +42,20 @@ class MoeOptions(ctypes.Structure):
 
 _OptP = ctypes.POINTER(MoeOptions)
 
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("data", _vp), ("num_pages", _i32), ("page_size", _i32), ("num_kv_heads", _i32), ("head_dim", _i32)]
+
+
+class KvAttnStruct(ctypes.Structure):
+    _fields_ = [("R", _i32), ("N", _i32), ("Hq", _i32), ("max_blocks", _i32), ("max_q_len", _i32), ("causal", _i32),
+                ("window", _i32), ("q_stride", ctypes.c_int64), ("scale", ctypes.c_float)]
+
+
+_CacheP = ctypes.POINTER(KvCacheStruct)
+_AttnP = ctypes.POINTER(KvAttnStruct)
+
 SIGNATURES = {
     "moe_workspace_bytes": (ctypes.c_size_t, [_DimsP]),
     "moe_a16w4_mxfp4": (ctypes.c_int, [_DimsP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
@@ -64,6 +78,13 @@ SIGNATURES = {
     "moe_noalloc_read_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _vp]),
     "moe_quantize_act": (ctypes.c_int, [_i32, _vp, _i32, ctypes.c_int64, _i32, ctypes.c_float, _vp, _vp, _vp]),
     "moe_set_timing_events": (ctypes.c_int, [ctypes.POINTER(_vp), _i32]),
+    "kv_mxfp4_cache_bytes": (ctypes.c_size_t, [_CacheP]),
+    "kv_mxfp4_page_tables": (ctypes.c_int, [_i32] * 5 + [_vp] * 11),
+    "kv_mxfp4_append": (ctypes.c_int, [_CacheP, _vp, _vp, _i32, ctypes.c_int64, ctypes.c_int64, _i32, _vp, _vp]),
+    "kv_mxfp4_gather": (ctypes.c_int, [_CacheP, _vp, _i32, _vp, _vp, _vp]),
+    "kv_mxfp4_attention_workspace_bytes": (ctypes.c_size_t, [_CacheP, _AttnP]),
+    "kv_mxfp4_attention": (ctypes.c_int, [_CacheP, _AttnP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "kv_mxfp4_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "moe_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_abi_version": (ctypes.c_int, []),
 }

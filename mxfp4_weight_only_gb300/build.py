@@ -22,9 +22,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libmoe_a16w4.so"
 CHECK_LIB_NAME = "libmoe_a16w4_check.so"
-SOURCES = ["api.cu", "route.cu", "requant.cu", "decode.cu", "prefill.cu", "noalloc.cu", "actquant.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "moe_internal.h")] + [
-    os.path.join(ROOT, "include", "moe_a16w4.h")
+SOURCES = ["api.cu", "route.cu", "requant.cu", "decode.cu", "prefill.cu", "noalloc.cu", "actquant.cu",
+           "kv_api.cu", "kv_cache.cu", "kv_attn.cu"]
+HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "moe_internal.h", "kv_internal.h")] + [
+    os.path.join(ROOT, "include", h) for h in ("moe_a16w4.h", "kv_mxfp4.h")
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I" + os.path.join(ROOT, "include")]

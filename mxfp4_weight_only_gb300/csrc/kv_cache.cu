@@ -1,0 +1,352 @@
+// The 4-bit KV cache outside attention: page tables and slot maps from request
+// lengths, the quantising write of new rows, and the read-back.
+#include "common.cuh"
+#include "kv_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTableThreads = 512;
+
+// Exclusive block-wide sums of two values per thread (kTableThreads threads);
+// totals in *ta, *tb.  Sums saturate nowhere: 64 bits.
+__device__ __forceinline__ void block_exclusive2(long long& a, long long& b, long long* ta, long long* tb,
+                                                 long long* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = kTableThreads / 32;
+  long long ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) {
+      ia += xa;
+      ib += xb;
+    }
+  }
+  __syncthreads();  // scratch may still be read by the previous call
+  if (lane == 31) {
+    scratch[warp] = ia;
+    scratch[kWarps + warp] = ib;
+  }
+  __syncthreads();
+  long long pa = 0, pb = 0, sa = 0, sb = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const long long xa = scratch[w], xb = scratch[kWarps + w];
+    if (w < warp) {
+      pa += xa;
+      pb += xb;
+    }
+    sa += xa;
+    sb += xb;
+  }
+  a = pa + ia - a;
+  b = pb + ib - b;
+  *ta = sa;
+  *tb = sb;
+}
+
+// Page tables and slot maps (kv_mxfp4_page_tables).  Latency-bound: a few KB
+// of lengths in, 8 bytes per new token out.  Every CTA redoes the two prefix
+// sums over the requests (tokens, then pages) in shared memory, so one launch
+// needs no grid-wide step; the CTAs then share the tokens and the finished
+// requests.  A token whose position starts a page that its request does not
+// hold yet takes the page off the ring and writes the table entry.
+__global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTableArgs a) {
+  extern __shared__ int32_t sm[];
+  int32_t* start = sm;              // [R + 1] first token of each request
+  int32_t* cached = start + a.R + 1;  // [R]
+  int32_t* ofs = cached + a.R;      // [R] ring offset of its first new page; -1: refused
+  __shared__ long long scratch[2 * (kTableThreads / 32)];
+  const int tid = threadIdx.x, R = a.R;
+  const int page = 1 << a.page_shift;
+  const int per = (R + kTableThreads - 1) / kTableThreads;  // consecutive requests of this thread
+  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  const int head = ((a.state[0] % a.ring_size) + a.ring_size) % a.ring_size;
+  const int avail = min(max(a.state[1], 0), a.ring_size);
+
+  for (int r = tid; r < R; r += kTableThreads) {
+    cached[r] = max(a.cached[r], 0);
+    ofs[r] = a.added[r];
+  }
+  __syncthreads();
+  long long tok = 0, zero = 0, total = 0, unused = 0;
+  for (int r = r0; r < r1; ++r) tok += max(ofs[r], 0);
+  block_exclusive2(tok, zero, &total, &unused, scratch);
+  // pages needed by requests that fit otherwise, pages given back
+  long long need = 0, gone = 0;
+  {
+    long long t = tok;
+    for (int r = r0; r < r1; ++r) {
+      const int n = ofs[r];
+      const long long have = ((long long)cached[r] + page - 1) >> a.page_shift;
+      const long long all = ((long long)cached[r] + max(n, 0) + page - 1) >> a.page_shift;
+      if (n < 0) gone += min(have, (long long)a.max_blocks);
+      else if (t + n <= a.max_tokens && all <= a.max_blocks) need += all - have;
+      t += max(n, 0);
+    }
+  }
+  long long need_all, gone_all;
+  block_exclusive2(need, gone, &need_all, &gone_all, scratch);
+  const bool first = blockIdx.x == 0;
+  long long taken = 0;  // pages taken by this thread's requests
+  for (int r = r0; r < r1; ++r) {
+    const int n = ofs[r];
+    const long long have = ((long long)cached[r] + page - 1) >> a.page_shift;
+    const long long all = ((long long)cached[r] + max(n, 0) + page - 1) >> a.page_shift;
+    start[r] = (int)min(tok, 0x7FFFFFFFll);
+    int seq = 0, o = -1;
+    if (n < 0) {
+      // finished: its pages go to the ring's end, this thread's share of the
+      // CTAs' work below; the offset is kept as -2 - offset
+      o = -2 - (int)gone;
+      gone += min(have, (long long)a.max_blocks);
+    } else {
+      bool ok = tok + n <= a.max_tokens && all <= a.max_blocks;
+      const long long want = ok ? all - have : 0;
+      ok = ok && (want == 0 || need + want <= avail);
+      if (ok) {
+        o = (int)need;
+        taken += want;
+      }
+      need += want;
+      seq = ok ? cached[r] + n : -1;
+      tok += n;
+    }
+    ofs[r] = o;
+    if (first) {
+      a.seq_lens[r] = seq;
+      a.query_start[r] = start[r];
+    }
+  }
+  if (tid == 0) start[R] = (int)min(total, 0x7FFFFFFFll);
+  long long t2 = 0, taken_all;
+  block_exclusive2(taken, t2, &taken_all, &unused, scratch);  // also orders the shared arrays before their readers
+  if (first && tid == 0) {
+    a.query_start[R] = start[R];
+    a.state_out[0] = (int)(((long long)head + taken_all) % a.ring_size);
+    a.state_out[1] = (int)(avail - taken_all + gone_all);
+  }
+
+  const int nt = gridDim.x * kTableThreads;
+  for (int t = blockIdx.x * kTableThreads + tid; t < a.max_tokens; t += nt) {
+    int slot = -1, pos = -1;
+    if (t < start[R]) {
+      int lo = 0, hi = R;  // start[lo] <= t < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      pos = cached[lo] + (t - start[lo]);
+      const int o = ofs[lo];
+      if (o >= 0) {
+        const int b = pos >> a.page_shift;
+        const int have = (cached[lo] + page - 1) >> a.page_shift;
+        int32_t* entry = a.table + (size_t)lo * a.max_blocks + b;
+        int pg;
+        if (b < have) {
+          pg = *entry;
+        } else {
+          pg = a.ring[((long long)head + o + (b - have)) % a.ring_size];
+          if ((pos & (page - 1)) == 0) *entry = pg;
+        }
+        slot = (int)(((long long)pg << a.page_shift) + (pos & (page - 1)));
+      }
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+  }
+  // finished requests: one warp each
+  const int lane = tid & 31, nw = gridDim.x * (kTableThreads / 32);
+  for (int r = blockIdx.x * (kTableThreads / 32) + (tid >> 5); r < R; r += nw) {
+    const int o = ofs[r];
+    if (o > -2) continue;
+    const int have = min((cached[r] + page - 1) >> a.page_shift, a.max_blocks);
+    for (int b = lane; b < have; b += 32)
+      a.ring[((long long)head + avail + (-2 - o) + b) % a.ring_size] = a.table[(size_t)r * a.max_blocks + b];
+  }
+}
+
+// Byte of a record that holds K row byte j (a multiple of 4) of token t, and V row byte j (a multiple of 2).
+template <int D>
+__device__ __forceinline__ int k_byte(int t, int j) {
+  constexpr int NB = D / 32;
+  return ((t * 4 + ((j >> 2) & 3)) * NB + (j >> 4)) * 4;
+}
+template <int D>
+__device__ __forceinline__ int v_byte(int t, int j) {
+  constexpr int NB = D / 32;
+  return 8 * D + ((((((t >> 3) * 8 + ((j >> 1) & 7)) * 4 + ((t >> 1) & 3)) * 2 + (t & 1)) * NB) + (j >> 4)) * 2;
+}
+
+// MXFP4 codes and scale byte of a lane's 8 values of a 32-value block (4
+// lanes; the whole warp calls it), any float inputs: a NaN makes the block's
+// byte 255 (its finite values keep their codes, the rest get 0), an infinity
+// saturates on the largest finite scale (byte 252).
+__device__ __forceinline__ void kv_quant8(float (&v)[8], uint32_t& codes, uint32_t& sbyte) {
+  float m = 0.f;
+  bool odd = false;  // infinite or NaN
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    m = fmaxf(m, fabsf(v[q]));
+    odd |= !(fabsf(v[q]) <= 3.402823466e38f);
+  }
+  bool nan = false;
+  if (__any_sync(0xffffffffu, odd)) {  // rare
+#pragma unroll
+    for (int q = 0; q < 8; ++q) nan |= v[q] != v[q];
+    nan |= (bool)__shfl_xor_sync(0xffffffffu, (int)nan, 1);
+    nan |= (bool)__shfl_xor_sync(0xffffffffu, (int)nan, 2);
+    if (nan) {
+      m = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (!(fabsf(v[q]) <= 3.402823466e38f)) v[q] = 0.f;
+        m = fmaxf(m, fabsf(v[q]));
+      }
+    }
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t s = min(mx_scale_byte(m), 252u);
+  const float rcp = __uint_as_float((254u - s) << 23);  // 2^(127 - s)
+  float r[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) r[q] = v[q] * rcp;
+  codes = f32x8_to_e2m1x8(r);
+  sbyte = nan ? 255u : s;
+}
+
+// Quantising write (kv_mxfp4_append).  HBM-bound: 2 or 4 bytes read and 17/32
+// byte written per value.  D / 8 lanes take one row (a token's K or V of one
+// head); the loop bound is uniform per warp, so every lane reaches the
+// block-maximum shuffles.
+template <int D, bool F32>
+__global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const void* __restrict__ k,
+                                                        const void* __restrict__ v, long long ks, long long vs, int N,
+                                                        const int32_t* __restrict__ slots) {
+  constexpr int L = D / 8, NB = D / 32;  // lanes per row
+  const long long rows = 2ll * N * c.heads;
+  const long long stride = (long long)gridDim.x * (256 / L);
+  const int sub = threadIdx.x % L;
+  for (long long w0 = (long long)blockIdx.x * (256 / L); w0 < rows; w0 += stride) {
+    const long long row = w0 + threadIdx.x / L;
+    const int which = (int)(row & 1);
+    const long long th = row >> 1;
+    const int tok = (int)(th / c.heads), head = (int)(th - (long long)tok * c.heads);
+    const int slot = row < rows ? slots[tok] : -1;
+    const bool live = slot >= 0 && (slot >> c.page_shift) < c.num_pages;
+    float x[8];
+    if (live) {
+      const long long at = (long long)tok * (which ? vs : ks) + (long long)head * D + 8 * sub;
+      if (F32) {
+        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(which ? v : k) + at);
+        const float4 a = __ldcs(p), b = __ldcs(p + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      } else {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(which ? v : k) + at));
+        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    uint32_t codes, sb;
+    kv_quant8(x, codes, sb);
+    if (live) {
+      const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
+      uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
+      if (which) {
+        *reinterpret_cast<uint16_t*>(rec + v_byte<D>(t, 4 * sub)) = (uint16_t)codes;
+        *reinterpret_cast<uint16_t*>(rec + v_byte<D>(t, 4 * sub + 2)) = (uint16_t)(codes >> 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(rec + k_byte<D>(t, 4 * sub)) = codes;
+      }
+      if ((sub & 3) == 0) rec[16 * D + which * (D / 2) + t * NB + (sub >> 2)] = (uint8_t)sb;
+    }
+  }
+}
+
+// Read-back (kv_mxfp4_gather): the write's mapping reversed.
+template <int D>
+__global__ void __launch_bounds__(256) kv_gather_kernel(const KvView c, const int32_t* __restrict__ slots, int N,
+                                                        uint4* __restrict__ ko, uint4* __restrict__ vo) {
+  constexpr int L = D / 8, NB = D / 32;
+  const long long rows = 2ll * N * c.heads;
+  const long long stride = (long long)gridDim.x * (256 / L);
+  const int sub = threadIdx.x % L;
+  for (long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L; row < rows; row += stride) {
+    const int which = (int)(row & 1);
+    const long long th = row >> 1;
+    const int tok = (int)(th / c.heads), head = (int)(th - (long long)tok * c.heads);
+    const int slot = slots[tok];
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (slot >= 0 && (slot >> c.page_shift) < c.num_pages) {
+      const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
+      const uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
+      uint32_t codes;
+      if (which)
+        codes = *reinterpret_cast<const uint16_t*>(rec + v_byte<D>(t, 4 * sub)) |
+                (uint32_t) * reinterpret_cast<const uint16_t*>(rec + v_byte<D>(t, 4 * sub + 2)) << 16;
+      else
+        codes = *reinterpret_cast<const uint32_t*>(rec + k_byte<D>(t, 4 * sub));
+      const uint32_t s = rec[16 * D + which * (D / 2) + t * NB + (sub >> 2)];
+      const float X = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_float(s);
+      uint32_t h[4];
+      e2m1x8_to_f16x8(codes, h[0], h[1], h[2], h[3]);
+      o.x = f32x2_to_bf16x2(f16_lo(h[0]) * X, f16_hi(h[0]) * X);
+      o.y = f32x2_to_bf16x2(f16_lo(h[1]) * X, f16_hi(h[1]) * X);
+      o.z = f32x2_to_bf16x2(f16_lo(h[2]) * X, f16_hi(h[2]) * X);
+      o.w = f32x2_to_bf16x2(f16_lo(h[3]) * X, f16_hi(h[3]) * X);
+    }
+    (which ? vo : ko)[th * L + sub] = o;
+  }
+}
+
+int grid_for(long long units, int per_cta, int num_sms, int ctas_per_sm) {
+  const long long want = (units + per_cta - 1) / per_cta, most = (long long)num_sms * ctas_per_sm;
+  return (int)(want < most ? want : most);
+}
+
+}  // namespace
+
+cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t s) {
+  const size_t smem = 4 * (3 * (size_t)a.R + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               4 * (3 * kMaxTableRequests + 1));
+    if (e != cudaSuccess) return e;
+  }
+  int grid = grid_for(a.max_tokens, 4 * kTableThreads, num_sms, 1);
+  if (grid < 1) grid = 1;
+  page_tables_kernel<<<grid, kTableThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool f32, long long ks, long long vs, int N,
+                             const int32_t* slots, int num_sms, cudaStream_t s) {
+  const int grid = grid_for(2ll * N * c.heads, 256 / (c.D / 8), num_sms, 8);
+  if (c.D == 128) {
+    if (f32) kv_append_kernel<128, true><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
+    else kv_append_kernel<128, false><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
+  } else {
+    if (f32) kv_append_kernel<64, true><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
+    else kv_append_kernel<64, false><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* ko, void* vo, int num_sms,
+                             cudaStream_t s) {
+  const int grid = grid_for(2ll * N * c.heads, 256 / (c.D / 8), num_sms, 8);
+  if (c.D == 128)
+    kv_gather_kernel<128><<<grid, 256, 0, s>>>(c, slots, N, reinterpret_cast<uint4*>(ko), reinterpret_cast<uint4*>(vo));
+  else
+    kv_gather_kernel<64><<<grid, 256, 0, s>>>(c, slots, N, reinterpret_cast<uint4*>(ko), reinterpret_cast<uint4*>(vo));
+  return cudaGetLastError();
+}
+
+}  // namespace moe

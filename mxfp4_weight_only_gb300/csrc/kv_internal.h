@@ -1,0 +1,56 @@
+// Internal declarations of the 4-bit KV cache operators.
+#pragma once
+
+#include "../../include/kv_mxfp4.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+// A record: 16 tokens of one kv head (see kv_mxfp4_cache_t for its layout).
+constexpr int kKvGroup = 16;
+__host__ __device__ constexpr int kv_record_bytes(int D) { return 17 * D; }
+
+// Device view of a cache.
+struct KvView {
+  uint8_t* data;
+  int num_pages, page_shift, heads, D;
+  // record of token group ``gi`` (16 tokens) of ``page`` and ``head``
+  __host__ __device__ size_t record(int page, int head, int gi) const {
+    const int gshift = page_shift - 4;
+    return ((((size_t)page * heads + head) << gshift) + gi) * (size_t)kv_record_bytes(D);
+  }
+};
+
+struct PageTableArgs {
+  int R, page_shift, max_blocks, max_tokens, ring_size;
+  const int32_t *cached, *added;
+  int32_t *table, *ring;
+  const int32_t* state;
+  int32_t *seq_lens, *query_start, *slots, *positions, *state_out;
+};
+constexpr int kMaxTableRequests = 8192;
+cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t s);
+
+cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool f32, long long k_stride,
+                             long long v_stride, int N, const int32_t* slots, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* k_out, void* v_out, int num_sms,
+                             cudaStream_t s);
+
+struct KvAttnArgs {
+  KvView cache;
+  int R, N, Hq, max_blocks, max_q_len;
+  int causal, window;
+  long long q_stride;
+  float scale;
+  const uint16_t* q;
+  const int32_t *table, *seq_lens, *query_start;
+  uint16_t* out;
+  float* lse;
+  uint8_t* workspace;
+  uint32_t* status;
+  int num_sms;
+};
+size_t kv_attention_workspace(const KvView& c, const kv_mxfp4_attn_t* a);
+cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t s);
+
+}  // namespace moe
