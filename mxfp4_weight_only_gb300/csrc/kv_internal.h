@@ -50,6 +50,11 @@ struct KvAttnArgs {
   uint32_t* status;
   int num_sms;
 };
+// Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
+// per kv head), row tiles of 8 * tiles rows (tiles 1 or 2).
+size_t kv_stream_workspace(int D);
+cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, int tiles, uint8_t* ws, cudaStream_t s);
+
 size_t kv_attention_workspace(const KvView& c, const kv_mxfp4_attn_t* a);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t s);
 
