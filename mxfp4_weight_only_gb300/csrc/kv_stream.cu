@@ -17,13 +17,16 @@
 // those below 2^-32; one bf16 weight has 8 bits).  Value scales outside
 // 2^-63 .. 2^64 (or NaN bytes) take an exact float32 path (add_group_f32).
 //
-// Work: a unit is one record of one item (request, kv head, row tile); the
-// units of all items in order are cut into equal runs, one per warp of a
-// one-CTA-per-SM grid, so ragged batches balance without a host-side plan: every
-// CTA finds its place by a prefix sum over the requests.  Each warp streams its
+// Work: a unit is one record of one item (request, kv head, row tile).  All items
+// in order, each at the cost of its units and kItemCost more (its queries and
+// its result), are cut into equal runs, one per warp of a one-CTA-per-SM grid,
+// so ragged batches balance without a host-side plan: every CTA finds its place
+// by a prefix sum over the requests.  Each warp streams its
 // run through a private ring of bulk copies (one per record) without any
 // barrier with other warps.  Items cut between warps are merged in shared
 // memory, items cut between CTAs through the workspace by kv_merge_kernel.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -37,10 +40,11 @@ constexpr uint64_t kKvWaitNs = kWaitLimitNs;
 template <int D, int NT>
 struct StreamCfg {
   static constexpr int NB = D / 32;
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRec = 17 * D;
-  static constexpr int kStages = (NT == 1 ? 4 : 8) * (128 / D);
+  static constexpr int kStages = (NT == 1 ? 4 : 8) * (128 / D);  // a power of two, at most 32
+  static constexpr int kStep = NT == 1 ? 2 : 1;                  // records per softmax step
   static constexpr int kCols = 8 * NT;
   // a piece in shared memory: O [kCols][D + 4] float, m, l [kCols], reference scale E
   static constexpr int kPieceFloats = kCols * (D + 4) + 2 * kCols + 4;
@@ -50,14 +54,19 @@ struct StreamCfg {
   static constexpr int kSmem = kWarps * (kRingBytes + kStash);
 };
 
-// Workspace after the status region: per CTA two part headers and two parts.
+// What an item costs beside its units, in units (measured: about 2 us a piece
+// next to 1.3 us a unit and warp on a busy SM).
+constexpr int kItemCost = 2;
+
+// A piece of an item: one warp's (shared memory) or one CTA's (workspace).
 struct PartHead {
-  long long item;  // first unit of the item
-  int units;       // its units
-  int r, pair;     // request; kv head * row tiles + row tile
-  int starts;      // 1: the item starts in this CTA and ends in a later one
-  int E;
-  int pad;
+  long long item;  // the item's first unit, counted over all items
+  int units;       // units of the item; 0: no piece here
+  int qb, rows;    // first query row of the request; its rows (query rows x heads)
+  int hq0, col0;   // first query head; first row of the row tile
+  int starts;      // workspace: 1 = the item starts in this CTA and ends in a later one
+  int last_cta;    // the CTA of its last unit
+  int E;           // O is in units of 2^(E - 127)
 };
 
 __host__ __device__ constexpr size_t part_floats(int cols, int D) { return (size_t)cols * D + 2 * cols; }
@@ -69,14 +78,25 @@ struct StreamParams {
   int max_ctas;
   PartHead* heads;   // [grid][2]
   float* parts;      // [grid][2][part_floats]
-  long long* plan;   // [2]: units, active warps
 };
 
 // What a request asks for: rows, the record range any of its rows can see.
 struct Req {
   int qb, ql, n, glo, ng, rt;
-  __device__ __forceinline__ long long units(int heads) const { return (long long)ng * heads * rt; }
+  __device__ __forceinline__ int items(int heads) const { return ng > 0 ? heads * rt : 0; }
 };
+
+// a / b, a % b for b >= 1; 32-bit where a allows.
+__device__ __forceinline__ long long divmod(long long a, int b, int& rem) {
+  if ((a >> 32) == 0) {
+    const uint32_t q = (uint32_t)a / (uint32_t)b;
+    rem = (int)((uint32_t)a - q * (uint32_t)b);
+    return q;
+  }
+  const long long q = a / b;
+  rem = (int)(a - q * b);
+  return q;
+}
 
 template <int COLS>
 __device__ __forceinline__ Req request(const StreamParams& p, int r) {
@@ -170,11 +190,73 @@ __device__ __forceinline__ void load_words(const uint8_t* p, int lane, uint32_t 
   }
 }
 
-// A token's NB scale bytes in the low bytes of a word; unused bytes hold ``fill``'s.
+// A token's NB scale bytes in a word (NB = 2: twice).
 template <int NB>
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int tok, uint32_t fill) {
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int tok) {
   if (NB == 4) return *reinterpret_cast<const uint32_t*>(p + 4 * tok);
-  return *reinterpret_cast<const uint16_t*>(p + 2 * tok) | (fill & 0xFFFF0000u);
+  const uint32_t v = *reinterpret_cast<const uint16_t*>(p + 2 * tok);
+  return v | (v << 16);
+}
+
+// The scale words of tokens tok and tok + 1 (tok even).
+template <int NB>
+__device__ __forceinline__ void scale_word2(const uint8_t* p, int tok, uint32_t& a, uint32_t& b) {
+  if (NB == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + 4 * tok);
+    a = u.x;
+    b = u.y;
+  } else {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p + 2 * tok);
+    a = prmt(u, 0u, 0x1010u);
+    b = prmt(u, 0u, 0x3232u);
+  }
+}
+
+// 2^(s-127) of the two bytes of each half of ``w``: bf16 pairs, exact (255: NaN).
+__device__ __forceinline__ void e8m0x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.bf16x2.ue8m0x2 %0, l;\n cvt.rn.bf16x2.ue8m0x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// Top bit of a byte set where the byte lies in 64 .. 191 (its two top bits differ).
+__device__ __forceinline__ uint32_t usual(uint32_t w) { return w ^ (w << 1); }
+
+// Key scale bytes plus ``shift`` (255 stays), within 0 .. 254: for factors of an unusual size.
+__device__ __noinline__ uint32_t shifted_scales(uint32_t w, int shift) {
+  uint32_t r = 0;
+  for (int b = 0; b < 4; ++b) {
+    const int x = (w >> (8 * b)) & 255;
+    r |= (uint32_t)(x == 255 ? 255 : min(max(x + shift, 0), 254)) << (8 * b);
+  }
+  return r;
+}
+
+// Any byte of a word outside 64 .. 191 and not 0?
+__device__ __forceinline__ bool unusual_scale(uint32_t w) {
+  bool r = false;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t x = (w >> (8 * b)) & 255u;
+    r |= x != 0u && x - 64u > 127u;
+  }
+  return r;
+}
+
+// Any byte equal to 255?
+__device__ __forceinline__ bool has_nan_byte(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u) != 0u;
+}
+
+// Largest byte of a word, 255 excluded.
+__device__ __forceinline__ int largest_scale(uint32_t w) {
+  int m = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int x = (w >> (8 * b)) & 255;
+    if (x != 255) m = max(m, x);
+  }
+  return m;
 }
 
 // One item's state in a warp.  Lane (g, t) = (lane / 4, lane % 4) holds, for its
@@ -183,13 +265,13 @@ template <int D, int NT>
 struct Acc {
   static constexpr int NB = D / 32;
   float o[NT][NB][2][4];  // [tile][block][dims 01 / 23][dim a rows 2t, 2t+1; dim b rows 2t, 2t+1]
-  float m[NT][2], l[NT][2];
-  int E;
+  float m[NT][2], l[NT][2];  // reference of the scores (before the factor f), sum of weights
+  float mf[NT][2];           // m f, 0 while m is -inf
+  int E;                     // O is in units of 2^(E - 127)
 };
 
 // O += p V in float32 for one record, any value scales (the exceptional case):
-// the weights of token k come from the lane that holds them.  O is kept in units
-// of 2^(E - 127).
+// the weights of token k come from the lane that holds them.
 template <int D, int NT>
 __device__ __noinline__ void add_group_f32(Acc<D, NT>& A, const uint8_t* rec, int lane, const float (&p)[NT][4],
                                            int valid) {
@@ -223,36 +305,43 @@ __device__ __noinline__ void add_group_f32(Acc<D, NT>& A, const uint8_t* rec, in
   }
 }
 
-// Largest value-scale byte (255 excluded) of the valid tokens of a record, warp-wide.
-template <int NB>
-__device__ __forceinline__ int largest_scale(uint32_t w0, uint32_t w1, bool ok0, bool ok1) {
-  int mx = 0;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int x = (w0 >> (8 * b)) & 255, y = (w1 >> (8 * b)) & 255;
-    if (ok0 && x != 255) mx = max(mx, x);
-    if (ok1 && y != 255) mx = max(mx, y);
+template <int N>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[N]) {
+  if (N == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
+    v[N - 2] = x.z;
+    v[N - 1] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[1] = x.y;
   }
-  return __reduce_max_sync(0xffffffffu, mx);
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[N]) {
+  if (N == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[N - 2], v[N - 1]);
+  else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
 }
 
-// Any of a word's first NB bytes outside 64 .. 191 and not 0?
-template <int NB>
-__device__ __forceinline__ bool unusual_scale(uint32_t w) {
-  bool r = false;
+// One finished row (row ``c`` of its request's rows x heads): lane holds dims
+// (D / 32) lane .. of O (units of 2^(E - 127)); l the sum of weights, m their
+// reference in units of log2.
+template <int D>
+__device__ __forceinline__ void store_row(const KvAttnArgs& a, const PartHead& h, int c, int G, const float (&o)[D / 32],
+                                          float l, float m, int E, int lane) {
+  const int row = c / G;
+  const size_t at = (size_t)(h.qb + row) * a.Hq + h.hq0 + c - row * G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t w[D / 64];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const uint32_t x = (w >> (8 * b)) & 255u;
-    r |= x != 0u && x - 64u > 127u;
-  }
-  return r;
-}
-
-// Any byte of a word equal to 255?
-__device__ __forceinline__ bool has_nan_byte(uint32_t w, int nb) {
-  bool r = false;
-  for (int b = 0; b < nb; ++b) r |= ((w >> (8 * b)) & 255u) == 255u;
-  return r;
+  for (int d = 0; d < D / 64; ++d)
+    w[d] = f32x2_to_bf16x2(mul_pow2(o[2 * d] * inv, E - 127), mul_pow2(o[2 * d + 1] * inv, E - 127));
+  uint16_t* dst = a.out + at * D + (D / 32) * lane;
+  if (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[D / 64 - 1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f;
 }
 
 template <int D, int NT>
@@ -261,10 +350,13 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   constexpr int NB = C::NB, W = C::kWarps, S = C::kStages, REC = C::kRec, COLS = C::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W * S];
-  __shared__ long long sc_scan[W], start_off[W];
-  __shared__ int start_r[W];
-  __shared__ PartHead ph[W][2];    // pieces left by each warp: [0] its first, [1] its last
-  __shared__ int empties[C::kThreads], n_empty;
+  __shared__ long long scan_c[W], scan_u[W];
+  __shared__ int n_empty, empties[C::kThreads];
+  // where each warp's run starts ([W]: where the last one ends): request, item
+  // within it, unit within that; units before it; cost before its request
+  __shared__ int at_r[W + 1], at_item[W + 1], at_g[W + 1];
+  __shared__ long long at_unit[W + 1], at_cost[W + 1];
+  __shared__ PartHead ph[2 * W];  // pieces left by each warp: its first, its last
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -274,43 +366,56 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   if (lane == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&bars[warp * S + s], 1);
     fence_barrier_init();
-    ph[warp][0].units = ph[warp][1].units = 0;
-    start_r[warp] = -1;
+    ph[2 * warp].units = ph[2 * warp + 1].units = 0;
   }
+  if (tid < 2) p.heads[2 * blockIdx.x + tid].units = 0;
   grid_dep_launch_dependents();
 
-  // ---------------------------------------------------------------- units of all requests
+  // ---------------------------------------------------------------- cost and units of all requests
   const int H = a.cache.heads;
-  long long total = 0;
   const int chunks = (a.R + C::kThreads - 1) / C::kThreads;
-  long long my_first = 0;  // first unit of request tid (first chunk), kept for the search below
-  for (int ch = 0; ch < chunks; ++ch) {
+  long long T = 0, U = 0;          // totals so far
+  long long first_c = 0, first_u = 0;  // before request tid of the last chunk scanned
+  Req mine{};
+  auto scan = [&](int ch) {
     const int r = ch * C::kThreads + tid;
-    long long u = 0;
-    if (tid == 0) n_empty = 0;
-    __syncthreads();
-    if (r < a.R) {
-      const Req q = request<COLS>(p, r);
-      u = q.units(H);
-      // requests without a key: their rows are zeros, written by one CTA each
-      if (u == 0 && q.rt > 0 && r % gridDim.x == blockIdx.x) empties[atomicAdd(&n_empty, 1)] = r;
-    }
-    long long incl = u;
+    mine = Req{};
+    if (r < a.R) mine = request<COLS>(p, r);
+    const long long it = mine.items(H), c = it * (mine.ng + kItemCost), u = it * mine.ng;
+    long long ic = c, iu = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      const long long xc = __shfl_up_sync(0xffffffffu, ic, o), xu = __shfl_up_sync(0xffffffffu, iu, o);
+      if (lane >= o) {
+        ic += xc;
+        iu += xu;
+      }
     }
-    if (lane == 31) sc_scan[warp] = incl;
+    __syncthreads();  // the previous chunk's sums have been read
+    if (lane == 31) {
+      scan_c[warp] = ic;
+      scan_u[warp] = iu;
+    }
     __syncthreads();
-    long long before = total, sum = 0;
+    first_c = T + ic - c;
+    first_u = U + iu - u;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (w < warp) before += sc_scan[w];
-      sum += sc_scan[w];
+      const long long xc = scan_c[w], xu = scan_u[w];
+      if (w < warp) {
+        first_c += xc;
+        first_u += xu;
+      }
+      T += xc;
+      U += xu;
     }
-    my_first = before + incl - u;
-    total += sum;
+  };
+  for (int ch = 0; ch < chunks; ++ch) {
+    if (tid == 0) n_empty = 0;
+    scan(ch);
+    // requests without a key: their rows are zeros, written by one CTA each
+    if (mine.rt > 0 && mine.ng <= 0 && tid % gridDim.x == blockIdx.x) empties[atomicAdd(&n_empty, 1)] = ch * C::kThreads + tid;
+    __syncthreads();
     for (int k = 0; k < n_empty; ++k) {
       const Req q = request<COLS>(p, empties[k]);
       const long long rows = (long long)q.ql * a.Hq;
@@ -321,77 +426,75 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     }
     __syncthreads();
   }
-  const long long U = total;
-  const long long all_warps = (long long)gridDim.x * W;
-  const long long A_w = max(min(all_warps, U), 1ll);  // active warps
-  auto begin_of = [&](long long w) { return w >= A_w ? U : w * U / A_w; };
-  const long long gw0 = (long long)blockIdx.x * W, cta_lo = begin_of(gw0), cta_hi = begin_of(gw0 + W);
-  if (blockIdx.x == 0 && tid == 0) {
-    p.plan[0] = U;
-    p.plan[1] = A_w;
-  }
-  if (tid < 2) p.heads[2 * blockIdx.x + tid].units = 0;
-  if (cta_lo >= cta_hi) return;
-  // the request in which each warp's run starts: the thread that holds it tells
-  long long base = 0;
+  if (U == 0) return;
+  // equal runs of cost: the first ``rem`` of A warps take one more
+  const long long cost = T;
+  const int A_w = (int)min((long long)gridDim.x * W, cost);
+  int rem;
+  const long long per = divmod(cost, A_w, rem);
+  auto begin_of = [&](int w) { return w >= A_w ? cost : w * per + min(w, rem); };
+  auto cta_of = [&](long long c) {  // the CTA in whose run cost index c lies
+    const long long cut = rem * (per + 1);
+    int x;
+    return (int)(c < cut ? divmod(c, (int)(per + 1), x) : rem + divmod(c - cut, (int)per, x)) / W;
+  };
+  const int gw0 = blockIdx.x * W;
+  if (begin_of(gw0) >= cost) return;
   for (int ch = 0; ch < chunks; ++ch) {
-    const int r = ch * C::kThreads + tid;
-    long long u = 0, first;
-    if (r < a.R) u = request<COLS>(p, r).units(H);
-    if (chunks == 1) {
-      first = my_first;
-    } else {
-      long long incl = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      if (lane == 31) sc_scan[warp] = incl;
-      __syncthreads();
-      first = base + incl - u;
-      long long sum = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) first += sc_scan[w];
-        sum += sc_scan[w];
-      }
-      base += sum;
+    if (chunks > 1) {
+      if (ch == 0) T = U = 0;
+      scan(ch);
     }
-    if (u > 0 && first < cta_hi && first + u > cta_lo) {
-      for (int w = 0; w < W; ++w) {
+    const int it = mine.items(H);
+    const long long c = (long long)it * (mine.ng + kItemCost);
+    if (c > 0 && first_c <= begin_of(gw0 + W) && first_c + c > begin_of(gw0)) {
+      for (int w = 0; w <= W; ++w) {
         const long long b = begin_of(gw0 + w);
-        if (b >= first && b < first + u && b < begin_of(gw0 + w + 1)) {
-          start_r[w] = r;
-          start_off[w] = b - first;
+        // (the end of everything belongs to the request that ends there)
+        if (b >= first_c && (b < first_c + c || (b == cost && first_c + c == cost))) {
+          int x;
+          const int k = (int)divmod(b - first_c, mine.ng + kItemCost, x);
+          at_r[w] = ch * C::kThreads + tid;
+          at_item[w] = k;
+          at_g[w] = max(0, x - kItemCost);
+          at_unit[w] = first_u + (long long)k * mine.ng + max(0, x - kItemCost);
+          at_cost[w] = first_c;
         }
       }
     }
-    __syncthreads();
   }
+  __syncthreads();
+  const long long cta_lo = at_unit[0], cta_hi = at_unit[W];
 
   // ---------------------------------------------------------------- this warp's run
-  const long long u_lo = begin_of(gw0 + warp), u_hi = begin_of(gw0 + warp + 1);
-  const int n_units = (int)(u_hi - u_lo);
+  const long long u_lo = at_unit[warp];
+  const int n_units = (int)(at_unit[warp + 1] - u_lo);
   if (n_units > 0) {
     // record addresses, 32 units at a time, one per lane; null for a page outside the cache
-    int br = start_r[warp];
-    long long bo = start_off[warp];
+    int br = at_r[warp];
+    long long bo;  // units of request br before the next batch
+    {
+      const Req q = request<COLS>(p, br);
+      bo = (long long)at_item[warp] * q.ng + at_g[warp];
+    }
     auto addresses = [&](int i0) -> const uint8_t* {
       const uint8_t* ptr = nullptr;
       int r = br;
       long long off = bo + lane;
       if (i0 + lane < n_units) {
         Req q = request<COLS>(p, r);
-        while (off >= q.units(H)) {
-          off -= q.units(H);
+        long long u = (long long)q.items(H) * q.ng;
+        while (off >= u) {
+          off -= u;
           q = request<COLS>(p, ++r);
+          u = (long long)q.items(H) * q.ng;
         }
-        const int pair = (int)(off / q.ng), gi = q.glo + (int)(off - (long long)pair * q.ng);
-        const int tok = gi << 4;
+        int gi;
+        const int item = (int)divmod(off, q.ng, gi);
+        const int tok = (q.glo + gi) << 4;
         const int pg = a.table[(size_t)r * a.max_blocks + (tok >> a.cache.page_shift)];
         if (pg >= 0 && pg < a.cache.num_pages)
-          ptr = a.cache.data + a.cache.record(pg, pair / q.rt, (tok & ((1 << a.cache.page_shift) - 1)) >> 4);
+          ptr = a.cache.data + a.cache.record(pg, item / q.rt, (tok & ((1 << a.cache.page_shift) - 1)) >> 4);
       }
       // the next 32 start after lane 31's
       br = __shfl_sync(0xffffffffu, r, 31);
@@ -400,37 +503,40 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     };
     const uint64_t policy = l2_policy_evict_first();
     const uint8_t* cur = addresses(0);
-    const uint8_t* nxt = n_units > 32 ? addresses(32) : nullptr;
+    const uint8_t* nxt = nullptr;
+    uint32_t here = __ballot_sync(0xffffffffu, cur != nullptr);  // which of the 32 have a record
     uint64_t* bar = bars + warp * S;
-    auto issue = [&](int i, const uint8_t* c0, const uint8_t* c1, int batch) {
-      // unit i lies in batch ``batch`` (addresses c0) or the next one (c1)
-      const unsigned long long v = (unsigned long long)((i >> 5) == batch ? c0 : c1);
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, v, i & 31));
-      if (lane == 0) {
-        const int s = i % S;
+    // copies of the units i0 .. i0 + n - 1 (at most 32): each by the lane that holds its address
+    auto issue = [&](int i0, int n, int batch) {
+      const int d = (lane - i0) & 31, i = i0 + d;
+      if (d < n && i < n_units) {
+        const uint8_t* src = (i >> 5) == batch ? cur : nxt;
+        const uint32_t st = (uint32_t)i % S;
         if (src) {
-          mbar_arrive_expect_tx(&bar[s], REC);
-          bulk_g2s(ring + s * REC, src, REC, &bar[s], policy);
+          mbar_arrive_expect_tx(&bar[st], REC);
+          bulk_g2s(ring + st * REC, src, REC, &bar[st], policy);
         } else {
-          mbar_arrive(&bar[s]);
+          mbar_arrive(&bar[st]);
         }
       }
     };
-    for (int i = 0; i < min(S, n_units); ++i) issue(i, cur, nxt, 0);
+    issue(0, S, 0);
+    if (n_units > 32) nxt = addresses(32);
 
-    int cr = start_r[warp];
-    long long co = start_off[warp];
+    int cr = at_r[warp], citem = at_item[warp], cg = at_g[warp];
+    long long ccost = at_cost[warp];
+    Req q = request<COLS>(p, cr);
     bool alive = true;
     int i = 0;
     while (i < n_units && alive) {
       // ------------------------------------------------------------ next item
-      Req q = request<COLS>(p, cr);
-      while (co >= q.units(H)) {
-        co -= q.units(H);
+      while (citem >= q.items(H)) {
+        ccost += (long long)q.items(H) * (q.ng + kItemCost);
         q = request<COLS>(p, ++cr);
+        citem = 0;
       }
-      const int pair = (int)(co / q.ng), g0 = (int)(co - (long long)pair * q.ng);
-      const int kvh = pair / q.rt, rt = pair - kvh * q.rt;
+      const int g0 = cg;
+      const int kvh = citem / q.rt, rt = citem - kvh * q.rt;
       const int len = min(q.ng - g0, n_units - i);
       const long long item = u_lo + i - g0;
       // queries: f16 times a power of two per row; f folds scale and log2 e
@@ -441,7 +547,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       {
         const int rows = q.ql * p.G;
         float fcol[NT];
-        int fe = -10000;
+        int fe = -127;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int c = rt * COLS + nt * 8 + g;
@@ -470,15 +576,22 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              qf[nt][b][k] = f32x2_to_f16x2(mul_pow2(bf16_lo(w[k]), -e), mul_pow2(bf16_hi(w[k]), -e));
+              qf[nt][b][k] = f32x2_to_f16x2(mul_pow2(bf16_lo(w[k]), -e), mul_pow2(bf16_hi(w[k]), -e)) ^
+                             (a.scale < 0.f ? 0x80008000u : 0u);
           }
-          fcol[nt] = mul_pow2(a.scale * kLog2e, e);
-          if (c < rows && fcol[nt] != 0.f) fe = max(fe, (int)((__float_as_uint(fcol[nt]) >> 23) & 255u) - 127);
+          // (a negative scale's sign goes into the queries: factors are positive)
+          fcol[nt] = mul_pow2(fabsf(a.scale) * kLog2e, e);
+          if (fcol[nt] == 0.f) {  // scores of 0: by the queries, so that hidden keys stay at -inf
+            fcol[nt] = 1.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qf[nt][b][0] = qf[nt][b][1] = qf[nt][b][2] = qf[nt][b][3] = 0u;
+          }
+          if (c < rows) fe = max(fe, (int)((__float_as_uint(fcol[nt]) >> 23) & 255u) - 127);
         }
         // factors of an unusual size go into the key scales, so that partial sums
         // stay near the scores' size
         fe = __reduce_max_sync(0xffffffffu, fe);
-        shift = fe > -9999 && (fe > 40 || fe < -40) ? min(max(fe, -126), 126) : 0;
+        shift = fe > 40 || fe < -40 ? min(max(fe, -126), 126) : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float v = mul_pow2(fcol[nt], -shift);
@@ -515,160 +628,195 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           for (int k = 0; k < 8; ++k) A.o[nt][b][k >> 2][k & 3] = 0.f;
         A.m[nt][0] = A.m[nt][1] = -INFINITY;
         A.l[nt][0] = A.l[nt][1] = 0.f;
+        A.mf[nt][0] = A.mf[nt][1] = 0.f;
       }
 
-      for (int k = 0; k < len; ++k, ++i) {
-        const int s = i % S;
-        if (!mbar_wait(&bar[s], (i / S) & 1, a.status, kKvWaitNs)) {
-          alive = false;
-          break;
-        }
-        const uint8_t* rec = ring + s * REC;
-        const bool present = __shfl_sync(0xffffffffu, (unsigned long long)cur, i & 31) != 0ull;
-        if (present) {
-          const int j0 = (q.glo + g0 + k) << 4;
-          const int valid = q.n - j0;  // tokens of the record that exist (above 16: all)
-          // ---------------------------------------------------- scores
-          float sc[NT][4];
+      // reference of the maximum, and what a score may exceed it by: 8 in units of log2
+      float margin[NT][2], limit[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          margin[nt][c] = 8.f / f[nt][c];
+          limit[nt][c] = -INFINITY;
+        }
+
+      // one softmax step over the records i .. i + NG - 1 (NG a compile-time count)
+      auto step = [&](auto ng_tag, int k) {
+        constexpr int NG = decltype(ng_tag)::value;
+        float sc[NG][NT][4];
+        uint32_t vsa[NG][2], vsb[NG][2];  // value scales of tokens 2t, 2t+1 (a, b), plus 8
+        const uint8_t* rec[NG];
+        const int j0 = (q.glo + g0 + k) << 4;
+        uint32_t ok = 0x80808080u;
+        const int ct = lane & 15;  // the token whose key (lanes 0-15) or value scales this lane looks at
+        const int coff = 16 * D + (lane >> 4) * (D / 2);
+#pragma unroll
+        for (int r = 0; r < NG; ++r) {
+          rec[r] = ring + ((uint32_t)(i + r) % S) * REC;
+          const int valid = q.n - (j0 + 16 * r);  // tokens of the record that exist (above 16: all)
+          // -------------------------------------------------- scores
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) sc[r][nt][0] = sc[r][nt][1] = sc[r][nt][2] = sc[r][nt][3] = 0.f;
           uint32_t kw[2][NB];
-          load_words<NB>(rec, lane, kw);
-          uint32_t ks0 = scale_word<NB>(rec + 16 * D, g, 0x7F7F7F7Fu), ks1 = scale_word<NB>(rec + 16 * D, g + 8, 0x7F7F7F7Fu);
-          uint32_t vs0 = scale_word<NB>(rec + 16 * D + D / 2, g, 0x7F7F7F7Fu),
-                   vs1 = scale_word<NB>(rec + 16 * D + D / 2, g + 8, 0x7F7F7F7Fu);
-          if (valid < 16) {
-            if (g >= valid) ks0 = 0x7F7F7F7Fu;
-            if (g + 8 >= valid) ks1 = 0x7F7F7F7Fu;
+          load_words<NB>(rec[r], lane, kw);
+          uint32_t ks0 = scale_word<NB>(rec[r] + 16 * D, g), ks1 = scale_word<NB>(rec[r] + 16 * D, g + 8);
+          scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t, vsa[r][0], vsb[r][0]);
+          scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t + 8, vsa[r][1], vsb[r][1]);
+          uint32_t look = scale_word<NB>(rec[r] + coff, ct);
+          const bool gone = !((here >> ((i + r) & 31)) & 1u);  // no record: a page outside the cache
+          if (valid < 16 || gone) {  // what lies past the end is not looked at
+            const int v = gone ? 0 : valid;
+            if (g >= v) ks0 = 0x7F7F7F7Fu;
+            if (g + 8 >= v) ks1 = 0x7F7F7F7Fu;
+            if (2 * t >= v) vsa[r][0] = 0x7F7F7F7Fu;
+            if (2 * t + 1 >= v) vsb[r][0] = 0x7F7F7F7Fu;
+            if (2 * t + 8 >= v) vsa[r][1] = 0x7F7F7F7Fu;
+            if (2 * t + 9 >= v) vsb[r][1] = 0x7F7F7F7Fu;
+            if (ct >= v) look = 0x7F7F7F7Fu;
+          }
+          ok &= usual(look);
+          if (shift != 0) {
+            ks0 = shifted_scales(ks0, shift);
+            ks1 = shifted_scales(ks1, shift);
           }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             uint32_t x[4], y[4];
             e2m1x8_to_f16x8(kw[0][b], x[0], x[1], x[2], x[3]);
             e2m1x8_to_f16x8(kw[1][b], y[0], y[1], y[2], y[3]);
-            float s0, s1;
-            if (shift == 0) {
-              // byte -> 2^(s-127): 0 gives 0 (for 2^-127), 255 infinity, which poisons the score below
-              s0 = __uint_as_float((b < 3 ? ks0 << (23 - 8 * b) : ks0 >> 1) & 0x7F800000u);
-              s1 = __uint_as_float((b < 3 ? ks1 << (23 - 8 * b) : ks1 >> 1) & 0x7F800000u);
-            } else {
-              const int b0 = (ks0 >> (8 * b)) & 255, b1 = (ks1 >> (8 * b)) & 255;
-              s0 = __uint_as_float((uint32_t)(b0 == 255 ? 255 : min(max(b0 + shift, 0), 254)) << 23);
-              s1 = __uint_as_float((uint32_t)(b1 == 255 ? 255 : min(max(b1 + shift, 0), 254)) << 23);
-            }
+            // byte -> 2^(s-127): 0 gives 0 (for 2^-127); 255 is seen to below
+            const float s0 = __uint_as_float((b < 3 ? ks0 << (23 - 8 * b) : ks0 >> 1) & 0x7F800000u);
+            const float s1 = __uint_as_float((b < 3 ? ks1 << (23 - 8 * b) : ks1 >> 1) & 0x7F800000u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
               const float z[4] = {0.f, 0.f, 0.f, 0.f};
               mma_f16_16816(d, x[0], y[0], x[1], y[1], qf[nt][b][0], qf[nt][b][1], z);
               mma_f16_16816(d, x[2], y[2], x[3], y[3], qf[nt][b][2], qf[nt][b][3], d);
-              sc[nt][0] = fmaf(d[0], s0, sc[nt][0]);
-              sc[nt][1] = fmaf(d[1], s0, sc[nt][1]);
-              sc[nt][2] = fmaf(d[2], s1, sc[nt][2]);
-              sc[nt][3] = fmaf(d[3], s1, sc[nt][3]);
+              sc[r][nt][0] = fmaf(d[0], s0, sc[r][nt][0]);
+              sc[r][nt][1] = fmaf(d[1], s0, sc[r][nt][1]);
+              sc[r][nt][2] = fmaf(d[2], s1, sc[r][nt][2]);
+              sc[r][nt][3] = fmaf(d[3], s1, sc[r][nt][3]);
             }
           }
+        }
+        // ---------------------------------------------------- scales of an unusual size
+        bool wide = A.E != 127;
+        if (__any_sync(0xffffffffu, ok != 0x80808080u) || wide) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int r = 0; r < NG; ++r) {
+            const bool gone = !((here >> ((i + r) & 31)) & 1u);
+            const int v = gone ? 0 : q.n - (j0 + 16 * r);
+            // NaN blocks of keys or values make their token NaN
+            const uint8_t* ks = rec[r] + 16 * D;
+            const float nan = __uint_as_float(0x7FC00000u);
+            const bool n0 = g < v && (has_nan_byte(scale_word<NB>(ks, g)) || has_nan_byte(scale_word<NB>(ks + D / 2, g)));
+            const bool n1 = g + 8 < v &&
+                            (has_nan_byte(scale_word<NB>(ks, g + 8)) || has_nan_byte(scale_word<NB>(ks + D / 2, g + 8)));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float v = sc[nt][c] * f[nt][c & 1];
-              sc[nt][c] = fmaf(v, 0.f, v);  // infinities become NaN
+            for (int nt = 0; nt < NT; ++nt) {
+              if (n0) sc[r][nt][0] = sc[r][nt][1] = nan;
+              if (n1) sc[r][nt][2] = sc[r][nt][3] = nan;
             }
-          // ---------------------------------------------------- value scales
-          if (valid < 16) {
-            if (g >= valid) vs0 = 0x7F7F7F7Fu;
-            if (g + 8 >= valid) vs1 = 0x7F7F7F7Fu;
-          }
-          // the common case: every byte in 64 .. 191 (its two top bits differ) and O in units of 1
-          bool wide = A.E != 127;
-          if (__any_sync(0xffffffffu, ((vs0 ^ (vs0 << 1)) & (vs1 ^ (vs1 << 1)) & 0x80808080u) != 0x80808080u) || wide) {
-            // zero bytes are as good: blocks below 2^-124, multiplied by 0
-            wide |= (bool)__any_sync(0xffffffffu, unusual_scale<NB>(vs0) || unusual_scale<NB>(vs1));
-            if (wide) {
-              const int mx = largest_scale<NB>(vs0, vs1, g < valid, g + 8 < valid);
-              if (mx > A.E + 60) {  // sums of values this large would overflow in the present unit
+            // zero value scales are as good as usual ones: blocks below 2^-124, next to nothing
+            const bool odd = unusual_scale(vsa[r][0]) || unusual_scale(vsb[r][0]) || unusual_scale(vsa[r][1]) ||
+                             unusual_scale(vsb[r][1]);
+            wide |= (bool)__any_sync(0xffffffffu, odd);
+            int mx = max(max(largest_scale(vsa[r][0]), largest_scale(vsb[r][0])),
+                         max(largest_scale(vsa[r][1]), largest_scale(vsb[r][1])));
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            if (wide && mx > A.E + 60) {  // sums of values this large would overflow in the present unit
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int b = 0; b < NB; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) A.o[nt][b][c >> 2][c & 3] = mul_pow2(A.o[nt][b][c >> 2][c & 3], A.E - mx);
-                A.E = mx;
-              }
-              // a NaN value block makes its token NaN
-              const float nan = __uint_as_float(0x7FC00000u);
-              const bool n0 = has_nan_byte(vs0, NB), n1 = has_nan_byte(vs1, NB);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if (n0) sc[nt][0] = sc[nt][1] = nan;
-                if (n1) sc[nt][2] = sc[nt][3] = nan;
-              }
+                  for (int c = 0; c < 8; ++c) A.o[nt][b][c >> 2][c & 3] = mul_pow2(A.o[nt][b][c >> 2][c & 3], A.E - mx);
+              A.E = mx;
             }
           }
-          // ---------------------------------------------------- masks
-          if (j0 + 16 > hi_min || j0 < lo_max) {
+        }
+        // ---------------------------------------------------- masks
+        if (j0 + 16 * NG > hi_min || j0 < lo_max || (~here >> (i & 31)) & ((1u << NG) - 1u)) {
+#pragma unroll
+          for (int r = 0; r < NG; ++r) {
+            const bool gone = !((here >> ((i + r) & 31)) & 1u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const int j = j0 + g + (c >> 1) * 8;
-                if (j >= hi[nt][c & 1] || j < lo[nt][c & 1]) sc[nt][c] = -INFINITY;
+                const int j = j0 + 16 * r + g + (c >> 1) * 8;
+                if (j >= hi[nt][c & 1] || j < lo[nt][c & 1] || gone) sc[r][nt][c] = -INFINITY;
               }
           }
-          // ---------------------------------------------------- running maximum and sum
-          float mn[NT][2];
-          bool grow = false;
+        }
+        // ---------------------------------------------------- running maximum and sum
+        float mn[NT][2];
+        bool grow = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v = fmaxf(sc[0][nt][c], sc[0][nt][c + 2]);
+#pragma unroll
+            for (int r = 1; r < NG; ++r) v = fmaxf(v, fmaxf(sc[r][nt][c], sc[r][nt][c + 2]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            mn[nt][c] = v;
+            // the reference follows the maximum only where a weight would pass 2^8
+            grow |= v > limit[nt][c];
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float al[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float v = fmaxf(sc[nt][c], sc[nt][c + 2]);
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-              mn[nt][c] = fmaxf(A.m[nt][c], v);
-              grow |= mn[nt][c] > A.m[nt][c];
+              const float m1 = fmaxf(A.m[nt][c], mn[nt][c]), mf1 = m1 == -INFINITY ? 0.f : m1 * f[nt][c];
+              al[c] = A.m[nt][c] == -INFINITY ? 0.f : ex2(A.mf[nt][c] - mf1);
+              A.l[nt][c] *= al[c];
+              A.m[nt][c] = m1;
+              A.mf[nt][c] = mf1;
+              limit[nt][c] = m1 == -INFINITY ? m1 : m1 + margin[nt][c];
             }
-          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float al[2];
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                al[c] = mn[nt][c] == -INFINITY ? 1.f : ex2(A.m[nt][c] - mn[nt][c]);
-                A.l[nt][c] *= al[c];
-                A.m[nt][c] = mn[nt][c];
-              }
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) A.o[nt][b][c >> 2][c & 3] *= al[c & 1];
-            }
+              for (int c = 0; c < 8; ++c) A.o[nt][b][c >> 2][c & 3] *= al[c & 1];
           }
-          uint32_t pk[NT][2][2];  // [token g / g + 8][upper 8 bits / the rest]
-          float pw[NT][4];
+        }
+        uint32_t pt[NG][NT][2][2];  // transposed: [tokens 2t, 2t+1 / plus 8][upper 8 bits / the rest], row g
+#pragma unroll
+        for (int r = 0; r < NG; ++r)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const float m0 = A.m[nt][c & 1];
-              // (a row that has seen nothing yet keeps weight 0)
-              pw[nt][c] = ex2(sc[nt][c] - (m0 == -INFINITY ? 0.f : m0));
-              A.l[nt][c & 1] += pw[nt][c];
+              sc[r][nt][c] = ex2(fmaf(sc[r][nt][c], f[nt][c & 1], -A.mf[nt][c & 1]));
+              A.l[nt][c & 1] += sc[r][nt][c];
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t u = __float_as_uint(pw[nt][2 * h]), v = __float_as_uint(pw[nt][2 * h + 1]);
-              pk[nt][h][0] = prmt(u, v, 0x7632u);
-              pk[nt][h][1] = f32x2_to_bf16x2(pw[nt][2 * h] - __uint_as_float(u & 0xFFFF0000u),
-                                             pw[nt][2 * h + 1] - __uint_as_float(v & 0xFFFF0000u));
+              const float p0 = sc[r][nt][2 * h], p1 = sc[r][nt][2 * h + 1];
+              const uint32_t u = __float_as_uint(p0), v = __float_as_uint(p1);
+              pt[r][nt][h][0] = movm(prmt(u, v, 0x7632u));
+              pt[r][nt][h][1] =
+                  movm(f32x2_to_bf16x2(p0 - __uint_as_float(u & 0xFFFF0000u), p1 - __uint_as_float(v & 0xFFFF0000u)));
             }
           }
-          // ---------------------------------------------------- weighted sum
-          if (!wide) {
-            uint32_t vw[2][NB];
-            load_words<NB>(rec + 8 * D, lane, vw);
+        // ---------------------------------------------------- weighted sum
+        if (!wide) {
+#pragma unroll
+          for (int r = 0; r < NG; ++r) {
+            uint32_t vw[2][NB], vs[2][NB];  // vs: scales of tokens (2t, 2t+1) as bf16 pairs, per block
+            load_words<NB>(rec[r] + 8 * D, lane, vw);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              e8m0x4_to_bf16x4(prmt(vsa[r][h], vsb[r][h], 0x5140u), vs[h][0], vs[h][1]);
+              if (NB == 4) e8m0x4_to_bf16x4(prmt(vsa[r][h], vsb[r][h], 0x7362u), vs[h][NB - 2], vs[h][NB - 1]);
+            }
 #pragma unroll
             for (int bp = 0; bp < NB / 2; ++bp) {
               // [half][block of the pair][dim]: two tokens, one dimension
@@ -678,40 +826,59 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 #pragma unroll
               for (int bb = 0; bb < 2; ++bb) {
                 const int b = 2 * bp + bb;
-                // 2^(s-127) as bf16, twice in a word
-                const uint32_t sel = 0x0404u | ((uint32_t)b << 4) | ((uint32_t)b << 12);
-                const uint32_t e0 = prmt(vs0, 0u, sel) >> 1, e1 = prmt(vs1, 0u, sel) >> 1;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int w = 0; w < 2; ++w) {
-                    const uint32_t p0 = movm(bf16mul2(pk[nt][0][w], e0)), p1 = movm(bf16mul2(pk[nt][1][w], e1));
+                    const uint32_t p0 = bf16mul2(pt[r][nt][0][w], vs[0][b]), p1 = bf16mul2(pt[r][nt][1][w], vs[1][b]);
                     mma_bf16_16816(A.o[nt][b][0], xv[0][bb][0], xv[0][bb][1], xv[1][bb][0], xv[1][bb][1], p0, p1);
                     mma_bf16_16816(A.o[nt][b][1], xv[0][bb][2], xv[0][bb][3], xv[1][bb][2], xv[1][bb][3], p0, p1);
                   }
               }
             }
-          } else {
-            // (copies, so that the common path keeps both in registers)
-            Acc<D, NT> B = A;
+          }
+        } else {
+          // (copies, so that the common path keeps both in registers)
+          Acc<D, NT> B = A;
+#pragma unroll
+          for (int r = 0; r < NG; ++r) {
+            const bool gone = !((here >> ((i + r) & 31)) & 1u);
             float w[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) w[nt][c] = pw[nt][c];
-            add_group_f32<D, NT>(B, rec, lane, w, valid);
-            A = B;
+              for (int c = 0; c < 4; ++c) w[nt][c] = sc[r][nt][c];
+            add_group_f32<D, NT>(B, rec[r], lane, w, gone ? 0 : q.n - (j0 + 16 * r));
           }
+          A = B;
         }
-        // the stage is free: the record S units on
+      };
+
+      for (int k = 0; k < len;) {
+        // both records of a step lie in one batch of 32 addresses
+        const int ng = C::kStep == 2 && k + 2 <= len && (i & 31) != 31 ? 2 : 1;
+        {
+          const uint32_t s0 = (uint32_t)i % S, p0 = ((uint32_t)i / S) & 1u;
+          const uint32_t s1 = (uint32_t)(i + ng - 1) % S, p1 = ((uint32_t)(i + ng - 1) / S) & 1u;
+          if (!mbar_try_wait2(&bar[s0], p0, &bar[s1], p1))
+            alive = mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs);
+          if (!alive) break;
+        }
+        if (C::kStep == 2 && ng == 2) step(std::integral_constant<int, C::kStep>{}, k);
+        else step(std::integral_constant<int, 1>{}, k);
+        // the stages are free: the records S units on
         __syncwarp();
-        if (i + S < n_units) issue(i + S, cur, nxt, i >> 5);
-        if ((i & 31) == 31) {
+        issue(i + S, ng, i >> 5);
+        i += ng;
+        k += ng;
+        if ((i & 31) == 0) {
           cur = nxt;
-          nxt = i + 33 < n_units ? addresses(i + 33) : nullptr;
+          here = __ballot_sync(0xffffffffu, cur != nullptr);
+          nxt = i + 32 < n_units ? addresses(i + 32) : nullptr;
         }
       }
-      co += len;
+      cg = 0;  // the run goes on with the next item
+      ++citem;
       // ------------------------------------------------------------ the item, or a piece of it
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -723,6 +890,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           l += __shfl_xor_sync(0xffffffffu, l, 16);
           A.l[nt][c] = l;
         }
+      // from here on m is in units of log2
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (A.m[nt][c] != -INFINITY) A.m[nt][c] = A.mf[nt][c];
       if (g0 == 0 && len == q.ng) {
         const int rows = q.ql * p.G;
 #pragma unroll
@@ -764,82 +937,87 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
               dst[COLS * (D + 4) + COLS + col] = A.l[nt][c];
             }
           }
-        if (lane == 0) ph[warp][last ? 1 : 0] = PartHead{item, q.ng, cr, pair, 0, A.E, 0};
+        if (lane == 0)
+          ph[2 * warp + (last ? 1 : 0)] =
+              PartHead{item, q.ng, q.qb, q.ql * p.G, kvh * p.G, rt * COLS, 0,
+                       cta_of(ccost + (long long)(citem - 1) * (q.ng + kItemCost) + kItemCost + q.ng - 1), A.E};
       }
     }
     if (!alive) {
       // a copy did not arrive in time: wait (bounded) for those in flight, leave no piece
       for (int k = i; k < min(i + S, n_units); ++k) mbar_wait(&bar[k % S], (k / S) & 1, a.status, kKvWaitNs);
       __syncwarp();
-      if (lane == 0) ph[warp][0].units = ph[warp][1].units = 0;
+      if (lane == 0) ph[2 * warp].units = ph[2 * warp + 1].units = 0;
     }
   }
   __syncthreads();
 
   // ---------------------------------------------------------------- pieces of one CTA
-  for (int k = 0; k < 2 * W;) {
-    if (ph[k >> 1][k & 1].units == 0) {
-      ++k;
-      continue;
-    }
-    const PartHead h = ph[k >> 1][k & 1];
-    int e = k + 1;
-    while (e < 2 * W && (ph[e >> 1][e & 1].units == 0 || ph[e >> 1][e & 1].item == h.item)) ++e;
-    auto piece = [&](int x) {
-      return reinterpret_cast<const float*>(x & 1 ? smem + (x >> 1) * C::kRingBytes
-                                                  : smem + W * C::kRingBytes + (x >> 1) * C::kStash);
-    };
-    const bool whole = h.item >= cta_lo && h.item + h.units <= cta_hi;
+  // Lane x of every warp looks at piece x (in order of the units): consecutive
+  // pieces of one item form a run; a warp takes one row of one run at a time.
+  static_assert(2 * W <= 32, "one piece per lane");
+  const bool has = lane < 2 * W && ph[min(lane, 2 * W - 1)].units > 0;
+  const long long id = has ? ph[lane].item : -1;
+  const uint32_t pieces = __ballot_sync(0xffffffffu, has);
+  const uint32_t below = pieces & ((1u << lane) - 1u);
+  const long long prev = __shfl_sync(0xffffffffu, id, below ? 31 - __clz(below) : lane);
+  const uint32_t heads = __ballot_sync(0xffffffffu, has && (!below || prev != id));  // first piece of each run
+  auto floats = [&](int x) {
+    return reinterpret_cast<const float*>(x & 1 ? smem + (x >> 1) * C::kRingBytes
+                                                : smem + W * C::kRingBytes + (x >> 1) * C::kStash);
+  };
+  const int n_tasks = __popc(heads) * COLS;
+  for (int task = warp; task < n_tasks; task += W) {
+    const int col = task % COLS;
+    uint32_t at = heads;  // the run's first piece: bit number task / COLS
+    for (int x = task / COLS; x; --x) at &= at - 1;
+    const int k = __ffs(at) - 1;
+    const uint32_t above = heads & ~((2u << k) - 1u);
+    const uint32_t run = pieces & (above ? ((1u << (__ffs(above) - 1)) - 1u) : 0xFFFFFFFFu) & ~((1u << k) - 1u);
+    const PartHead h = ph[k];
+    const int c = h.col0 + col;
+    if (c >= h.rows) continue;
+    float m = -INFINITY;
     int E = 0;
-    for (int x = k; x < e; ++x)
-      if (ph[x >> 1][x & 1].units) E = max(E, ph[x >> 1][x & 1].E);
-    const int slot = h.item <= cta_lo ? 0 : 1;
-    float* part = p.parts + (2ll * blockIdx.x + slot) * part_floats(COLS, D);
-    const Req q = request<COLS>(p, h.r);
-    const int kvh = h.pair / q.rt, rt = h.pair - kvh * q.rt;
-    for (int y = tid; y < COLS * (D / 4); y += C::kThreads) {
-      const int col = y / (D / 4), d = (y % (D / 4)) * 4;
-      float m = -INFINITY, l = 0.f;
-      for (int x = k; x < e; ++x)
-        if (ph[x >> 1][x & 1].units) m = fmaxf(m, piece(x)[COLS * (D + 4) + col]);
-      const float mb = m == -INFINITY ? 0.f : m;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = k; x < e; ++x) {
-        const PartHead& hx = ph[x >> 1][x & 1];
-        if (!hx.units) continue;
-        const float* pc = piece(x);
-        const float w = ex2(pc[COLS * (D + 4) + col] - mb);
-        l += pc[COLS * (D + 4) + COLS + col] * w;
-        const float4 v = *reinterpret_cast<const float4*>(pc + col * (D + 4) + d);
-        const int de = hx.E - E;
-        o.x += mul_pow2(v.x * w, de);
-        o.y += mul_pow2(v.y * w, de);
-        o.z += mul_pow2(v.z * w, de);
-        o.w += mul_pow2(v.w * w, de);
-      }
-      if (whole) {
-        const int c = rt * COLS + col;
-        if (c < q.ql * p.G) {
-          const int row = c / p.G, hq = kvh * p.G + c - row * p.G;
-          const size_t at = (size_t)(q.qb + row) * a.Hq + hq;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          *reinterpret_cast<uint2*>(a.out + at * D + d) =
-              make_uint2(f32x2_to_bf16x2(mul_pow2(o.x * inv, E - 127), mul_pow2(o.y * inv, E - 127)),
-                         f32x2_to_bf16x2(mul_pow2(o.z * inv, E - 127), mul_pow2(o.w * inv, E - 127)));
-          if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f);
-        }
-      } else {
-        *reinterpret_cast<float4*>(part + col * D + d) = o;
-        if (d == 0) {
-          part[COLS * D + col] = m;
-          part[COLS * D + COLS + col] = l;
+    for (uint32_t x = run; x; x &= x - 1) {
+      const int y = __ffs(x) - 1;
+      m = fmaxf(m, floats(y)[COLS * (D + 4) + col]);
+      E = max(E, ph[y].E);
+    }
+    const float mb = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float o[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) o[d] = 0.f;
+    for (uint32_t x = run; x; x &= x - 1) {
+      const int y = __ffs(x) - 1;
+      const float* pc = floats(y);
+      const float w = ex2(pc[COLS * (D + 4) + col] - mb);
+      l += pc[COLS * (D + 4) + COLS + col] * w;
+      const int de = ph[y].E - E;
+      float v[D / 32];
+      load_vec<D / 32>(pc + col * (D + 4) + (D / 32) * lane, v);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] += de == 0 ? v[d] * w : mul_pow2(v[d] * w, de);
+    }
+    const bool whole = h.item >= cta_lo && h.item + h.units <= cta_hi;
+    if (whole) {
+      store_row<D>(a, h, c, p.G, o, l, m, E, lane);
+    } else {
+      const int slot = h.item <= cta_lo ? 0 : 1;
+      float* part = p.parts + (2ll * blockIdx.x + slot) * part_floats(COLS, D);
+      store_vec<D / 32>(part + col * D + (D / 32) * lane, o);
+      if (lane == 0) {
+        part[COLS * D + col] = m;
+        part[COLS * D + COLS + col] = l;
+        if (col == 0) {
+          PartHead hh = h;
+          hh.starts = h.item >= cta_lo && h.item + h.units > cta_hi ? 1 : 0;
+          hh.E = E;
+          p.heads[2 * blockIdx.x + slot] = hh;
         }
       }
     }
-    if (!whole && tid == 0)
-      p.heads[2 * blockIdx.x + slot] =
-          PartHead{h.item, h.units, h.r, h.pair, h.item >= cta_lo && h.item + h.units > cta_hi ? 1 : 0, E, 0};
-    k = e;
   }
 }
 
@@ -849,74 +1027,59 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 template <int D, int NT>
 __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
   using C = StreamCfg<D, NT>;
-  constexpr int COLS = C::kCols, W = C::kWarps, L = D / 4;  // L lanes of 4 dims
-  constexpr int kTeams = 128 / L;
-  __shared__ float4 so[kTeams][L];
-  __shared__ float sl[kTeams];
-  const KvAttnArgs& a = p.a;
+  constexpr int COLS = C::kCols;
   grid_dep_wait();
-  const long long U = p.plan[0], A_w = p.plan[1];
   const int c0 = blockIdx.x, col = blockIdx.y;
   PartHead h = p.heads[2 * c0];
+  const PartHead h1 = p.heads[2 * c0 + 1];
   int slot0 = 0;
   if (h.units == 0 || !h.starts) {
-    h = p.heads[2 * c0 + 1];
+    h = h1;
     slot0 = 1;
   }
   if (h.units == 0 || !h.starts) return;
-  const Req q = request<COLS>(p, h.r);
-  const int kvh = h.pair / q.rt, rt = h.pair - kvh * q.rt;
-  const int cc = rt * COLS + col;
-  if (cc >= q.ql * p.G) return;
-  // last CTA: owner of the item's last unit
-  const long long u = h.item + h.units - 1;
-  const int c1 = (int)((((u + 1) * A_w - 1) / U) / W);
-  auto head_of = [&](int c) { return p.heads[2 * c + (c == c0 ? slot0 : 0)]; };
-  auto part_of = [&](int c) { return p.parts + (2ll * c + (c == c0 ? slot0 : 0)) * part_floats(COLS, D); };
+  const int cc = h.col0 + col;
+  if (cc >= h.rows) return;
+  const int c1 = h.last_cta;
+  auto slot_of = [&](int c) { return 2ll * c + (c == c0 ? slot0 : 0); };
   const int lane = threadIdx.x & 31;
   float m = -INFINITY;
   int E = 0;
   for (int c = c0 + lane; c <= c1; c += 32) {
-    m = fmaxf(m, part_of(c)[COLS * D + col]);
-    E = max(E, head_of(c).E);
+    m = fmaxf(m, p.parts[slot_of(c) * part_floats(COLS, D) + COLS * D + col]);
+    E = max(E, p.heads[slot_of(c)].E);
   }
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   E = __reduce_max_sync(0xffffffffu, E);
   const float mb = m == -INFINITY ? 0.f : m;
-  const int team = threadIdx.x / L, x = threadIdx.x % L;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kTeams = 4, N = D / 32;  // a warp takes every fourth part
+  const int team = threadIdx.x >> 5;
+  float l = 0.f, o[N];
+#pragma unroll
+  for (int d = 0; d < N; ++d) o[d] = 0.f;
 #pragma unroll 4
   for (int c = c0 + team; c <= c1; c += kTeams) {
-    const float* pc = part_of(c);
+    const float* pc = p.parts + slot_of(c) * part_floats(COLS, D);
     const float w = ex2(pc[COLS * D + col] - mb);
     l += pc[COLS * D + COLS + col] * w;
-    const float4 v = *reinterpret_cast<const float4*>(pc + col * D + 4 * x);
-    const int de = head_of(c).E - E;
-    o.x += mul_pow2(v.x * w, de);
-    o.y += mul_pow2(v.y * w, de);
-    o.z += mul_pow2(v.z * w, de);
-    o.w += mul_pow2(v.w * w, de);
+    const int de = p.heads[slot_of(c)].E - E;
+    float v[N];
+    load_vec<N>(pc + col * D + N * lane, v);
+#pragma unroll
+    for (int d = 0; d < N; ++d) o[d] += mul_pow2(v[d] * w, de);
   }
-  so[team][x] = o;
-  if (x == 0) sl[team] = l;
+  __shared__ float so[kTeams][D], sl[kTeams];
+#pragma unroll
+  for (int d = 0; d < N; ++d) so[team][N * lane + d] = o[d];
+  if (lane == 0) sl[team] = l;
   __syncthreads();
   if (team == 0) {
     for (int k = 1; k < kTeams; ++k) {
-      const float4 v = so[k][x];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
+#pragma unroll
+      for (int d = 0; d < N; ++d) o[d] += so[k][N * lane + d];
       l += sl[k];
     }
-    const int row = cc / p.G, hq = kvh * p.G + cc - row * p.G;
-    const size_t at = (size_t)(q.qb + row) * a.Hq + hq;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(a.out + at * D + 4 * x) =
-        make_uint2(f32x2_to_bf16x2(mul_pow2(o.x * inv, E - 127), mul_pow2(o.y * inv, E - 127)),
-                   f32x2_to_bf16x2(mul_pow2(o.z * inv, E - 127), mul_pow2(o.w * inv, E - 127)));
-    if (a.lse && x == 0) a.lse[at] = l == 0.f ? -INFINITY : (m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f);
+    store_row<D>(p.a, h, cc, p.G, o, l, m, E, lane);
   }
 }
 
@@ -935,9 +1098,9 @@ constexpr int kMaxStreamCtas = 256;
 
 }  // namespace
 
-// Workspace of the streaming kernels: plan, part headers, parts (sized for 16 rows).
+// Workspace of the streaming kernels: part headers, parts (sized for 16 rows).
 size_t kv_stream_workspace(int D) {
-  return 256 + sizeof(PartHead) * 2 * kMaxStreamCtas + 4 * part_floats(16, D) * 2 * kMaxStreamCtas;
+  return sizeof(PartHead) * 2 * kMaxStreamCtas + 4 * part_floats(16, D) * 2 * kMaxStreamCtas;
 }
 
 cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, int tiles, uint8_t* ws, cudaStream_t s) {
@@ -946,9 +1109,8 @@ cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, int tiles, uint
   p.G = a.Hq / a.cache.heads;
   p.row_limit = row_limit;
   p.max_ctas = a.num_sms < kMaxStreamCtas ? a.num_sms : kMaxStreamCtas;
-  p.plan = reinterpret_cast<long long*>(ws);
-  p.heads = reinterpret_cast<PartHead*>(ws + 256);
-  p.parts = reinterpret_cast<float*>(ws + 256 + sizeof(PartHead) * 2 * kMaxStreamCtas);
+  p.heads = reinterpret_cast<PartHead*>(ws);
+  p.parts = reinterpret_cast<float*>(ws + sizeof(PartHead) * 2 * kMaxStreamCtas);
   if (a.cache.D == 128) return tiles == 1 ? launch_stream<128, 1>(p, s) : launch_stream<128, 2>(p, s);
   return tiles == 1 ? launch_stream<64, 1>(p, s) : launch_stream<64, 2>(p, s);
 }
