@@ -25,8 +25,6 @@
 // run through a private ring of bulk copies (one per record) without any
 // barrier with other warps.  Items cut between warps are merged in shared
 // memory, items cut between CTAs through the workspace by kv_merge_kernel.
-#include <type_traits>
-
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -44,7 +42,7 @@ struct StreamCfg {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kRec = 17 * D;
   static constexpr int kStages = (NT == 1 ? 4 : 8) * (128 / D);  // a power of two, at most 32
-  static constexpr int kStep = NT == 1 ? 2 : 1;                  // records per softmax step
+  static constexpr int kStep = 2;                                // records per softmax step
   static constexpr int kCols = 8 * NT;
   // a piece in shared memory: O [kCols][D + 4] float, m, l [kCols], reference scale E
   static constexpr int kPieceFloats = kCols * (D + 4) + 2 * kCols + 4;
@@ -57,6 +55,8 @@ struct StreamCfg {
 // What an item costs beside its units, in units (measured: about 2 us a piece
 // next to 1.3 us a unit and warp on a busy SM).
 constexpr int kItemCost = 2;
+// Least run of a warp, in units: shorter runs only add pieces to merge.
+constexpr int kMinRun = 2;
 
 // A piece of an item: one warp's (shared memory) or one CTA's (workspace).
 struct PartHead {
@@ -305,6 +305,12 @@ __device__ __noinline__ void add_group_f32(Acc<D, NT>& A, const uint8_t* rec, in
   }
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 template <int N>
 __device__ __forceinline__ void load_vec(const float* p, float (&v)[N]) {
   if (N == 4) {
@@ -351,6 +357,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[W * S];
   __shared__ long long scan_c[W], scan_u[W];
+  __shared__ long long before_c[C::kThreads], before_u[C::kThreads];  // cost and units before each request of a chunk
   __shared__ int n_empty, empties[C::kThreads];
   // where each warp's run starts ([W]: where the last one ends): request, item
   // within it, unit within that; units before it; cost before its request
@@ -427,48 +434,60 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     __syncthreads();
   }
   if (U == 0) return;
-  // equal runs of cost: the first ``rem`` of A warps take one more
+  // equal runs of cost: the first ``rem`` of A_w warps take one more; few
+  // active warps are spread over all CTAs
   const long long cost = T;
-  const int A_w = (int)min((long long)gridDim.x * W, cost);
+  const int A_w = (int)min((long long)gridDim.x * W, (cost + kMinRun - 1) / kMinRun);
+  const int wpc = (A_w + gridDim.x - 1) / gridDim.x;  // active warps of a CTA
   int rem;
   const long long per = divmod(cost, A_w, rem);
   auto begin_of = [&](int w) { return w >= A_w ? cost : w * per + min(w, rem); };
   auto cta_of = [&](long long c) {  // the CTA in whose run cost index c lies
     const long long cut = rem * (per + 1);
     int x;
-    return (int)(c < cut ? divmod(c, (int)(per + 1), x) : rem + divmod(c - cut, (int)per, x)) / W;
+    return (int)(c < cut ? divmod(c, (int)(per + 1), x) : rem + divmod(c - cut, (int)per, x)) / wpc;
   };
-  const int gw0 = blockIdx.x * W;
-  if (begin_of(gw0) >= cost) return;
+  const int gw0 = blockIdx.x * wpc;
+  if (gw0 >= A_w) return;
+  // thread w finds where warp w's run starts (wpc: where the last one ends)
   for (int ch = 0; ch < chunks; ++ch) {
     if (chunks > 1) {
       if (ch == 0) T = U = 0;
       scan(ch);
     }
-    const int it = mine.items(H);
-    const long long c = (long long)it * (mine.ng + kItemCost);
-    if (c > 0 && first_c <= begin_of(gw0 + W) && first_c + c > begin_of(gw0)) {
-      for (int w = 0; w <= W; ++w) {
-        const long long b = begin_of(gw0 + w);
-        // (the end of everything belongs to the request that ends there)
-        if (b >= first_c && (b < first_c + c || (b == cost && first_c + c == cost))) {
-          int x;
-          const int k = (int)divmod(b - first_c, mine.ng + kItemCost, x);
-          at_r[w] = ch * C::kThreads + tid;
-          at_item[w] = k;
-          at_g[w] = max(0, x - kItemCost);
-          at_unit[w] = first_u + (long long)k * mine.ng + max(0, x - kItemCost);
-          at_cost[w] = first_c;
+    before_c[tid] = first_c;
+    before_u[tid] = first_u;
+    __syncthreads();
+    if (tid <= wpc) {
+      const long long b = min(begin_of(gw0 + tid), cost - 1);  // the end counts as after the last unit
+      const int n = min(C::kThreads, a.R - ch * C::kThreads);
+      if (b >= before_c[0] && b < T) {  // (T: the cost up to this chunk's end)
+        int lo = 0, hi = n;  // before_c[lo] <= b, the last such: requests that cost nothing share a value
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (before_c[mid] <= b) lo = mid;
+          else hi = mid;
         }
+        const int r = ch * C::kThreads + lo;
+        const Req q = request<COLS>(p, r);
+        int x;
+        const int k = (int)divmod(b - before_c[lo], q.ng + kItemCost, x);
+        const bool end = begin_of(gw0 + tid) == cost;
+        const int gg = max(0, x - kItemCost) + (end ? 1 : 0);
+        at_r[tid] = r;
+        at_item[tid] = k;
+        at_g[tid] = gg;
+        at_unit[tid] = before_u[lo] + (long long)k * q.ng + gg;
+        at_cost[tid] = before_c[lo];
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  const long long cta_lo = at_unit[0], cta_hi = at_unit[W];
+  const long long cta_lo = at_unit[0], cta_hi = at_unit[wpc];
 
   // ---------------------------------------------------------------- this warp's run
-  const long long u_lo = at_unit[warp];
-  const int n_units = (int)(at_unit[warp + 1] - u_lo);
+  const long long u_lo = at_unit[min(warp, wpc)];
+  const int n_units = warp < wpc ? (int)(at_unit[warp + 1] - u_lo) : 0;
   if (n_units > 0) {
     // record addresses, 32 units at a time, one per lane; null for a page outside the cache
     int br = at_r[warp];
@@ -542,7 +561,6 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       // queries: f16 times a power of two per row; f folds scale and log2 e
       uint32_t qf[NT][NB][4];
       float f[NT][2];
-      int lo[NT][2], hi[NT][2];
       int shift = 0;
       {
         const int rows = q.ql * p.G;
@@ -598,25 +616,22 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             f[nt][k] = __shfl_sync(0xffffffffu, v, 4 * (2 * t + k));
-            const int c = rt * COLS + nt * 8 + 2 * t + k;
-            const int row = c / p.G;
-            const int pos = q.n - q.ql + row;
-            const bool real = c < rows;
-            hi[nt][k] = real && a.causal ? min(q.n, pos + 1) : q.n;
-            lo[nt][k] = real && a.window ? max(0, pos - a.window + 1) : 0;
           }
         }
       }
-      int lo_max = 0, hi_min = q.n;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          lo_max = max(lo_max, lo[nt][k]);
-          hi_min = min(hi_min, hi[nt][k]);
-        }
-      lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-      hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+      // keys [lo, hi) that row c of the request sees (rows past the last: all)
+      auto sees = [&](int c, int& lo, int& hi) {
+        const int pos = q.n - q.ql + c / p.G;
+        const bool real = c < q.ql * p.G;
+        hi = real && a.causal ? min(q.n, pos + 1) : q.n;
+        lo = real && a.window ? max(0, pos - a.window + 1) : 0;
+      };
+      int lo_max = 0, hi_min = q.n;  // over the tile's rows: the last sees the latest first key, the first the fewest
+      {
+        int x;
+        sees(min(rt * COLS + COLS, q.ql * p.G) - 1, lo_max, x);
+        sees(rt * COLS, x, hi_min);
+      }
 
       Acc<D, NT> A;
       A.E = 127;
@@ -631,19 +646,16 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         A.mf[nt][0] = A.mf[nt][1] = 0.f;
       }
 
-      // reference of the maximum, and what a score may exceed it by: 8 in units of log2
-      float margin[NT][2], limit[NT][2];
+      // a score above its limit moves the reference: 8 above it in units of log2
+      float limit[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          margin[nt][c] = 8.f / f[nt][c];
-          limit[nt][c] = -INFINITY;
-        }
+      for (int nt = 0; nt < NT; ++nt) limit[nt][0] = limit[nt][1] = -INFINITY;
 
-      // one softmax step over the records i .. i + NG - 1 (NG a compile-time count)
-      auto step = [&](auto ng_tag, int k) {
-        constexpr int NG = decltype(ng_tag)::value;
+      // one softmax step over the records i .. i + ng - 1 (where ng < NG, the last
+      // one is taken again with nothing visible)
+      auto step = [&](int k, int ng) {
+        constexpr int NG = C::kStep;
+        const uint32_t live = (here >> (i & 31)) & ((1u << ng) - 1u);  // bit r: record r exists
         float sc[NG][NT][4];
         uint32_t vsa[NG][2], vsb[NG][2];  // value scales of tokens 2t, 2t+1 (a, b), plus 8
         const uint8_t* rec[NG];
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int coff = 16 * D + (lane >> 4) * (D / 2);
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
-          rec[r] = ring + ((uint32_t)(i + r) % S) * REC;
+          rec[r] = ring + ((uint32_t)(i + min(r, ng - 1)) % S) * REC;
           const int valid = q.n - (j0 + 16 * r);  // tokens of the record that exist (above 16: all)
           // -------------------------------------------------- scores
 #pragma unroll
@@ -664,7 +676,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t, vsa[r][0], vsb[r][0]);
           scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t + 8, vsa[r][1], vsb[r][1]);
           uint32_t look = scale_word<NB>(rec[r] + coff, ct);
-          const bool gone = !((here >> ((i + r) & 31)) & 1u);  // no record: a page outside the cache
+          const bool gone = !((live >> r) & 1u);  // no record: a page outside the cache
           if (valid < 16 || gone) {  // what lies past the end is not looked at
             const int v = gone ? 0 : valid;
             if (g >= v) ks0 = 0x7F7F7F7Fu;
@@ -706,7 +718,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         if (__any_sync(0xffffffffu, ok != 0x80808080u) || wide) {
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
-            const bool gone = !((here >> ((i + r) & 31)) & 1u);
+            const bool gone = !((live >> r) & 1u);
             const int v = gone ? 0 : q.n - (j0 + 16 * r);
             // NaN blocks of keys or values make their token NaN
             const uint8_t* ks = rec[r] + 16 * D;
@@ -738,18 +750,21 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
         }
         // ---------------------------------------------------- masks
-        if (j0 + 16 * NG > hi_min || j0 < lo_max || (~here >> (i & 31)) & ((1u << NG) - 1u)) {
+        if (j0 + 16 * NG > hi_min || j0 < lo_max || live != (1u << NG) - 1u) {
 #pragma unroll
-          for (int r = 0; r < NG; ++r) {
-            const bool gone = !((here >> ((i + r) & 31)) & 1u);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < 2; ++c) {
+              int lo, hi;
+              sees(rt * COLS + nt * 8 + 2 * t + c, lo, hi);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int j = j0 + 16 * r + g + (c >> 1) * 8;
-                if (j >= hi[nt][c & 1] || j < lo[nt][c & 1] || gone) sc[r][nt][c] = -INFINITY;
-              }
-          }
+              for (int r = 0; r < NG; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int j = j0 + 16 * r + g + 8 * h;
+                  if (j >= hi || j < lo || !((live >> r) & 1u)) sc[r][nt][2 * h + c] = -INFINITY;
+                }
+            }
         }
         // ---------------------------------------------------- running maximum and sum
         float mn[NT][2];
@@ -779,7 +794,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
               A.l[nt][c] *= al[c];
               A.m[nt][c] = m1;
               A.mf[nt][c] = mf1;
-              limit[nt][c] = m1 == -INFINITY ? m1 : m1 + margin[nt][c];
+              limit[nt][c] = m1 == -INFINITY ? m1 : m1 + __fdividef(8.f, f[nt][c]);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -842,7 +857,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           Acc<D, NT> B = A;
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
-            const bool gone = !((here >> ((i + r) & 31)) & 1u);
+            const bool gone = !((live >> r) & 1u);
             float w[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -864,8 +879,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             alive = mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs);
           if (!alive) break;
         }
-        if (C::kStep == 2 && ng == 2) step(std::integral_constant<int, C::kStep>{}, k);
-        else step(std::integral_constant<int, 1>{}, k);
+        step(k, ng);
         // the stages are free: the records S units on
         __syncwarp();
         issue(i + S, ng, i >> 5);
@@ -977,28 +991,26 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     const PartHead h = ph[k];
     const int c = h.col0 + col;
     if (c >= h.rows) continue;
-    float m = -INFINITY;
-    int E = 0;
-    for (uint32_t x = run; x; x &= x - 1) {
-      const int y = __ffs(x) - 1;
-      m = fmaxf(m, floats(y)[COLS * (D + 4) + col]);
-      E = max(E, ph[y].E);
-    }
-    const float mb = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
+    // lane y weighs piece y
+    const bool mine_y = (run >> lane) & 1u;
+    const float my = mine_y ? floats(lane)[COLS * (D + 4) + col] : -INFINITY;
+    const float m = warp_max(my);
+    const int E = __reduce_max_sync(0xffffffffu, mine_y ? ph[min(lane, 2 * W - 1)].E : 0);
+    const float w = mine_y ? ex2(my - (m == -INFINITY ? 0.f : m)) : 0.f;
+    float l = mine_y ? w * floats(lane)[COLS * (D + 4) + COLS + col] : 0.f;
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     float o[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) o[d] = 0.f;
-    for (uint32_t x = run; x; x &= x - 1) {
-      const int y = __ffs(x) - 1;
-      const float* pc = floats(y);
-      const float w = ex2(pc[COLS * (D + 4) + col] - mb);
-      l += pc[COLS * (D + 4) + COLS + col] * w;
+#pragma unroll 4
+    for (int y = k; y < 2 * W; ++y) {
+      if (!((run >> y) & 1u)) continue;
+      const float wy = __shfl_sync(0xffffffffu, w, y);
       const int de = ph[y].E - E;
       float v[D / 32];
-      load_vec<D / 32>(pc + col * (D + 4) + (D / 32) * lane, v);
+      load_vec<D / 32>(floats(y) + col * (D + 4) + (D / 32) * lane, v);
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] += de == 0 ? v[d] * w : mul_pow2(v[d] * w, de);
+      for (int d = 0; d < D / 32; ++d) o[d] += de == 0 ? v[d] * wy : mul_pow2(v[d] * wy, de);
     }
     const bool whole = h.item >= cta_lo && h.item + h.units <= cta_hi;
     if (whole) {
@@ -1049,7 +1061,7 @@ __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
     m = fmaxf(m, p.parts[slot_of(c) * part_floats(COLS, D) + COLS * D + col]);
     E = max(E, p.heads[slot_of(c)].E);
   }
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_max(m);
   E = __reduce_max_sync(0xffffffffu, E);
   const float mb = m == -INFINITY ? 0.f : m;
   constexpr int kTeams = 4, N = D / 32;  // a warp takes every fourth part
