@@ -311,43 +311,21 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-template <int N>
-__device__ __forceinline__ void load_vec(const float* p, float (&v)[N]) {
-  if (N == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    v[0] = x.x;
-    v[1] = x.y;
-    v[N - 2] = x.z;
-    v[N - 1] = x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(p);
-    v[0] = x.x;
-    v[1] = x.y;
+// Dims d .. d + 3 of output row ``row`` (token x query head): O (units of 2^(E - 127)) over the sum of weights.
+template <int D>
+__device__ __forceinline__ void store4(const KvAttnArgs& a, size_t row, int d, const float4& o, float l, int E) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  if (E != 127) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = mul_pow2(v[k], E - 127);
   }
-}
-template <int N>
-__device__ __forceinline__ void store_vec(float* p, const float (&v)[N]) {
-  if (N == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[N - 2], v[N - 1]);
-  else *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+  *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
 }
 
-// One finished row (row ``c`` of its request's rows x heads): lane holds dims
-// (D / 32) lane .. of O (units of 2^(E - 127)); l the sum of weights, m their
-// reference in units of log2.
-template <int D>
-__device__ __forceinline__ void store_row(const KvAttnArgs& a, const PartHead& h, int c, int G, const float (&o)[D / 32],
-                                          float l, float m, int E, int lane) {
-  const int row = c / G;
-  const size_t at = (size_t)(h.qb + row) * a.Hq + h.hq0 + c - row * G;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t w[D / 64];
-#pragma unroll
-  for (int d = 0; d < D / 64; ++d)
-    w[d] = f32x2_to_bf16x2(mul_pow2(o[2 * d] * inv, E - 127), mul_pow2(o[2 * d + 1] * inv, E - 127));
-  uint16_t* dst = a.out + at * D + (D / 32) * lane;
-  if (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[D / 64 - 1]);
-  else *reinterpret_cast<uint32_t*>(dst) = w[0];
-  if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f;
+// lse from the sum of weights and their reference m (units of log2).
+__device__ __forceinline__ void store_lse(const KvAttnArgs& a, size_t row, float l, float m) {
+  if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f;
 }
 
 template <int D, int NT>
@@ -920,16 +898,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             if (col < rows) {
               const int row = col / p.G, hq = kvh * p.G + col - row * p.G;
               const size_t at = (size_t)(q.qb + row) * a.Hq + hq;
-              const float l = A.l[nt][c], inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                float v[4];
-#pragma unroll
-                for (int d = 0; d < 4; ++d) v[d] = mul_pow2(A.o[nt][b][d >> 1][(d & 1) * 2 + c] * inv, A.E - 127);
-                *reinterpret_cast<uint2*>(a.out + at * D + 32 * b + 4 * g) =
-                    make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
-              }
-              if (a.lse && g == 0) a.lse[at] = l == 0.f ? -INFINITY : (A.m[nt][c] == -INFINITY ? l : (A.m[nt][c] + lg2(l)) * 0.6931471805599453f);
+              for (int b = 0; b < NB; ++b)
+                store4<D>(a, at, 32 * b + 4 * g,
+                          make_float4(A.o[nt][b][0][c], A.o[nt][b][0][2 + c], A.o[nt][b][1][c], A.o[nt][b][1][2 + c]),
+                          A.l[nt][c], A.E);
+              if (g == 0) store_lse(a, at, A.l[nt][c], A.m[nt][c]);
             }
           }
       } else {
@@ -968,7 +942,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 
   // ---------------------------------------------------------------- pieces of one CTA
   // Lane x of every warp looks at piece x (in order of the units): consecutive
-  // pieces of one item form a run; a warp takes one row of one run at a time.
+  // pieces of one item form a run; a warp takes four rows of one run at a time,
+  // eight lanes a row.
   static_assert(2 * W <= 32, "one piece per lane");
   const bool has = lane < 2 * W && ph[min(lane, 2 * W - 1)].units > 0;
   const long long id = has ? ph[lane].item : -1;
@@ -980,46 +955,59 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     return reinterpret_cast<const float*>(x & 1 ? smem + (x >> 1) * C::kRingBytes
                                                 : smem + W * C::kRingBytes + (x >> 1) * C::kStash);
   };
-  const int n_tasks = __popc(heads) * COLS;
+  constexpr int N = D / 32;  // 16-byte words of a row per lane: word x + 8 d
+  const int n_tasks = __popc(heads) * (COLS / 4);
   for (int task = warp; task < n_tasks; task += W) {
-    const int col = task % COLS;
-    uint32_t at = heads;  // the run's first piece: bit number task / COLS
-    for (int x = task / COLS; x; --x) at &= at - 1;
+    const int col = task % (COLS / 4) * 4 + (lane >> 3), x8 = lane & 7;
+    uint32_t at = heads;  // the run's first piece: bit number task / (COLS / 4)
+    for (int x = task / (COLS / 4); x; --x) at &= at - 1;
     const int k = __ffs(at) - 1;
     const uint32_t above = heads & ~((2u << k) - 1u);
     const uint32_t run = pieces & (above ? ((1u << (__ffs(above) - 1)) - 1u) : 0xFFFFFFFFu) & ~((1u << k) - 1u);
     const PartHead h = ph[k];
-    const int c = h.col0 + col;
-    if (c >= h.rows) continue;
-    // lane y weighs piece y
-    const bool mine_y = (run >> lane) & 1u;
-    const float my = mine_y ? floats(lane)[COLS * (D + 4) + col] : -INFINITY;
-    const float m = warp_max(my);
-    const int E = __reduce_max_sync(0xffffffffu, mine_y ? ph[min(lane, 2 * W - 1)].E : 0);
-    const float w = mine_y ? ex2(my - (m == -INFINITY ? 0.f : m)) : 0.f;
-    float l = mine_y ? w * floats(lane)[COLS * (D + 4) + COLS + col] : 0.f;
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    float o[D / 32];
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) o[d] = 0.f;
-#pragma unroll 4
-    for (int y = k; y < 2 * W; ++y) {
-      if (!((run >> y) & 1u)) continue;
-      const float wy = __shfl_sync(0xffffffffu, w, y);
-      const int de = ph[y].E - E;
-      float v[D / 32];
-      load_vec<D / 32>(floats(y) + col * (D + 4) + (D / 32) * lane, v);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] += de == 0 ? v[d] * wy : mul_pow2(v[d] * wy, de);
+    float m = -INFINITY;
+    int E = 0;
+    for (uint32_t x = run; x; x &= x - 1) {
+      const int y = __ffs(x) - 1;
+      m = fmaxf(m, floats(y)[COLS * (D + 4) + col]);
+      E = max(E, ph[y].E);
     }
-    const bool whole = h.item >= cta_lo && h.item + h.units <= cta_hi;
-    if (whole) {
-      store_row<D>(a, h, c, p.G, o, l, m, E, lane);
+    const float mb = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o[N];
+#pragma unroll
+    for (int d = 0; d < N; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t x = run; x; x &= x - 1) {
+      const int y = __ffs(x) - 1;
+      const float* pc = floats(y);
+      const float w = ex2(pc[COLS * (D + 4) + col] - mb);
+      l = fmaf(pc[COLS * (D + 4) + COLS + col], w, l);
+      const int de = ph[y].E - E;
+#pragma unroll
+      for (int d = 0; d < N; ++d) {
+        float4 v = *reinterpret_cast<const float4*>(pc + col * (D + 4) + 4 * x8 + 32 * d);
+        if (de != 0) v = make_float4(mul_pow2(v.x, de), mul_pow2(v.y, de), mul_pow2(v.z, de), mul_pow2(v.w, de));
+        o[d].x = fmaf(v.x, w, o[d].x);
+        o[d].y = fmaf(v.y, w, o[d].y);
+        o[d].z = fmaf(v.z, w, o[d].z);
+        o[d].w = fmaf(v.w, w, o[d].w);
+      }
+    }
+    if (h.item >= cta_lo && h.item + h.units <= cta_hi) {  // whole in this CTA
+      const int c = h.col0 + col;
+      if (c < h.rows) {
+        const int row = c / p.G;
+        const size_t dst = (size_t)(h.qb + row) * a.Hq + h.hq0 + c - row * p.G;
+#pragma unroll
+        for (int d = 0; d < N; ++d) store4<D>(a, dst, 4 * x8 + 32 * d, o[d], l, E);
+        if (x8 == 0) store_lse(a, dst, l, m);
+      }
     } else {
       const int slot = h.item <= cta_lo ? 0 : 1;
       float* part = p.parts + (2ll * blockIdx.x + slot) * part_floats(COLS, D);
-      store_vec<D / 32>(part + col * D + (D / 32) * lane, o);
-      if (lane == 0) {
+#pragma unroll
+      for (int d = 0; d < N; ++d) *reinterpret_cast<float4*>(part + col * D + 4 * x8 + 32 * d) = o[d];
+      if (x8 == 0) {
         part[COLS * D + col] = m;
         part[COLS * D + COLS + col] = l;
         if (col == 0) {
@@ -1064,34 +1052,41 @@ __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
   m = warp_max(m);
   E = __reduce_max_sync(0xffffffffu, E);
   const float mb = m == -INFINITY ? 0.f : m;
-  constexpr int kTeams = 4, N = D / 32;  // a warp takes every fourth part
-  const int team = threadIdx.x >> 5;
-  float l = 0.f, o[N];
-#pragma unroll
-  for (int d = 0; d < N; ++d) o[d] = 0.f;
+  constexpr int L = D / 4, kTeams = 128 / L;  // L lanes of 4 dims take every kTeams-th part
+  const int team = threadIdx.x / L, x = threadIdx.x % L;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int c = c0 + team; c <= c1; c += kTeams) {
     const float* pc = p.parts + slot_of(c) * part_floats(COLS, D);
     const float w = ex2(pc[COLS * D + col] - mb);
-    l += pc[COLS * D + COLS + col] * w;
+    l = fmaf(pc[COLS * D + COLS + col], w, l);
+    const float4 v = *reinterpret_cast<const float4*>(pc + col * D + 4 * x);
     const int de = p.heads[slot_of(c)].E - E;
-    float v[N];
-    load_vec<N>(pc + col * D + N * lane, v);
-#pragma unroll
-    for (int d = 0; d < N; ++d) o[d] += mul_pow2(v[d] * w, de);
+    o.x += mul_pow2(v.x * w, de);
+    o.y += mul_pow2(v.y * w, de);
+    o.z += mul_pow2(v.z * w, de);
+    o.w += mul_pow2(v.w * w, de);
   }
-  __shared__ float so[kTeams][D], sl[kTeams];
-#pragma unroll
-  for (int d = 0; d < N; ++d) so[team][N * lane + d] = o[d];
-  if (lane == 0) sl[team] = l;
+  __shared__ float4 so[kTeams][L];
+  __shared__ float sl[kTeams];
+  so[team][x] = o;
+  if (x == 0) sl[team] = l;
   __syncthreads();
   if (team == 0) {
-    for (int k = 1; k < kTeams; ++k) {
 #pragma unroll
-      for (int d = 0; d < N; ++d) o[d] += so[k][N * lane + d];
+    for (int k = 1; k < kTeams; ++k) {
+      const float4 v = so[k][x];
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
       l += sl[k];
     }
-    store_row<D>(p.a, h, cc, p.G, o, l, m, E, lane);
+    const int row = cc / p.G;
+    const size_t dst = (size_t)(h.qb + row) * p.a.Hq + h.hq0 + cc - row * p.G;
+    store4<D>(p.a, dst, 4 * x, o, l, E);
+    if (x == 0) store_lse(p.a, dst, l, m);
   }
 }
 
