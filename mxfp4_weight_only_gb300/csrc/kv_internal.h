@@ -50,10 +50,26 @@ struct KvAttnArgs {
   uint32_t* status;
   int num_sms;
 };
+// Which kernel takes a request: the streaming one those of at most ``row_limit``
+// rows (query rows x heads per kv head), and those whose rows see at most
+// kFewKeys keys, where a row's result may hang on weights of very unlike size:
+// it holds them to 16 bits at any size, the tensor-core kernel to 11 bits above
+// 2^-25 of the row's largest.
+constexpr int kFewKeys = 256;
+__host__ __device__ inline bool kv_streamed(long long rows, int keys, int window, int row_limit) {
+  return rows <= row_limit || keys <= kFewKeys || (window > 0 && window <= kFewKeys);
+}
+
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
-// per kv head), row tiles of 8 * tiles rows (tiles 1 or 2).
+// per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows
+// (tiles 1 or 2).
 size_t kv_stream_workspace(int D);
-cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, int tiles, uint8_t* ws, cudaStream_t s);
+cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, const int32_t* odd, int tiles, uint8_t* ws,
+                             cudaStream_t s);
+
+// Tensor-core kernel: requests of more than ``row_limit`` rows; marks in odd [R]
+// those whose scales it cannot hold, for launch_kv_stream to do over.
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, cudaStream_t s);
 
 size_t kv_attention_workspace(const KvView& c, const kv_mxfp4_attn_t* a);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t s);

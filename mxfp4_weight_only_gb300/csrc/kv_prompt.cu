@@ -1,0 +1,691 @@
+// Attention over the 4-bit KV cache, many query rows per request (prompts):
+// tcgen05 MMAs, tensor-bound (kv_mxfp4_attention).
+//
+// One CTA takes up to 256 rows (query tokens x heads of one kv head, in two
+// tiles of 128) of one request and walks over the keys they can see, 128 at a
+// time:
+//   S = Q K^T          tcgen05 f16, accumulator 128 columns of tensor memory
+//   p = 2^(S f - m)    f: scale, log2 e and the row's power of two; m follows the
+//                      row's maximum only where p would pass 2^4, so the sum
+//                      below is rarely rescaled
+//   O += P V           tcgen05 f16, P from tensor memory (over S's columns)
+// Four converter warps expand each 128-key tile of the cache once for both
+// query tiles: E2M1 codes to f16 (one conversion per two values) times the
+// block's 2^(s-127), exact for scale bytes 104 .. 140 (and 0, blocks below
+// 2^-124, as zeros); K rows and V rows go to shared memory as they are, K as the
+// K-major and V as the MN-major operand, both with the 128-byte swizzle.  A
+// request with any other scale byte (NaN among them) is marked and left to the
+// streaming kernel, which runs next.  Queries enter as f16 times a power of two
+// per row (exact: 8 significant bits), weights as f16 of p 2^11 (11 bits down to
+// p = 2^-25 of the reference).
+// While one tile's softmax runs, the tensor core works on the other tile:
+// PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...
+#include "common.cuh"
+#include "kv_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 4;
+constexpr int kPromptThreads = 32 * (kSoftWarps + 1 + kConvWarps);
+constexpr int kKeys = 128;         // keys of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 4.f;      // a weight may reach 2^kSlack before its row's reference moves
+constexpr float kWeightExp = 11.f; // weights are held times 2^11: at most 2^15 in f16
+
+template <int D>
+struct PromptCfg {
+  static constexpr int kQBytes = 128 * D * 2;            // one query tile
+  static constexpr int kTile = kKeys * D * 2;            // one K or V tile
+  static constexpr int kStages = 2;
+  static constexpr int kKOff = 2 * kQBytes, kVOff = kKOff + kStages * kTile;
+  static constexpr int kBarOff = kVOff + kStages * kTile;
+  static constexpr int kSmem = 1024 + kBarOff + 256;
+  // tensor memory: S (and P) of both tiles, O of both tiles
+  static constexpr uint32_t kSCol = 0, kOCol = 256, kCols = 512;
+};
+
+struct PromptParams {
+  KvAttnArgs a;
+  int G, row_limit;
+  int32_t* odd;  // [R] set for requests with scales outside the exact range
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+__device__ __forceinline__ void tc_alloc(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// Matrix descriptor, 128-byte swizzle.  K-major (rows of 64 values of K): groups
+// of 8 rows 1024 bytes apart.  MN-major (rows of 64 values of MN, one per K):
+// groups of 8 K 1024 bytes apart (stride), next 64 of MN ``lead`` bytes on.
+__device__ __forceinline__ uint64_t sw128(uint32_t saddr, uint32_t lead) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, f16 operands, f32 accumulator, M x N; B MN-major with ``tb``.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool tb) {
+  return (1u << 4) | (tb ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Waits for the loads before it; the registers pass through, so that no use moves above.
+__device__ __forceinline__ void tc_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
+}
+// a * b + c and a + b on two floats at once.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float lg2(float v) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float mul_pow2(float v, int e) {
+  const int c = min(max(e, -252), 252), h = c >> 1;
+  return v * exp2_int(h) * exp2_int(c - h);
+}
+
+// 2^(s-127) twice in f16 for s in 104 .. 140 (below 113 subnormal, still exact), 0 for s = 0.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t s) {
+  const int e = (int)s - 112;  // f16 exponent field
+  uint32_t v = e > 0 ? (uint32_t)e << 10 : 1u << max(e + 9, 0);
+  if (s == 0u) v = 0u;
+  return v | (v << 16);
+}
+__device__ __forceinline__ bool odd_scale(uint32_t s) { return s != 0u && s - 104u > 36u; }
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const PromptParams p) {
+  using C = PromptCfg<D>;
+  constexpr int NB = D / 32, S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* k_full = bars;            // [S] a K tile is in shared memory
+  uint64_t* k_empty = k_full + S;     // [S] its MMAs are done
+  uint64_t* v_full = k_empty + S;     // [S]
+  uint64_t* v_empty = v_full + S;     // [S]
+  uint64_t* q_full = v_empty + S;     // the query tiles are in shared memory
+  uint64_t* s_full = q_full + 1;      // [2] scores of a tile are in tensor memory
+  uint64_t* p_full = s_full + 2;      // [2] weights are, and O is in their unit
+  uint64_t* o_done = p_full + 2;      // [2] the product with V is done
+  uint64_t* drain = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ int item[4];  // request, kv head, first row, units before
+  const KvAttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = a.cache.heads;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], kConvWarps);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], kConvWarps);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(q_full, kSoftWarps);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_done[x], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    item[0] = -1;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tc_alloc(tmem_slot, C::kCols);
+  if (warp == 0) {
+    // this CTA's item: the last row tiles of a request first (they see the most keys), heads innermost
+    __syncwarp();
+    long long before = 0;
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
+      const int r = r0 + lane;
+      long long rows = 0;
+      if (r < a.R) {
+        const int qb = min(max(a.query_start[r], 0), a.N);
+        rows = (long long)max(min(min(max(a.query_start[r + 1], 0), a.N) - qb, a.max_q_len), 0) * p.G;
+      }
+      const bool mine = r < a.R && !kv_streamed(rows, r < a.R ? a.seq_lens[r] : 0, a.window, p.row_limit);
+      const int tiles = mine ? (int)((rows + 255) / 256) : 0;
+      long long incl = (long long)tiles * H;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const long long off = (long long)blockIdx.x - before - (incl - (long long)tiles * H);
+      if (off >= 0 && off < (long long)tiles * H) {
+        const int qt = tiles - 1 - (int)(off / H);
+        item[0] = r;
+        item[1] = (int)(off % H);
+        item[2] = qt * 256;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+      if (before > (long long)blockIdx.x) break;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  const int r = item[0];
+  if (r >= 0) {
+    const int kvh = item[1], row0 = item[2];
+    const int qb = min(max(a.query_start[r], 0), a.N);
+    const int ql = min(min(max(a.query_start[r + 1], 0), a.N) - qb, a.max_q_len);
+    const int rows = min(ql * p.G - row0, 256);  // rows of this CTA
+    const int n = (int)min((long long)max(a.seq_lens[r], 0), (long long)a.max_blocks << a.cache.page_shift);
+    const int first_pos = n - ql + row0 / p.G, last_pos = n - ql + (row0 + rows - 1) / p.G;
+    const int key_hi = a.causal ? min(n, last_pos + 1) : n;
+    const int key_lo = a.window ? max(0, first_pos - a.window + 1) : 0;
+    const int t0 = key_lo / kKeys, nt = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - t0 : 0;
+    const int nq = rows > 128 ? 2 : 1;
+    const int32_t* table = a.table + (size_t)r * a.max_blocks;
+
+    if (warp < kSoftWarps) {
+      // ---------------------------------------------------------------- softmax: thread = row
+      const int x = warp >> 2, quad = warp & 3;
+      const int trow = 32 * quad + lane;           // row of the tile
+      const int row = row0 + 128 * x + trow;       // row of the request
+      const bool real = 128 * x + trow < rows;
+      const int i = row / p.G, hq = kvh * p.G + row - i * p.G;
+      float f = 1.f;
+      {
+        // the row's query, f16 times a power of two that puts its largest magnitude in [8, 16)
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(qb + i) * a.q_stride + (size_t)hq * D);
+        float mx = 0.f;
+        if (real) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = __ldg(src + c);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+          }
+        }
+        const int e = mx > 0.f && mx < INFINITY ? (int)(__float_as_uint(mx) >> 23) - 127 - 3 : 0;
+        f = mul_pow2(fabsf(a.scale) * kLog2e, e);
+        const bool zero = f == 0.f || !real;
+        if (f == 0.f) f = 1.f;
+        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+        uint8_t* dst = smem + x * C::kQBytes + trow * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 o = make_uint4(0u, 0u, 0u, 0u);
+          if (!zero) {
+            const uint4 u = __ldg(src + c);
+            o.x = f32x2_to_f16x2(mul_pow2(bf16_lo(u.x), -e), mul_pow2(bf16_hi(u.x), -e)) ^ sign;
+            o.y = f32x2_to_f16x2(mul_pow2(bf16_lo(u.y), -e), mul_pow2(bf16_hi(u.y), -e)) ^ sign;
+            o.z = f32x2_to_f16x2(mul_pow2(bf16_lo(u.z), -e), mul_pow2(bf16_hi(u.z), -e)) ^ sign;
+            o.w = f32x2_to_f16x2(mul_pow2(bf16_lo(u.w), -e), mul_pow2(bf16_hi(u.w), -e)) ^ sign;
+          }
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (trow & 7)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      }
+      const int pos = n - ql + i;
+      const int hi = a.causal ? min(n, pos + 1) : n;           // keys [lo, hi) are seen
+      const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+      const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + C::kSCol + 128 * x;
+      const uint32_t tO = tmem + ((uint32_t)(32 * quad) << 16) + C::kOCol + 128 * x;
+      float m = -INFINITY, mf = 0.f, l = 0.f;  // reference of the scores, times f; sum of weights (2^11 times)
+      bool ok = true;
+      if (x < nq) {
+        for (int j = 0; j < nt; ++j) {
+          const int j0 = (t0 + j) * kKeys;
+          // records of this tile that exist: bit k for keys 16 k ..
+          bool there = false;
+          if (lane < 8 && j0 + 16 * lane < n) {
+            const int pg = table[(j0 + 16 * lane) >> a.cache.page_shift];
+            there = pg >= 0 && pg < a.cache.num_pages;
+          }
+          const uint32_t have = __ballot_sync(0xffffffffu, there) & 0xFFu;
+          if (*abort_flag || !mbar_wait(&s_full[x], j & 1, a.status, kWaitLimitNs)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_after();
+          // every row of the warp sees every key of the tile?
+          const bool full = __all_sync(0xffffffffu, (lo <= j0 && hi >= j0 + kKeys) || !real) && have == 0xFFu;
+          if (!full) {  // hidden keys: -inf, put back where the score was
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t v[16];
+              tc_ld16(tS + 16 * c, v);
+              tc_ld_wait16(v);
+              const bool gone = !((have >> c) & 1u);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const int key = j0 + 16 * c + k;
+                if (key < lo || key >= hi || gone) v[k] = 0xFF800000u;
+              }
+              tc_st16(tS + 16 * c, v);
+            }
+            tc_st_wait();
+          }
+          float mx = -INFINITY;
+          {
+            uint32_t v[2][32];
+            tc_ld32(tS, v[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t(&u)[32] = v[c & 1];
+              tc_ld_wait32(u);
+              if (c < 3) tc_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
+            }
+          }
+          // the reference follows the maximum where a weight would pass 2^kSlack
+          const bool grow = m == -INFINITY ? mx > -INFINITY : fmaf(mx, f, -mf) > kSlack;
+          if (__any_sync(0xffffffffu, grow)) {
+            float al = 1.f;
+            if (grow) {
+              const float mf1 = mx * f;
+              al = m == -INFINITY ? 0.f : ex2(mf - mf1);
+              m = mx;
+              mf = mf1;
+              l *= al;
+            }
+            if (j > 0) {
+              if (!mbar_wait(&o_done[x], (j - 1) & 1, a.status, kWaitLimitNs)) {
+                *abort_flag = 1;
+                ok = false;
+                break;
+              }
+              tc_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t v[16];
+                tc_ld16(tO + 16 * c, v);
+                tc_ld_wait16(v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
+                tc_st16(tO + 16 * c, v);
+              }
+            }
+          }
+          {
+            const uint64_t f2 = pack2(f, f), off2 = pack2(kWeightExp - mf, kWeightExp - mf);
+            uint64_t sum = pack2(0.f, 0.f);
+            uint32_t v[2][32];
+            tc_ld32(tS, v[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t(&u)[32] = v[c & 1];
+              tc_ld_wait32(u);
+              // (the next scores are read before this step's weights go over earlier ones)
+              if (c < 3) tc_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float x0, x1;
+                unpack2(fma2(pack2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), f2, off2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sum = add2(sum, pack2(p0, p1));
+                w[k] = f32x2_to_f16x2(p0, p1);
+              }
+              tc_st16(tS + 16 * c, w);
+            }
+            float l0, l1;
+            unpack2(sum, l0, l1);
+            l += l0 + l1;
+          }
+          tc_st_wait();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[x]);
+        }
+        if (ok && nt > 0 && !mbar_wait(&o_done[x], (nt - 1) & 1, a.status, kWaitLimitNs)) {
+          *abort_flag = 1;
+          ok = false;
+        }
+        if (ok) {
+          tc_after();
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const size_t at = (size_t)(qb + i) * a.Hq + hq;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            if (nt > 0) {
+              tc_ld32(tO + 32 * c, v);
+              tc_ld_wait();
+            }
+            if (real) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t o[4] = {0u, 0u, 0u, 0u};
+                if (nt > 0 && l != 0.f) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    o[e] = f32x2_to_bf16x2(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
+                }
+                dst[k] = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          }
+          if (real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (mf + lg2(l) - kWeightExp) * 0.6931471805599453f;
+        }
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0 && nt > 0) {
+        const uint32_t sq = smem_u32(smem), sk = sq + C::kKOff, sv = sq + C::kVOff;
+        constexpr uint32_t id_s = idesc(128, kKeys, false), id_o = idesc(128, D, true);
+        auto scores = [&](int x, int s) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
+            mma_ss(tmem + C::kSCol + 128 * x, sw128(sq + x * C::kQBytes + o, 16), sw128(sk + s * C::kTile + o, 16), id_s,
+                   k > 0);
+          }
+          tc_commit(&s_full[x]);
+        };
+        bool ok = mbar_wait(q_full, 0, a.status, kWaitLimitNs) && mbar_wait(&k_full[0], 0, a.status, kWaitLimitNs);
+        tc_after();
+        if (ok) {
+          for (int x = 0; x < nq; ++x) scores(x, 0);
+          tc_commit(&k_empty[0]);
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const int s = j % S, s1 = (j + 1) % S;
+          for (int x = 0; x < nq && ok; ++x) {
+            ok = (x > 0 || mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs)) &&
+                 mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs);
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + C::kOCol + 128 * x, tmem + C::kSCol + 128 * x + 8 * k,
+                     sw128(sv + s * C::kTile + k * 16 * 128, kKeys * 128), id_o, j > 0 || k > 0);
+            tc_commit(&o_done[x]);
+            if (x == nq - 1) tc_commit(&v_empty[s]);
+            if (j + 1 < nt) {
+              ok = x > 0 || mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs);
+              if (!ok) break;
+              tc_after();
+              scores(x, s1);
+              if (x == nq - 1) tc_commit(&k_empty[s1]);
+            }
+          }
+          if (*abort_flag) ok = false;
+        }
+        if (!ok) *abort_flag = 1;
+        // all issued MMAs complete before tensor memory is released
+        tc_commit(drain);
+        mbar_wait(drain, 0, a.status, kWaitLimitNs);
+      }
+    } else {
+      // ---------------------------------------------------------------- converters: two records of a tile per warp
+      const int cw = warp - kMmaWarp - 1;
+      const int g = lane >> 2, t = lane & 3;
+      bool odd = false;
+      bool ok = true;
+      // codes and scales of a tile in registers: lane (g, t) takes, per record, two
+      // tokens' words of K and four tokens' of V; loaded a tile ahead
+      const uint8_t* rec[2];
+      int valid[2];
+      uint32_t kc[2][2][NB], vc[2][2][NB], ks[2][2], vs[2][4];
+      auto locate = [&](int j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = (t0 + j) * kKeys + (2 * cw + h) * 16;
+          rec[h] = nullptr;
+          valid[h] = 0;
+          if (j < nt && key < n) {
+            const int pg = table[key >> a.cache.page_shift];
+            if (pg >= 0 && pg < a.cache.num_pages) {
+              rec[h] = a.cache.data + a.cache.record(pg, kvh, (key & ((1 << a.cache.page_shift) - 1)) >> 4);
+              valid[h] = min(16, n - key);
+            }
+          }
+        }
+      };
+      // the scale bytes of token tok (0: past the end, whose values become zeros)
+      auto scales = [&](int h, int which, int tok) -> uint32_t {
+        if (tok >= valid[h]) return 0u;
+        const uint8_t* q = rec[h] + 16 * D + which * (D / 2) + tok * NB;
+        return NB == 4 ? *reinterpret_cast<const uint32_t*>(q) : (uint32_t) * reinterpret_cast<const uint16_t*>(q);
+      };
+      auto words = [&](const uint8_t* q, uint32_t (&c)[NB]) {
+        if (NB == 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + lane);
+          c[0] = x.x; c[1] = x.y; c[NB - 2] = x.z; c[NB - 1] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(q) + lane);
+          c[0] = x.x; c[1] = x.y;
+        }
+      };
+      auto load_k = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (rec[h]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              words(rec[h] + u * 4 * D, kc[h][u]);
+              ks[h][u] = scales(h, 0, 8 * u + g);
+            }
+          } else {
+            ks[h][0] = ks[h][1] = 0u;
+          }
+      };
+      auto load_v = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (rec[h]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              words(rec[h] + 8 * D + u * 4 * D, vc[h][u]);
+              vs[h][2 * u] = scales(h, 1, 8 * u + 2 * t);
+              vs[h][2 * u + 1] = scales(h, 1, 8 * u + 2 * t + 1);
+            }
+          } else {
+            vs[h][0] = vs[h][1] = vs[h][2] = vs[h][3] = 0u;
+          }
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) kc[h][u][b] = vc[h][u][b] = 0u;
+      locate(0);
+      load_k();
+      load_v();
+      for (int j = 0; j < nt && ok; ++j) {
+        const int s = j % S;
+        locate(j + 1);
+        if (*abort_flag || (j >= S && !mbar_wait(&k_empty[s], ((j / S) - 1) & 1, a.status, kWaitLimitNs))) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int krow = (2 * cw + h) * 16 + 8 * u + g;
+            uint8_t* dst = smem + C::kKOff + s * C::kTile + krow * 128;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const uint32_t sb = (ks[h][u] >> (8 * b)) & 255u, sc = scale_f16x2(sb);
+              odd |= odd_scale(sb);
+              uint32_t y[4];
+              e2m1x8_to_f16x8(kc[h][u][b], y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(dst + (b >> 1) * (128 * 128) + ((((b & 1) * 4 + t) ^ (krow & 7)) << 4)) =
+                  make_uint4(hmul2(y[0], sc), hmul2(y[1], sc), hmul2(y[2], sc), hmul2(y[3], sc));
+            }
+          }
+        load_k();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_full[s]);
+        if (j >= S && !mbar_wait(&v_empty[s], ((j / S) - 1) & 1, a.status, kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {  // token 8 u + 2 t + w: dims 4 g .. of every block
+              const int krow = (2 * cw + h) * 16 + 8 * u + 2 * t + w;
+              uint8_t* dst = smem + C::kVOff + s * C::kTile + krow * 128 + 8 * (g & 1);
+#pragma unroll
+              for (int bp = 0; bp < NB / 2; ++bp) {
+                uint32_t y[4];
+                e2m1x8_to_f16x8(vc[h][u][w * (NB / 2) + bp], y[0], y[1], y[2], y[3]);
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb) {
+                  const uint32_t sb = (vs[h][2 * u + w] >> (8 * (2 * bp + bb))) & 255u, sc = scale_f16x2(sb);
+                  odd |= odd_scale(sb);
+                  *reinterpret_cast<uint2*>(dst + bp * (kKeys * 128) + (((bb * 4 + (g >> 1)) ^ (krow & 7)) << 4)) =
+                      make_uint2(hmul2(y[2 * bb], sc), hmul2(y[2 * bb + 1], sc));
+                }
+              }
+            }
+        load_v();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[s]);
+      }
+      if (!ok) *abort_flag = 1;
+      if (odd) p.odd[r] = 1;
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_after();
+    tc_dealloc(tmem, C::kCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t s) {
+  using C = PromptCfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  kv_prompt_kernel<D><<<grid, kPromptThreads, C::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, cudaStream_t s) {
+  PromptParams p{};
+  p.a = a;
+  p.G = a.Hq / a.cache.heads;
+  p.row_limit = row_limit;
+  p.odd = odd;
+  cudaError_t e = cudaMemsetAsync(odd, 0, sizeof(int32_t) * a.R, s);
+  if (e != cudaSuccess) return e;
+  // at most one tile per 256 rows, and one partial tile per request that has more rows than the limit
+  const long long rows = (long long)a.N * p.G;
+  const long long most = rows / (row_limit + 1) < a.R ? rows / (row_limit + 1) : a.R;
+  const long long grid = (rows / 256 + most) * a.cache.heads;
+  if (grid == 0) return cudaSuccess;
+  return a.cache.D == 128 ? launch_prompt<128>(p, (unsigned)grid, s) : launch_prompt<64>(p, (unsigned)grid, s);
+}
+
+}  // namespace moe

@@ -74,7 +74,8 @@ __host__ __device__ constexpr size_t part_floats(int cols, int D) { return (size
 struct StreamParams {
   KvAttnArgs a;
   int G;           // query heads per kv head
-  int row_limit;   // requests with more rows than this are not this kernel's
+  int row_limit;   // requests with more rows than this are not this kernel's,
+  const int32_t* odd;  // unless marked here ([R], or null: none)
   int max_ctas;
   PartHead* heads;   // [grid][2]
   float* parts;      // [grid][2][part_floats]
@@ -108,7 +109,7 @@ __device__ __forceinline__ Req request(const StreamParams& p, int r) {
   const int full = a.seq_lens[r];
   q.n = (int)min((long long)max(full, 0), cap);
   const long long rows = (long long)max(q.ql, 0) * p.G;
-  const bool mine = rows > 0 && rows <= p.row_limit;
+  const bool mine = rows > 0 && (kv_streamed(rows, full, a.window, p.row_limit) || (p.odd && p.odd[r] != 0));
   q.rt = mine ? (int)((rows + COLS - 1) / COLS) : 0;
   q.glo = a.window ? max(0, q.n - q.ql - a.window + 1) >> 4 : 0;
   q.ng = mine ? ((q.n + 15) >> 4) - q.glo : 0;
@@ -1110,11 +1111,12 @@ size_t kv_stream_workspace(int D) {
   return sizeof(PartHead) * 2 * kMaxStreamCtas + 4 * part_floats(16, D) * 2 * kMaxStreamCtas;
 }
 
-cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, int tiles, uint8_t* ws, cudaStream_t s) {
+cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, const int32_t* odd, int tiles, uint8_t* ws, cudaStream_t s) {
   StreamParams p{};
   p.a = a;
   p.G = a.Hq / a.cache.heads;
   p.row_limit = row_limit;
+  p.odd = odd;
   p.max_ctas = a.num_sms < kMaxStreamCtas ? a.num_sms : kMaxStreamCtas;
   p.heads = reinterpret_cast<PartHead*>(ws);
   p.parts = reinterpret_cast<float*>(ws + sizeof(PartHead) * 2 * kMaxStreamCtas);
