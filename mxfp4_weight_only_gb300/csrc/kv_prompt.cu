@@ -80,18 +80,40 @@ __device__ __forceinline__ uint64_t sw128(uint32_t saddr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t idesc(int M, int N, bool tb) {
   return (1u << 4) | (tb ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+// The issuing thread must not fall behind the tensor core (an MMA takes 64
+// cycles): descriptors differ in their low word only, accumulation is a constant
+// wherever it can be.
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t hi, uint32_t bytes) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void mma_ss_first(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      "{\n .reg .pred p;\n setp.ne.u32 p, 0, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      "l"(ad), "l"(bd), "r"(id)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_acc(uint32_t d, uint32_t a, uint64_t bd, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
       "r"(a), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bd, uint32_t id) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(bd), "r"(id)
       : "memory");
 }
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -470,14 +492,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
       if (lane == 0 && nt > 0) {
-        const uint32_t sq = smem_u32(smem), sk = sq + C::kKOff, sv = sq + C::kVOff;
         constexpr uint32_t id_s = idesc(128, kKeys, false), id_o = idesc(128, D, true);
+        const uint64_t dk = sw128(smem_u32(smem), 16), dv = sw128(smem_u32(smem) + C::kVOff, kKeys * 128);
+        const uint32_t q_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), k_lo = q_lo + (C::kKOff >> 4);
+        const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
         auto scores = [&](int x, int s) {
+          const uint32_t qx = q_lo + x * (C::kQBytes >> 4), ks = k_lo + s * (C::kTile >> 4), d = tmem + C::kSCol + 128 * x;
+          mma_ss_first(d, desc_at(qx, k_hi, 0), desc_at(ks, k_hi, 0), id_s);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
+          for (int k = 1; k < D / 16; ++k) {
             const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            mma_ss(tmem + C::kSCol + 128 * x, sw128(sq + x * C::kQBytes + o, 16), sw128(sk + s * C::kTile + o, 16), id_s,
-                   k > 0);
+            mma_ss(d, desc_at(qx, k_hi, o), desc_at(ks, k_hi, o), id_s);
           }
           tc_commit(&s_full[x]);
         };
@@ -494,10 +519,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
                  mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs);
             if (!ok) break;
             tc_after();
+            const uint32_t vs = v_lo + s * (C::kTile >> 4), d = tmem + C::kOCol + 128 * x, pa = tmem + C::kSCol + 128 * x;
+            mma_ts_acc(d, pa, desc_at(vs, v_hi, 0), id_o, j > 0);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + C::kOCol + 128 * x, tmem + C::kSCol + 128 * x + 8 * k,
-                     sw128(sv + s * C::kTile + k * 16 * 128, kKeys * 128), id_o, j > 0 || k > 0);
+            for (int k = 1; k < kKeys / 16; ++k) mma_ts(d, pa + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
             tc_commit(&o_done[x]);
             if (x == nq - 1) tc_commit(&v_empty[s]);
             if (j + 1 < nt) {
