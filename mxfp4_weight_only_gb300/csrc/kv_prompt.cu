@@ -9,7 +9,7 @@
 //                      row's maximum only where p would pass 2^4, so the sum
 //                      below is rarely rescaled
 //   O += P V           tcgen05 f16, P from tensor memory (over S's columns)
-// Four converter warps expand each 128-key tile of the cache once for both
+// Eight converter warps expand each 128-key tile of the cache once for both
 // query tiles: E2M1 codes to f16 (one conversion per two values) times the
 // block's 2^(s-127), exact for scale bytes 104 .. 140 (and 0, blocks below
 // 2^-124, as zeros); K rows and V rows go to shared memory as they are, K as the
@@ -18,8 +18,10 @@
 // streaming kernel, which runs next.  Queries enter as f16 times a power of two
 // per row (exact: 8 significant bits), weights as f16 of p 2^11 (11 bits down to
 // p = 2^-25 of the reference).
-// While one tile's softmax runs, the tensor core works on the other tile:
-// PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) ...
+// While one tile's softmax runs, the tensor core works on the other tile.  Each
+// query tile has an issuing thread of its own: a thread that issues MMAs keeps
+// only a short queue, so its barrier probes and commits (about 100 cycles each)
+// leave the tensor core idle unless another thread's MMAs fill in.
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -27,8 +29,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kConvWarps = 4;
-constexpr int kPromptThreads = 32 * (kSoftWarps + 1 + kConvWarps);
+constexpr int kSoftWarps = 8, kConvWarp = 8, kConvWarps = 8, kMmaWarp = 16;
+constexpr int kPromptThreads = 32 * (kMmaWarp + 4);  // the last two warps only fill a warpgroup
+// Registers a thread of each warpgroup (launched with 96, 61,440 in all): 2
+// softmax groups x 128 x 160 + 2 converter groups x 128 x 56 + 128 x 40 = 60,416.
+constexpr int kLaunchRegs = 96, kSoftRegs = 160, kConvRegs = 56, kMmaRegs = 40;
+static_assert(128 * (2 * kSoftRegs + 2 * kConvRegs + kMmaRegs) <= kPromptThreads * kLaunchRegs, "register split");
 constexpr int kKeys = 128;         // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 4.f;      // a weight may reach 2^kSlack before its row's reference moves
@@ -170,7 +176,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -201,14 +206,27 @@ __device__ __forceinline__ float mul_pow2(float v, int e) {
   return v * exp2_int(h) * exp2_int(c - h);
 }
 
-// 2^(s-127) twice in f16 for s in 104 .. 140 (below 113 subnormal, still exact), 0 for s = 0.
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t s) {
-  const int e = (int)s - 112;  // f16 exponent field
-  uint32_t v = e > 0 ? (uint32_t)e << 10 : 1u << max(e + 9, 0);
-  if (s == 0u) v = 0u;
-  return v | (v << 16);
+// The f16 factors 2^(s-127), twice each, of a word's first NB scale bytes, for s
+// in 104 .. 140 (below 113 subnormal, still exact) and 0 (blocks below 2^-124:
+// zeros); any other sets ``odd``.
+template <int NB>
+__device__ __forceinline__ void scale_pairs(uint32_t w, uint32_t (&f)[4], bool& odd) {
+  if (NB == 2) w |= 0x7F7F0000u;
+  const uint32_t d = w - 0x70707070u;  // exponent fields s - 112, 1 .. 28 for s in 113 .. 140, if no byte borrows
+  const uint32_t e = d << 2;           // upper bytes of the factors
+#pragma unroll
+  for (int b = 0; b < NB; ++b) f[b] = prmt(e, 0u, 0x0404u | ((uint32_t)b << 4) | ((uint32_t)b << 12));
+  if (((d | (d - 0x01010101u) | (d + 0x03030303u)) & 0xE0E0E0E0u) != 0u) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t s = (w >> (8 * b)) & 255u;
+      const int x = (int)s - 112;
+      const uint32_t v = s == 0u ? 0u : x > 0 ? (uint32_t)min(x, 30) << 10 : 1u << max(x + 9, 0);
+      odd |= s != 0u && s - 104u > 36u;
+      f[b] = v | (v << 16);
+    }
+  }
 }
-__device__ __forceinline__ bool odd_scale(uint32_t s) { return s != 0u && s - 104u > 36u; }
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const PromptParams p) {
@@ -223,10 +241,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   uint64_t* v_empty = v_full + S;     // [S]
   uint64_t* q_full = v_empty + S;     // the query tiles are in shared memory
   uint64_t* s_full = q_full + 1;      // [2] scores of a tile are in tensor memory
-  uint64_t* p_full = s_full + 2;      // [2] weights are, and O is in their unit
+  uint64_t* p_half = s_full + 2;      // [2] weights of the first 64 keys are, and O is in their unit
+  uint64_t* p_full = p_half + 2;      // [2] all weights are
   uint64_t* o_done = p_full + 2;      // [2] the product with V is done
-  uint64_t* drain = o_done + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = o_done + 2;       // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ int item[4];  // request, kv head, first row, units before
   const KvAttnArgs& a = p.a;
@@ -236,17 +255,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&k_full[s], kConvWarps);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);
       mbar_init(&v_full[s], kConvWarps);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
     }
     mbar_init(q_full, kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], 4);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_done[x], 1);
+      mbar_init(&drain[x], 1);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     item[0] = -1;
     fence_barrier_init();
@@ -301,6 +321,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     const int32_t* table = a.table + (size_t)r * a.max_blocks;
 
     if (warp < kSoftWarps) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
       // ---------------------------------------------------------------- softmax: thread = row
       const int x = warp >> 2, quad = warp & 3;
       const int trow = 32 * quad + lane;           // row of the tile
@@ -311,33 +332,34 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
       {
         // the row's query, f16 times a power of two that puts its largest magnitude in [8, 16)
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(qb + i) * a.q_stride + (size_t)hq * D);
+        uint4 u[D / 8];
         float mx = 0.f;
-        if (real) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = __ldg(src + c);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int c = 0; c < D / 8; ++c) u[c] = real ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-          }
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
         }
         const int e = mx > 0.f && mx < INFINITY ? (int)(__float_as_uint(mx) >> 23) - 127 - 3 : 0;
         f = mul_pow2(fabsf(a.scale) * kLog2e, e);
-        const bool zero = f == 0.f || !real;
-        if (f == 0.f) f = 1.f;
+        // 2^-e in two factors (either alone may leave the range); none where the scores are all 0
+        float e0 = exp2_int((-e) >> 1), e1 = exp2_int(-e - ((-e) >> 1));
+        if (f == 0.f) {
+          f = 1.f;
+          e0 = 0.f;
+        }
         const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
         uint8_t* dst = smem + x * C::kQBytes + trow * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          uint4 o = make_uint4(0u, 0u, 0u, 0u);
-          if (!zero) {
-            const uint4 u = __ldg(src + c);
-            o.x = f32x2_to_f16x2(mul_pow2(bf16_lo(u.x), -e), mul_pow2(bf16_hi(u.x), -e)) ^ sign;
-            o.y = f32x2_to_f16x2(mul_pow2(bf16_lo(u.y), -e), mul_pow2(bf16_hi(u.y), -e)) ^ sign;
-            o.z = f32x2_to_f16x2(mul_pow2(bf16_lo(u.z), -e), mul_pow2(bf16_hi(u.z), -e)) ^ sign;
-            o.w = f32x2_to_f16x2(mul_pow2(bf16_lo(u.w), -e), mul_pow2(bf16_hi(u.w), -e)) ^ sign;
-          }
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (trow & 7)) << 4)) = o;
+          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = f32x2_to_f16x2(bf16_lo(w[k]) * e0 * e1, bf16_hi(w[k]) * e0 * e1) ^ sign;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (trow & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -384,24 +406,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
             }
             tc_st_wait();
           }
+          // the row's scores, once, in registers
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc_ld32(tS + 32 * c, v[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc_ld_wait32(v[c]);
           float mx = -INFINITY;
-          {
-            uint32_t v[2][32];
-            tc_ld32(tS, v[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t(&u)[32] = v[c & 1];
-              tc_ld_wait32(u);
-              if (c < 3) tc_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(u[k]), __uint_as_float(u[k + 1])));
-            }
-          }
+          for (int k = 0; k < 32; ++k)
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(v[0][k]), __uint_as_float(v[1][k]))),
+                       fmaxf(__uint_as_float(v[2][k]), __uint_as_float(v[3][k])));
           // the reference follows the maximum where a weight would pass 2^kSlack
           const bool grow = m == -INFINITY ? mx > -INFINITY : fmaf(mx, f, -mf) > kSlack;
           if (__any_sync(0xffffffffu, grow)) {
             float al = 1.f;
-            if (grow) {
+            if (mx > m) {  // (every row of the warp, now that its sums are read anyway)
               const float mf1 = mx * f;
               al = m == -INFINITY ? 0.f : ex2(mf - mf1);
               m = mx;
@@ -415,47 +435,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
                 break;
               }
               tc_after();
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t v[16];
-                tc_ld16(tO + 16 * c, v);
-                tc_ld_wait16(v);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * al);
-                tc_st16(tO + 16 * c, v);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tc_ld16(tO + 16 * c, o);
+                tc_ld_wait16(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                tc_st16(tO + 16 * c, o);
               }
             }
           }
           {
             const uint64_t f2 = pack2(f, f), off2 = pack2(kWeightExp - mf, kWeightExp - mf);
             uint64_t sum = pack2(0.f, 0.f);
-            uint32_t v[2][32];
-            tc_ld32(tS, v[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t(&u)[32] = v[c & 1];
-              tc_ld_wait32(u);
-              // (the next scores are read before this step's weights go over earlier ones)
-              if (c < 3) tc_ld32(tS + 32 * (c + 1), v[(c + 1) & 1]);
               uint32_t w[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
                 float x0, x1;
-                unpack2(fma2(pack2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), f2, off2), x0, x1);
+                unpack2(fma2(pack2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), f2, off2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
                 sum = add2(sum, pack2(p0, p1));
                 w[k] = f32x2_to_f16x2(p0, p1);
               }
               tc_st16(tS + 16 * c, w);
+              if (c & 1) {  // half of the keys: their product may start
+                tc_st_wait();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_full[x]);
+              }
             }
             float l0, l1;
             unpack2(sum, l0, l1);
             l += l0 + l1;
           }
-          tc_st_wait();
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[x]);
         }
         if (ok && nt > 0 && !mbar_wait(&o_done[x], (nt - 1) & 1, a.status, kWaitLimitNs)) {
           *abort_flag = 1;
@@ -470,7 +486,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
             uint32_t v[32];
             if (nt > 0) {
               tc_ld32(tO + 32 * c, v);
-              tc_ld_wait();
+              tc_ld_wait32(v);
             }
             if (real) {
               uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 32 * c);
@@ -489,87 +505,89 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
           if (real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (mf + lg2(l) - kWeightExp) * 0.6931471805599453f;
         }
       }
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0 && nt > 0) {
+    } else if (warp >= kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issuer of query tile x
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+      const int x = warp - kMmaWarp;
+      if (lane == 0 && nt > 0 && x < nq) {
         constexpr uint32_t id_s = idesc(128, kKeys, false), id_o = idesc(128, D, true);
         const uint64_t dk = sw128(smem_u32(smem), 16), dv = sw128(smem_u32(smem) + C::kVOff, kKeys * 128);
-        const uint32_t q_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), k_lo = q_lo + (C::kKOff >> 4);
-        const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
-        auto scores = [&](int x, int s) {
-          const uint32_t qx = q_lo + x * (C::kQBytes >> 4), ks = k_lo + s * (C::kTile >> 4), d = tmem + C::kSCol + 128 * x;
-          mma_ss_first(d, desc_at(qx, k_hi, 0), desc_at(ks, k_hi, 0), id_s);
+        const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
+        const uint32_t qx = (uint32_t)dk + x * (C::kQBytes >> 4), k_lo = (uint32_t)dk + (C::kKOff >> 4), v_lo = (uint32_t)dv;
+        const uint32_t ts = tmem + C::kSCol + 128 * x, to = tmem + C::kOCol + 128 * x;
+        const int commits = 3 - nq;  // the stages' barriers count one arrival per query tile
+        auto scores = [&](int s) {
+          const uint32_t ks = k_lo + s * (C::kTile >> 4);
+          mma_ss_first(ts, desc_at(qx, k_hi, 0), desc_at(ks, k_hi, 0), id_s);
 #pragma unroll
           for (int k = 1; k < D / 16; ++k) {
             const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            mma_ss(d, desc_at(qx, k_hi, o), desc_at(ks, k_hi, o), id_s);
+            mma_ss(ts, desc_at(qx, k_hi, o), desc_at(ks, k_hi, o), id_s);
           }
           tc_commit(&s_full[x]);
+          for (int c = 0; c < commits; ++c) tc_commit(&k_empty[s]);
         };
         bool ok = mbar_wait(q_full, 0, a.status, kWaitLimitNs) && mbar_wait(&k_full[0], 0, a.status, kWaitLimitNs);
         tc_after();
-        if (ok) {
-          for (int x = 0; x < nq; ++x) scores(x, 0);
-          tc_commit(&k_empty[0]);
-        }
+        if (ok) scores(0);
         for (int j = 0; j < nt && ok; ++j) {
           const int s = j % S, s1 = (j + 1) % S;
-          for (int x = 0; x < nq && ok; ++x) {
-            ok = (x > 0 || mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs)) &&
-                 mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs);
+          ok = mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs) &&
+               mbar_wait(&p_half[x], j & 1, a.status, kWaitLimitNs);
+          if (!ok) break;
+          tc_after();
+          const uint32_t vs = v_lo + s * (C::kTile >> 4);
+          mma_ts_acc(to, ts, desc_at(vs, v_hi, 0), id_o, j > 0);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
+          ok = mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs);
+          if (!ok) break;
+          tc_after();
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
+          tc_commit(&o_done[x]);
+          for (int c = 0; c < commits; ++c) tc_commit(&v_empty[s]);
+          if (j + 1 < nt) {
+            ok = mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs);
             if (!ok) break;
             tc_after();
-            const uint32_t vs = v_lo + s * (C::kTile >> 4), d = tmem + C::kOCol + 128 * x, pa = tmem + C::kSCol + 128 * x;
-            mma_ts_acc(d, pa, desc_at(vs, v_hi, 0), id_o, j > 0);
-#pragma unroll
-            for (int k = 1; k < kKeys / 16; ++k) mma_ts(d, pa + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
-            tc_commit(&o_done[x]);
-            if (x == nq - 1) tc_commit(&v_empty[s]);
-            if (j + 1 < nt) {
-              ok = x > 0 || mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs);
-              if (!ok) break;
-              tc_after();
-              scores(x, s1);
-              if (x == nq - 1) tc_commit(&k_empty[s1]);
-            }
+            scores(s1);
           }
           if (*abort_flag) ok = false;
         }
         if (!ok) *abort_flag = 1;
         // all issued MMAs complete before tensor memory is released
-        tc_commit(drain);
-        mbar_wait(drain, 0, a.status, kWaitLimitNs);
+        tc_commit(&drain[x]);
+        mbar_wait(&drain[x], 0, a.status, kWaitLimitNs);
       }
     } else {
-      // ---------------------------------------------------------------- converters: two records of a tile per warp
-      const int cw = warp - kMmaWarp - 1;
+      // ---------------------------------------------------------------- converters: one record of a tile per warp
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+      const int cw = warp - kConvWarp;
       const int g = lane >> 2, t = lane & 3;
       bool odd = false;
       bool ok = true;
-      // codes and scales of a tile in registers: lane (g, t) takes, per record, two
-      // tokens' words of K and four tokens' of V; loaded a tile ahead
-      const uint8_t* rec[2];
-      int valid[2];
-      uint32_t kc[2][2][NB], vc[2][2][NB], ks[2][2], vs[2][4];
+      // codes and scales of a record in registers: lane (g, t) takes two tokens'
+      // words of K and four tokens' of V; loaded a tile ahead
+      const uint8_t* rec = nullptr;
+      int valid = 0;
+      uint32_t kc[2][NB], vc[2][NB], ks[2] = {0u, 0u}, vs[4] = {0u, 0u, 0u, 0u};
       auto locate = [&](int j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int key = (t0 + j) * kKeys + (2 * cw + h) * 16;
-          rec[h] = nullptr;
-          valid[h] = 0;
-          if (j < nt && key < n) {
-            const int pg = table[key >> a.cache.page_shift];
-            if (pg >= 0 && pg < a.cache.num_pages) {
-              rec[h] = a.cache.data + a.cache.record(pg, kvh, (key & ((1 << a.cache.page_shift) - 1)) >> 4);
-              valid[h] = min(16, n - key);
-            }
+        const int key = (t0 + j) * kKeys + cw * 16;
+        rec = nullptr;
+        valid = 0;
+        if (j < nt && key < n) {
+          const int pg = table[key >> a.cache.page_shift];
+          if (pg >= 0 && pg < a.cache.num_pages) {
+            rec = a.cache.data + a.cache.record(pg, kvh, (key & ((1 << a.cache.page_shift) - 1)) >> 4);
+            valid = min(16, n - key);
           }
         }
       };
       // the scale bytes of token tok (0: past the end, whose values become zeros)
-      auto scales = [&](int h, int which, int tok) -> uint32_t {
-        if (tok >= valid[h]) return 0u;
-        const uint8_t* q = rec[h] + 16 * D + which * (D / 2) + tok * NB;
+      auto scales = [&](int which, int tok) -> uint32_t {
+        if (tok >= valid) return 0u;
+        const uint8_t* q = rec + 16 * D + which * (D / 2) + tok * NB;
         return NB == 4 ? *reinterpret_cast<const uint32_t*>(q) : (uint32_t) * reinterpret_cast<const uint16_t*>(q);
       };
       auto words = [&](const uint8_t* q, uint32_t (&c)[NB]) {
@@ -582,38 +600,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         }
       };
       auto load_k = [&]() {
+        ks[0] = ks[1] = 0u;
+        if (rec) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (rec[h]) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              words(rec[h] + u * 4 * D, kc[h][u]);
-              ks[h][u] = scales(h, 0, 8 * u + g);
-            }
-          } else {
-            ks[h][0] = ks[h][1] = 0u;
+          for (int u = 0; u < 2; ++u) {
+            words(rec + u * 4 * D, kc[u]);
+            ks[u] = scales(0, 8 * u + g);
           }
+        }
       };
       auto load_v = [&]() {
+        vs[0] = vs[1] = vs[2] = vs[3] = 0u;
+        if (rec) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (rec[h]) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              words(rec[h] + 8 * D + u * 4 * D, vc[h][u]);
-              vs[h][2 * u] = scales(h, 1, 8 * u + 2 * t);
-              vs[h][2 * u + 1] = scales(h, 1, 8 * u + 2 * t + 1);
-            }
-          } else {
-            vs[h][0] = vs[h][1] = vs[h][2] = vs[h][3] = 0u;
+          for (int u = 0; u < 2; ++u) {
+            words(rec + 8 * D + u * 4 * D, vc[u]);
+            vs[2 * u] = scales(1, 8 * u + 2 * t);
+            vs[2 * u + 1] = scales(1, 8 * u + 2 * t + 1);
           }
+        }
       };
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int b = 0; b < NB; ++b) kc[h][u][b] = vc[h][u][b] = 0u;
+        for (int b = 0; b < NB; ++b) kc[u][b] = vc[u][b] = 0u;
       locate(0);
       load_k();
       load_v();
@@ -625,54 +635,49 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
           break;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int u = 0; u < 2; ++u) {
+          const int krow = cw * 16 + 8 * u + g;
+          uint8_t* dst = smem + C::kKOff + s * C::kTile + krow * 128;
+          uint32_t sc[4];
+          scale_pairs<NB>(ks[u], sc, odd);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int krow = (2 * cw + h) * 16 + 8 * u + g;
-            uint8_t* dst = smem + C::kKOff + s * C::kTile + krow * 128;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              const uint32_t sb = (ks[h][u] >> (8 * b)) & 255u, sc = scale_f16x2(sb);
-              odd |= odd_scale(sb);
-              uint32_t y[4];
-              e2m1x8_to_f16x8(kc[h][u][b], y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(dst + (b >> 1) * (128 * 128) + ((((b & 1) * 4 + t) ^ (krow & 7)) << 4)) =
-                  make_uint4(hmul2(y[0], sc), hmul2(y[1], sc), hmul2(y[2], sc), hmul2(y[3], sc));
-            }
+          for (int b = 0; b < NB; ++b) {
+            uint32_t y[4];
+            e2m1x8_to_f16x8(kc[u][b], y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + (b >> 1) * (128 * 128) + ((((b & 1) * 4 + t) ^ (krow & 7)) << 4)) =
+                make_uint4(hmul2(y[0], sc[b]), hmul2(y[1], sc[b]), hmul2(y[2], sc[b]), hmul2(y[3], sc[b]));
           }
-        load_k();
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[s]);
+        load_k();
         if (j >= S && !mbar_wait(&v_empty[s], ((j / S) - 1) & 1, a.status, kWaitLimitNs)) {
           ok = false;
           break;
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int w = 0; w < 2; ++w) {  // token 8 u + 2 t + w: dims 4 g .. of every block
+            const int krow = cw * 16 + 8 * u + 2 * t + w;
+            uint8_t* dst = smem + C::kVOff + s * C::kTile + krow * 128 + 8 * (g & 1);
+            uint32_t sc[4];
+            scale_pairs<NB>(vs[2 * u + w], sc, odd);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {  // token 8 u + 2 t + w: dims 4 g .. of every block
-              const int krow = (2 * cw + h) * 16 + 8 * u + 2 * t + w;
-              uint8_t* dst = smem + C::kVOff + s * C::kTile + krow * 128 + 8 * (g & 1);
+            for (int bp = 0; bp < NB / 2; ++bp) {
+              uint32_t y[4];
+              e2m1x8_to_f16x8(vc[u][w * (NB / 2) + bp], y[0], y[1], y[2], y[3]);
 #pragma unroll
-              for (int bp = 0; bp < NB / 2; ++bp) {
-                uint32_t y[4];
-                e2m1x8_to_f16x8(vc[h][u][w * (NB / 2) + bp], y[0], y[1], y[2], y[3]);
-#pragma unroll
-                for (int bb = 0; bb < 2; ++bb) {
-                  const uint32_t sb = (vs[h][2 * u + w] >> (8 * (2 * bp + bb))) & 255u, sc = scale_f16x2(sb);
-                  odd |= odd_scale(sb);
-                  *reinterpret_cast<uint2*>(dst + bp * (kKeys * 128) + (((bb * 4 + (g >> 1)) ^ (krow & 7)) << 4)) =
-                      make_uint2(hmul2(y[2 * bb], sc), hmul2(y[2 * bb + 1], sc));
-                }
-              }
+              for (int bb = 0; bb < 2; ++bb)
+                *reinterpret_cast<uint2*>(dst + bp * (kKeys * 128) + (((bb * 4 + (g >> 1)) ^ (krow & 7)) << 4)) =
+                    make_uint2(hmul2(y[2 * bb], sc[2 * bp + bb]), hmul2(y[2 * bb + 1], sc[2 * bp + bb]));
             }
-        load_v();
+          }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[s]);
+        load_v();
       }
       if (!ok) *abort_flag = 1;
       if (odd) p.odd[r] = 1;
@@ -689,7 +694,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
 template <int D>
 cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t s) {
   using C = PromptCfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  // the register split draws on what the kernel is launched with: never launch it with less
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, kv_prompt_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   kv_prompt_kernel<D><<<grid, kPromptThreads, C::kSmem, s>>>(p);
   return cudaGetLastError();
