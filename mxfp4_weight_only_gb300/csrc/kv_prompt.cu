@@ -6,7 +6,7 @@
 // time:
 //   S = Q K^T          tcgen05 f16, accumulator 128 columns of tensor memory
 //   p = 2^(S f - m)    f: scale, log2 e and the row's power of two; m follows the
-//                      row's maximum only where p would pass 2^4, so the sum
+//                      row's maximum only where p would pass 2^6, so the sum
 //                      below is rarely rescaled
 //   O += P V           tcgen05 f16, P from tensor memory (over S's columns)
 // Eight converter warps expand each 128-key tile of the cache once for both
@@ -16,12 +16,14 @@
 // K-major and V as the MN-major operand, both with the 128-byte swizzle.  A
 // request with any other scale byte (NaN among them) is marked and left to the
 // streaming kernel, which runs next.  Queries enter as f16 times a power of two
-// per row (exact: 8 significant bits), weights as f16 of p 2^11 (11 bits down to
-// p = 2^-25 of the reference).
+// per row (exact: 8 significant bits), weights as f16 of p 2^9 (11 bits down to
+// p = 2^-23 of the reference).
 // While one tile's softmax runs, the tensor core works on the other tile.  Each
 // query tile has an issuing thread of its own: a thread that issues MMAs keeps
 // only a short queue, so its barrier probes and commits (about 100 cycles each)
-// leave the tensor core idle unless another thread's MMAs fill in.
+// leave the tensor core idle unless another thread's MMAs fill in.  The two take
+// turns, which keeps one tile's softmax beside the other's MMAs (without turns
+// both softmaxes fell into step, and then both products).
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -37,8 +39,9 @@ constexpr int kLaunchRegs = 96, kSoftRegs = 160, kConvRegs = 56, kMmaRegs = 40;
 static_assert(128 * (2 * kSoftRegs + 2 * kConvRegs + kMmaRegs) <= kPromptThreads * kLaunchRegs, "register split");
 constexpr int kKeys = 128;         // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 4.f;      // a weight may reach 2^kSlack before its row's reference moves
-constexpr float kWeightExp = 11.f; // weights are held times 2^11: at most 2^15 in f16
+// Weights are held in f16 times 2^kWeightExp; one may reach 2^kSlack before its
+// row's reference moves (at most 2^15 in f16), which rescales O.
+constexpr float kSlack = 6.f, kWeightExp = 9.f;
 
 template <int D>
 struct PromptCfg {
@@ -157,6 +160,11 @@ __device__ __forceinline__ void tc_ld_wait32(uint32_t (&r)[32]) {
                : "memory");
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // a * b + c and a + b on two floats at once.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -241,10 +249,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   uint64_t* v_empty = v_full + S;     // [S]
   uint64_t* q_full = v_empty + S;     // the query tiles are in shared memory
   uint64_t* s_full = q_full + 1;      // [2] scores of a tile are in tensor memory
-  uint64_t* p_half = s_full + 2;      // [2] weights of the first 64 keys are, and O is in their unit
-  uint64_t* p_full = p_half + 2;      // [2] all weights are
+  uint64_t* p_full = s_full + 2;      // [2] weights are, and O is in their unit
   uint64_t* o_done = p_full + 2;      // [2] the product with V is done
-  uint64_t* drain = o_done + 2;       // [2]
+  uint64_t* turn = o_done + 2;        // [2] the other query tile's MMAs have been issued
+  uint64_t* drain = turn + 2;         // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ int item[4];  // request, kv head, first row, units before
@@ -262,8 +270,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     mbar_init(q_full, kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_half[x], 4);
       mbar_init(&p_full[x], 4);
+      mbar_init(&turn[x], 1);
       mbar_init(&o_done[x], 1);
       mbar_init(&drain[x], 1);
     }
@@ -372,16 +380,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
       const uint32_t tO = tmem + ((uint32_t)(32 * quad) << 16) + C::kOCol + 128 * x;
       float m = -INFINITY, mf = 0.f, l = 0.f;  // reference of the scores, times f; sum of weights (2^11 times)
       bool ok = true;
+      // page of record ``lane`` of tile j, -1 for none; looked up a tile ahead
+      auto page_of = [&](int j) -> int {
+        const int key = (t0 + j) * kKeys + 16 * lane;
+        return lane < 8 && j < nt && key < n ? table[key >> a.cache.page_shift] : -1;
+      };
+      int next_page = page_of(0);
       if (x < nq) {
         for (int j = 0; j < nt; ++j) {
           const int j0 = (t0 + j) * kKeys;
           // records of this tile that exist: bit k for keys 16 k ..
-          bool there = false;
-          if (lane < 8 && j0 + 16 * lane < n) {
-            const int pg = table[(j0 + 16 * lane) >> a.cache.page_shift];
-            there = pg >= 0 && pg < a.cache.num_pages;
-          }
-          const uint32_t have = __ballot_sync(0xffffffffu, there) & 0xFFu;
+          const uint32_t have = __ballot_sync(0xffffffffu, next_page >= 0 && next_page < a.cache.num_pages) & 0xFFu;
+          next_page = page_of(j + 1);
           if (*abort_flag || !mbar_wait(&s_full[x], j & 1, a.status, kWaitLimitNs)) {
             *abort_flag = 1;
             ok = false;
@@ -413,42 +423,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc_ld_wait32(v[c]);
           float mx = -INFINITY;
+          {
+            float part[4] = {mx, mx, mx, mx};
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(v[0][k]), __uint_as_float(v[1][k]))),
-                       fmaxf(__uint_as_float(v[2][k]), __uint_as_float(v[3][k])));
+            for (int k = 0; k < 32; k += 2)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) part[c] = max3(part[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
+            mx = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+          }
           // the reference follows the maximum where a weight would pass 2^kSlack
           const bool grow = m == -INFINITY ? mx > -INFINITY : fmaf(mx, f, -mf) > kSlack;
-          if (__any_sync(0xffffffffu, grow)) {
-            float al = 1.f;
-            if (mx > m) {  // (every row of the warp, now that its sums are read anyway)
-              const float mf1 = mx * f;
-              al = m == -INFINITY ? 0.f : ex2(mf - mf1);
-              m = mx;
-              mf = mf1;
-              l *= al;
-            }
-            if (j > 0) {
-              if (!mbar_wait(&o_done[x], (j - 1) & 1, a.status, kWaitLimitNs)) {
-                *abort_flag = 1;
-                ok = false;
-                break;
-              }
-              tc_after();
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tc_ld16(tO + 16 * c, o);
-                tc_ld_wait16(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                tc_st16(tO + 16 * c, o);
-              }
-            }
+          const bool move = __any_sync(0xffffffffu, grow);
+          float al = 1.f;
+          if (move && mx > m) {  // (every row of the warp, now that its sums are read anyway)
+            const float mf1 = mx * f;
+            al = m == -INFINITY ? 0.f : ex2(mf - mf1);
+            m = mx;
+            mf = mf1;
+            l *= al;
           }
           {
             const uint64_t f2 = pack2(f, f), off2 = pack2(kWeightExp - mf, kWeightExp - mf);
-            uint64_t sum = pack2(0.f, 0.f);
+            uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t w[16];
@@ -457,19 +453,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
                 float x0, x1;
                 unpack2(fma2(pack2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), f2, off2), x0, x1);
                 const float p0 = ex2(x0), p1 = ex2(x1);
-                sum = add2(sum, pack2(p0, p1));
+                sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
                 w[k] = f32x2_to_f16x2(p0, p1);
               }
               tc_st16(tS + 16 * c, w);
-              if (c & 1) {  // half of the keys: their product may start
-                tc_st_wait();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_full[x]);
+            }
+            if (move && j > 0) {
+              // O, after the scores, whose registers it takes (the product before
+              // these scores is done: one thread's MMAs complete in order)
+              if (!mbar_wait(&o_done[x], (j - 1) & 1, a.status, kWaitLimitNs)) {
+                *abort_flag = 1;
+                ok = false;
+                break;
+              }
+              tc_after();
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) {
+                uint32_t o[2][32];
+                tc_ld32(tO + 64 * c, o[0]);
+                tc_ld32(tO + 64 * c + 32, o[1]);
+                tc_ld_wait32(o[0]);
+                tc_ld_wait32(o[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(o[h][16 * q + k]) * al);
+                    tc_st16(tO + 64 * c + 32 * h + 16 * q, w);
+                  }
               }
             }
+            tc_st_wait();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[x]);
             float l0, l1;
-            unpack2(sum, l0, l1);
+            unpack2(add2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
           }
         }
@@ -532,19 +553,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         if (ok) scores(0);
         for (int j = 0; j < nt && ok; ++j) {
           const int s = j % S, s1 = (j + 1) % S;
+          // (A's turn j comes after B's j - 1, B's after A's j)
           ok = mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs) &&
-               mbar_wait(&p_half[x], j & 1, a.status, kWaitLimitNs);
+               mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs) &&
+               (nq == 1 || (x == 0 && j == 0) || mbar_wait(&turn[x], (j - (x == 0)) & 1, a.status, kWaitLimitNs));
           if (!ok) break;
           tc_after();
           const uint32_t vs = v_lo + s * (C::kTile >> 4);
           mma_ts_acc(to, ts, desc_at(vs, v_hi, 0), id_o, j > 0);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
-          ok = mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs);
-          if (!ok) break;
-          tc_after();
-#pragma unroll
-          for (int k = 4; k < 8; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
+          for (int k = 1; k < kKeys / 16; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
           tc_commit(&o_done[x]);
           for (int c = 0; c < commits; ++c) tc_commit(&v_empty[s]);
           if (j + 1 < nt) {
@@ -553,6 +571,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
             tc_after();
             scores(s1);
           }
+          if (nq == 2) mbar_arrive(&turn[1 - x]);
           if (*abort_flag) ok = false;
         }
         if (!ok) *abort_flag = 1;
