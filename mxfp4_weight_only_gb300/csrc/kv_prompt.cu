@@ -90,8 +90,16 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool tb) {
   return (1u << 4) | (tb ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // The issuing thread must not fall behind the tensor core (an MMA takes 64
-// cycles): descriptors differ in their low word only, accumulation is a constant
-// wherever it can be.
+// cycles).  Its operands live in uniform registers: the whole warp runs the
+// issuing loop on warp-uniform values and one elected lane issues (computed in a
+// branch of one lane, every operand is moved there for every MMA: about 120
+// cycles an MMA).  Descriptors differ in their low word only, accumulation is a
+// constant wherever it can be.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t hi, uint32_t bytes) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ int item[4];  // request, kv head, first row, units before
   const KvAttnArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int H = a.cache.heads;
 
   if (tid == 0) {
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int r = item[0];
   if (r >= 0) {
     const int kvh = item[1], row0 = item[2];
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
       // ---------------------------------------------------------------- MMA issuer of query tile x
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
       const int x = warp - kMmaWarp;
-      if (lane == 0 && nt > 0 && x < nq) {
+      if (nt > 0 && x < nq) {
         constexpr uint32_t id_s = idesc(128, kKeys, false), id_o = idesc(128, D, true);
         const uint64_t dk = sw128(smem_u32(smem), 16), dv = sw128(smem_u32(smem) + C::kVOff, kKeys * 128);
         const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32);
@@ -539,44 +547,53 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         const int commits = 3 - nq;  // the stages' barriers count one arrival per query tile
         auto scores = [&](int s) {
           const uint32_t ks = k_lo + s * (C::kTile >> 4);
-          mma_ss_first(ts, desc_at(qx, k_hi, 0), desc_at(ks, k_hi, 0), id_s);
+          if (elect_one()) {
+            mma_ss_first(ts, desc_at(qx, k_hi, 0), desc_at(ks, k_hi, 0), id_s);
 #pragma unroll
-          for (int k = 1; k < D / 16; ++k) {
-            const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            mma_ss(ts, desc_at(qx, k_hi, o), desc_at(ks, k_hi, o), id_s);
+            for (int k = 1; k < D / 16; ++k) {
+              const uint32_t o = (k >> 2) * (128 * 128) + (k & 3) * 32;
+              mma_ss(ts, desc_at(qx, k_hi, o), desc_at(ks, k_hi, o), id_s);
+            }
+            tc_commit(&s_full[x]);
+            for (int c = 0; c < commits; ++c) tc_commit(&k_empty[s]);
           }
-          tc_commit(&s_full[x]);
-          for (int c = 0; c < commits; ++c) tc_commit(&k_empty[s]);
+          __syncwarp();
         };
-        bool ok = mbar_wait(q_full, 0, a.status, kWaitLimitNs) && mbar_wait(&k_full[0], 0, a.status, kWaitLimitNs);
+        // (every lane waits; a wait that runs out in one lane ends the loop in all)
+        auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+        bool ok = all(mbar_wait(q_full, 0, a.status, kWaitLimitNs) && mbar_wait(&k_full[0], 0, a.status, kWaitLimitNs));
         tc_after();
         if (ok) scores(0);
         for (int j = 0; j < nt && ok; ++j) {
           const int s = j % S, s1 = (j + 1) % S;
           // (A's turn j comes after B's j - 1, B's after A's j)
-          ok = mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs) &&
-               mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs) &&
-               (nq == 1 || (x == 0 && j == 0) || mbar_wait(&turn[x], (j - (x == 0)) & 1, a.status, kWaitLimitNs));
+          ok = all(mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs) &&
+                   mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs) &&
+                   (nq == 1 || (x == 0 && j == 0) || mbar_wait(&turn[x], (j - (x == 0)) & 1, a.status, kWaitLimitNs)));
           if (!ok) break;
           tc_after();
           const uint32_t vs = v_lo + s * (C::kTile >> 4);
-          mma_ts_acc(to, ts, desc_at(vs, v_hi, 0), id_o, j > 0);
+          if (elect_one()) {
+            mma_ts_acc(to, ts, desc_at(vs, v_hi, 0), id_o, j > 0);
 #pragma unroll
-          for (int k = 1; k < kKeys / 16; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
-          tc_commit(&o_done[x]);
-          for (int c = 0; c < commits; ++c) tc_commit(&v_empty[s]);
+            for (int k = 1; k < kKeys / 16; ++k) mma_ts(to, ts + 8 * k, desc_at(vs, v_hi, k * 16 * 128), id_o);
+            tc_commit(&o_done[x]);
+            for (int c = 0; c < commits; ++c) tc_commit(&v_empty[s]);
+          }
+          __syncwarp();
           if (j + 1 < nt) {
-            ok = mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs);
+            ok = all(mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs));
             if (!ok) break;
             tc_after();
             scores(s1);
           }
-          if (nq == 2) mbar_arrive(&turn[1 - x]);
-          if (*abort_flag) ok = false;
+          if (nq == 2 && lane == 0) mbar_arrive(&turn[1 - x]);
+          ok = all(*abort_flag == 0);
         }
         if (!ok) *abort_flag = 1;
         // all issued MMAs complete before tensor memory is released
-        tc_commit(&drain[x]);
+        if (elect_one()) tc_commit(&drain[x]);
+        __syncwarp();
         mbar_wait(&drain[x], 0, a.status, kWaitLimitNs);
       }
     } else {
