@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
   int32_t* start = sm;              // [R + 1] first token of each request
   int32_t* cached = start + a.R + 1;  // [R]
   int32_t* ofs = cached + a.R;      // [R] ring offset of its first new page; -1: refused
-  __shared__ long long scratch[2 * (kTableThreads / 32)];
+  __shared__ long long scratch[2 * (kTableThreads / 32)], taken_sum;
   const int tid = threadIdx.x, R = a.R;
+  if (tid == 0) taken_sum = 0;
   const int page = 1 << a.page_shift;
   const int per = (R + kTableThreads - 1) / kTableThreads;  // consecutive requests of this thread
   const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     ofs[r] = a.added[r];
   }
   __syncthreads();
-  long long tok = 0, zero = 0, total = 0, unused = 0;
+  long long tok = 0, zero = 0, total, unused;
   for (int r = r0; r < r1; ++r) tok += max(ofs[r], 0);
   block_exclusive2(tok, zero, &total, &unused, scratch);
   // pages needed by requests that fit otherwise, pages given back
@@ -121,8 +122,9 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     }
   }
   if (tid == 0) start[R] = (int)min(total, 0x7FFFFFFFll);
-  long long t2 = 0, taken_all;
-  block_exclusive2(taken, t2, &taken_all, &unused, scratch);  // also orders the shared arrays before their readers
+  if (taken > 0) atomicAdd(reinterpret_cast<unsigned long long*>(&taken_sum), (unsigned long long)taken);
+  __syncthreads();  // the shared arrays are complete
+  const long long taken_all = taken_sum;
   if (first && tid == 0) {
     a.query_start[R] = start[R];
     a.state_out[0] = (int)(((long long)head + taken_all) % a.ring_size);
@@ -219,53 +221,92 @@ __device__ __forceinline__ void kv_quant8(float (&v)[8], uint32_t& codes, uint32
   sbyte = nan ? 255u : s;
 }
 
+template <bool F32>
+struct Raw8;  // eight input values as loaded
+template <>
+struct Raw8<false> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    u = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+  }
+};
+template <>
+struct Raw8<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+    a = __ldcs(q);
+    b = __ldcs(q + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
+// Rows a thread keeps in flight: with one, the chain slot -> row -> store of each
+// row stood in the open (append and gather of 16,384 x 8 x 128: 52.9 us).
+constexpr int kRowsInFlight = 4;
+
 // Quantising write (kv_mxfp4_append).  HBM-bound: 2 or 4 bytes read and 17/32
-// byte written per value.  D / 8 lanes take one row (a token's K or V of one
-// head); the loop bound is uniform per warp, so every lane reaches the
-// block-maximum shuffles.
+// byte written per value.  D / 8 lanes take a token's K and V row of one head;
+// the loop bounds are uniform per warp, so every lane reaches the shuffles.
+// Neighbouring blocks' lanes trade halves of their V words, so that each writes
+// four bytes of one lane's operand.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const void* __restrict__ k,
                                                         const void* __restrict__ v, long long ks, long long vs, int N,
                                                         const int32_t* __restrict__ slots) {
   constexpr int L = D / 8, NB = D / 32;  // lanes per row
-  const long long rows = 2ll * N * c.heads;
-  const long long stride = (long long)gridDim.x * (256 / L);
-  const int sub = threadIdx.x % L;
-  for (long long w0 = (long long)blockIdx.x * (256 / L); w0 < rows; w0 += stride) {
-    const long long row = w0 + threadIdx.x / L;
-    const int which = (int)(row & 1);
-    const long long th = row >> 1;
-    const int tok = (int)(th / c.heads), head = (int)(th - (long long)tok * c.heads);
-    const int slot = row < rows ? slots[tok] : -1;
-    const bool live = slot >= 0 && (slot >> c.page_shift) < c.num_pages;
-    float x[8];
-    if (live) {
-      const long long at = (long long)tok * (which ? vs : ks) + (long long)head * D + 8 * sub;
-      if (F32) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(which ? v : k) + at);
-        const float4 a = __ldcs(p), b = __ldcs(p + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-      } else {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(which ? v : k) + at));
-        x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-        x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
-      }
-    } else {
+  const long long rows = (long long)N * c.heads;
+  const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
+  const long long step = (long long)gridDim.x * (256 / L), first = (long long)blockIdx.x * (256 / L);
+  for (long long w0 = first; w0 < rows; w0 += step * kRowsInFlight) {
+    Raw8<F32> raw[kRowsInFlight][2];
+    int slot[kRowsInFlight], head[kRowsInFlight];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    uint32_t codes, sb;
-    kv_quant8(x, codes, sb);
-    if (live) {
-      const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
-      uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
-      if (which) {
-        *reinterpret_cast<uint16_t*>(rec + v_byte<D>(t, 4 * sub)) = (uint16_t)codes;
-        *reinterpret_cast<uint16_t*>(rec + v_byte<D>(t, 4 * sub + 2)) = (uint16_t)(codes >> 16);
-      } else {
-        *reinterpret_cast<uint32_t*>(rec + k_byte<D>(t, 4 * sub)) = codes;
+    for (int i = 0; i < kRowsInFlight; ++i) {
+      const long long row = w0 + i * step + threadIdx.x / L;
+      const int tok = (int)(row / c.heads);
+      head[i] = (int)(row - (long long)tok * c.heads);
+      slot[i] = -1;
+      if (row < rows) {
+        slot[i] = slots[tok];
+        const long long at = (long long)head[i] * D + 8 * sub;
+        raw[i][0].load(k, (long long)tok * ks + at);
+        raw[i][1].load(v, (long long)tok * vs + at);
       }
-      if ((sub & 3) == 0) rec[16 * D + which * (D / 2) + t * NB + (sub >> 2)] = (uint8_t)sb;
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsInFlight; ++i) {
+      if (w0 + i * step >= rows) break;  // (uniform per CTA)
+      const bool live = slot[i] >= 0 && (slot[i] >> c.page_shift) < c.num_pages;
+      uint32_t code[2], sb[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        float x[8];
+        if (live) {
+          raw[i][w].get(x);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) x[q] = 0.f;
+        }
+        kv_quant8(x, code[w], sb[w]);
+      }
+      // V: lanes of blocks b and b ^ 1 hold bytes 2 t4 (lower half) and 2 t4 + 1
+      // (upper) of their blocks; even b takes the lower halves of both, odd b the upper
+      const uint32_t theirs = __shfl_xor_sync(0xffffffffu, code[1], 4);
+      const uint32_t vw = (b & 1) ? prmt(theirs, code[1], 0x7632u) : prmt(code[1], theirs, 0x5410u);
+      if (live) {
+        const int off = slot[i] & ((1 << c.page_shift) - 1), t = off & 15;
+        uint8_t* rec = c.data + c.record(slot[i] >> c.page_shift, head[i], off >> 4);
+        *reinterpret_cast<uint32_t*>(rec + k_byte<D>(t, 4 * sub)) = code[0];
+        *reinterpret_cast<uint32_t*>(rec + v_byte<D>(t, 4 * t4 + 2 * (b & 1) + 16 * (b & ~1))) = vw;
+        if (t4 < 2) rec[16 * D + t4 * (D / 2) + t * NB + b] = (uint8_t)sb[t4];
+      }
     }
   }
 }
@@ -275,34 +316,51 @@ template <int D>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const KvView c, const int32_t* __restrict__ slots, int N,
                                                         uint4* __restrict__ ko, uint4* __restrict__ vo) {
   constexpr int L = D / 8, NB = D / 32;
-  const long long rows = 2ll * N * c.heads;
-  const long long stride = (long long)gridDim.x * (256 / L);
-  const int sub = threadIdx.x % L;
-  for (long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L; row < rows; row += stride) {
-    const int which = (int)(row & 1);
-    const long long th = row >> 1;
-    const int tok = (int)(th / c.heads), head = (int)(th - (long long)tok * c.heads);
-    const int slot = slots[tok];
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && (slot >> c.page_shift) < c.num_pages) {
-      const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
-      const uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
-      uint32_t codes;
-      if (which)
-        codes = *reinterpret_cast<const uint16_t*>(rec + v_byte<D>(t, 4 * sub)) |
-                (uint32_t) * reinterpret_cast<const uint16_t*>(rec + v_byte<D>(t, 4 * sub + 2)) << 16;
-      else
-        codes = *reinterpret_cast<const uint32_t*>(rec + k_byte<D>(t, 4 * sub));
-      const uint32_t s = rec[16 * D + which * (D / 2) + t * NB + (sub >> 2)];
-      const float X = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_float(s);
-      uint32_t h[4];
-      e2m1x8_to_f16x8(codes, h[0], h[1], h[2], h[3]);
-      o.x = f32x2_to_bf16x2(f16_lo(h[0]) * X, f16_hi(h[0]) * X);
-      o.y = f32x2_to_bf16x2(f16_lo(h[1]) * X, f16_hi(h[1]) * X);
-      o.z = f32x2_to_bf16x2(f16_lo(h[2]) * X, f16_hi(h[2]) * X);
-      o.w = f32x2_to_bf16x2(f16_lo(h[3]) * X, f16_hi(h[3]) * X);
+  const long long rows = (long long)N * c.heads;
+  const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
+  const long long step = (long long)gridDim.x * (256 / L), first = (long long)blockIdx.x * (256 / L);
+  for (long long w0 = first; w0 < rows; w0 += step * kRowsInFlight) {
+    uint32_t code[kRowsInFlight][2], sb[kRowsInFlight][2];
+    bool live[kRowsInFlight];
+#pragma unroll
+    for (int i = 0; i < kRowsInFlight; ++i) {
+      const long long row = w0 + i * step + threadIdx.x / L;
+      const int tok = (int)(row / c.heads), head = (int)(row - (long long)tok * c.heads);
+      const int slot = row < rows ? slots[tok] : -1;
+      live[i] = slot >= 0 && (slot >> c.page_shift) < c.num_pages;
+      code[i][0] = code[i][1] = sb[i][0] = sb[i][1] = 0u;
+      if (live[i]) {
+        const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
+        const uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
+        code[i][0] = *reinterpret_cast<const uint32_t*>(rec + k_byte<D>(t, 4 * sub));
+        code[i][1] = *reinterpret_cast<const uint32_t*>(rec + v_byte<D>(t, 4 * t4 + 2 * (b & 1) + 16 * (b & ~1)));
+        sb[i][0] = rec[16 * D + t * NB + b];
+        sb[i][1] = rec[16 * D + D / 2 + t * NB + b];
+      }
     }
-    (which ? vo : ko)[th * L + sub] = o;
+#pragma unroll
+    for (int i = 0; i < kRowsInFlight; ++i) {
+      if (w0 + i * step >= rows) break;  // (uniform per CTA)
+      const long long row = w0 + i * step + threadIdx.x / L;
+      const uint32_t theirs = __shfl_xor_sync(0xffffffffu, code[i][1], 4);
+      // even b: lower halves of b and b + 1; odd b: upper halves of b - 1 and b
+      code[i][1] = (b & 1) ? prmt(theirs, code[i][1], 0x7632u) : prmt(code[i][1], theirs, 0x5410u);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t s = sb[i][w];
+        const float X = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_float(s);
+        uint32_t h[4];
+        e2m1x8_to_f16x8(code[i][w], h[0], h[1], h[2], h[3]);
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (live[i]) {
+          o.x = f32x2_to_bf16x2(f16_lo(h[0]) * X, f16_hi(h[0]) * X);
+          o.y = f32x2_to_bf16x2(f16_lo(h[1]) * X, f16_hi(h[1]) * X);
+          o.z = f32x2_to_bf16x2(f16_lo(h[2]) * X, f16_hi(h[2]) * X);
+          o.w = f32x2_to_bf16x2(f16_lo(h[3]) * X, f16_hi(h[3]) * X);
+        }
+        if (row < rows) __stcs((w ? vo : ko) + row * L + sub, o);
+      }
+    }
   }
 }
 
@@ -320,7 +378,7 @@ cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t
                                                4 * (3 * kMaxTableRequests + 1));
     if (e != cudaSuccess) return e;
   }
-  int grid = grid_for(a.max_tokens, 4 * kTableThreads, num_sms, 1);
+  int grid = grid_for(a.max_tokens, kTableThreads, num_sms, 1);
   if (grid < 1) grid = 1;
   page_tables_kernel<<<grid, kTableThreads, smem, s>>>(a);
   return cudaGetLastError();
@@ -328,7 +386,7 @@ cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t
 
 cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool f32, long long ks, long long vs, int N,
                              const int32_t* slots, int num_sms, cudaStream_t s) {
-  const int grid = grid_for(2ll * N * c.heads, 256 / (c.D / 8), num_sms, 8);
+  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, 4);
   if (c.D == 128) {
     if (f32) kv_append_kernel<128, true><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
     else kv_append_kernel<128, false><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
@@ -341,7 +399,7 @@ cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool
 
 cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* ko, void* vo, int num_sms,
                              cudaStream_t s) {
-  const int grid = grid_for(2ll * N * c.heads, 256 / (c.D / 8), num_sms, 8);
+  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, 4);
   if (c.D == 128)
     kv_gather_kernel<128><<<grid, 256, 0, s>>>(c, slots, N, reinterpret_cast<uint4*>(ko), reinterpret_cast<uint4*>(vo));
   else

@@ -1,10 +1,26 @@
 // Internal declarations of the 4-bit KV cache operators.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/kv_mxfp4.h"
 #include "moe_internal.h"
 
 namespace moe {
+
+// Lets ``kern`` use ``bytes`` of dynamic shared memory: asked of the runtime once
+// per device (``done``: one bit per device, a static of the caller's).
+template <typename K>
+inline cudaError_t allow_shared(K kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A record: 16 tokens of one kv head (see kv_mxfp4_cache_t for its layout).
 constexpr int kKvGroup = 16;

@@ -731,11 +731,16 @@ template <int D>
 cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t s) {
   using C = PromptCfg<D>;
   // the register split draws on what the kernel is launched with: never launch it with less
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kv_prompt_kernel<D>);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kv_prompt_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs.store(attr.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_shared(kv_prompt_kernel<D>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   kv_prompt_kernel<D><<<grid, kPromptThreads, C::kSmem, s>>>(p);
   return cudaGetLastError();

@@ -1094,7 +1094,8 @@ __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
 template <int D, int NT>
 cudaError_t launch_stream(const StreamParams& p, cudaStream_t s) {
   using C = StreamCfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kv_stream_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_shared(kv_stream_kernel<D, NT>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const int grid = p.max_ctas;
   e = launch_kernel(kv_stream_kernel<D, NT>, dim3(grid), dim3(C::kThreads), C::kSmem, s, false, false, p);

@@ -23,11 +23,26 @@ from ._native import KvAttnStruct, KvCacheStruct
 _i32 = torch.int32
 
 
+# The current stream's handle by device index; torch.cuda.current_stream() builds
+# a Stream object for it (2.9 us on the GB300's host cores, against 0.1).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _stream(stream, t):
     # a call belongs on its tensors' device: the library launches on the current one
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    i = t.get_device()
+    if i != _current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{_current_device()}")
+    return _raw_stream(i) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """An output made for the caller: from the allocator's pool of the stream it is written on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _need(t, name, dtype, shape, device):
@@ -101,18 +116,18 @@ def kv_page_tables(cached_lens, new_lens, block_table, free_ring, ring_state, pa
     if block_table.dim() != 2 or free_ring.dim() != 1:
         raise ValueError("block_table must be [R, max_blocks] and free_ring [ring size]")
     mb, C = block_table.shape[1], free_ring.shape[0]
-    new = lambda n: torch.empty(n, dtype=_i32, device=dev)  # noqa: E731
-    seq_lens = new(R) if seq_lens is None else seq_lens
-    query_start = new(R + 1) if query_start is None else query_start
-    slots = new(max_tokens) if slots is None else slots
-    positions = new(max_tokens) if positions is None else positions
-    ring_state_out = new(2) if ring_state_out is None else ring_state_out
+    seq_lens = _empty(R, _i32, dev, stream) if seq_lens is None else seq_lens
+    query_start = _empty(R + 1, _i32, dev, stream) if query_start is None else query_start
+    slots = _empty(max_tokens, _i32, dev, stream) if slots is None else slots
+    positions = _empty(max_tokens, _i32, dev, stream) if positions is None else positions
+    ring_state_out = _empty(2, _i32, dev, stream) if ring_state_out is None else ring_state_out
     for t, name, shape in ((cached_lens, "cached_lens", (R,)), (new_lens, "new_lens", (R,)),
                            (block_table, "block_table", (R, mb)), (free_ring, "free_ring", (C,)),
                            (ring_state, "ring_state", (2,)), (seq_lens, "seq_lens", (R,)),
                            (query_start, "query_start", (R + 1,)), (slots, "slots", (max_tokens,)),
                            (positions, "positions", (max_tokens,)), (ring_state_out, "ring_state_out", (2,))):
-        _need(t, name, _i32, shape, dev)
+        if t.dtype is not _i32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            _need(t, name, _i32, shape, dev)
     if ring_state_out.data_ptr() == ring_state.data_ptr():
         raise ValueError("ring_state_out must not be ring_state")
     rc = _native.load().kv_mxfp4_page_tables(
@@ -160,9 +175,9 @@ def kv_gather_mxfp4(cache: KvCacheMxfp4, slots, k_out=None, v_out=None, stream=N
     _need(slots, "slots", _i32, (N,), cache.device)
     shape = (N, cache.num_kv_heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        k_out = _empty(shape, torch.bfloat16, cache.device, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        v_out = _empty(shape, torch.bfloat16, cache.device, stream)
     _need(k_out, "k_out", torch.bfloat16, shape, cache.device)
     _need(v_out, "v_out", torch.bfloat16, shape, cache.device)
     rc = _native.load().kv_mxfp4_gather(cache._ref, slots.data_ptr(), N, k_out.data_ptr(), v_out.data_ptr(),
@@ -207,11 +222,12 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     if block_table.dim() != 2:
         raise ValueError("block_table must be [R, max_blocks]")
     mb = block_table.shape[1]
-    _need(block_table, "block_table", _i32, (R, mb), dev)
-    _need(seq_lens, "seq_lens", _i32, (R,), dev)
-    _need(query_start, "query_start", _i32, (R + 1,), dev)
+    for t, name, shape in ((block_table, "block_table", (R, mb)), (seq_lens, "seq_lens", (R,)),
+                           (query_start, "query_start", (R + 1,))):
+        if t.dtype is not _i32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            _need(t, name, _i32, shape, dev)
     if out is None:
-        out = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
@@ -220,9 +236,7 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     lib = _native.load()
     ref = ctypes.byref(a)
     if workspace is None:
-        workspace = torch.empty(max(256, lib.kv_mxfp4_attention_workspace_bytes(cache._ref, ref)), dtype=torch.uint8,
-                                device=dev)
-        workspace[:4].zero_()
+        workspace = _empty(max(256, lib.kv_mxfp4_attention_workspace_bytes(cache._ref, ref)), torch.uint8, dev, stream)
     elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     rc = lib.kv_mxfp4_attention(cache._ref, ref, q.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
