@@ -25,6 +25,8 @@
 // run through a private ring of bulk copies (one per record) without any
 // barrier with other warps.  Items cut between warps are merged in shared
 // memory, items cut between CTAs through the workspace by kv_merge_kernel.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -359,12 +361,16 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 
   // ---------------------------------------------------------------- cost and units of all requests
   const int H = a.cache.heads;
-  const int chunks = (a.R + C::kThreads - 1) / C::kThreads;
+  // Up to 32 requests every warp finds its own place, one request a lane, and the
+  // CTA does not meet before its pieces are merged; beyond, the CTA's threads scan
+  // the requests together, a chunk at a time.
+  const bool few = a.R <= 32;
+  const int chunks = few ? 1 : (a.R + C::kThreads - 1) / C::kThreads;
   long long T = 0, U = 0;          // totals so far
-  long long first_c = 0, first_u = 0;  // before request tid of the last chunk scanned
+  long long first_c = 0, first_u = 0;  // before this thread's request of the last chunk scanned
   Req mine{};
   auto scan = [&](int ch) {
-    const int r = ch * C::kThreads + tid;
+    const int r = few ? lane : ch * C::kThreads + tid;
     mine = Req{};
     if (r < a.R) mine = request<COLS>(p, r);
     const long long it = mine.items(H), c = it * (mine.ng + kItemCost), u = it * mine.ng;
@@ -377,14 +383,19 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         iu += xu;
       }
     }
+    first_c = T + ic - c;
+    first_u = U + iu - u;
+    if (few) {
+      T = __shfl_sync(0xffffffffu, ic, 31);
+      U = __shfl_sync(0xffffffffu, iu, 31);
+      return;
+    }
     __syncthreads();  // the previous chunk's sums have been read
     if (lane == 31) {
       scan_c[warp] = ic;
       scan_u[warp] = iu;
     }
     __syncthreads();
-    first_c = T + ic - c;
-    first_u = U + iu - u;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const long long xc = scan_c[w], xu = scan_u[w];
@@ -396,21 +407,28 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       U += xu;
     }
   };
+  // requests without a key: their rows are zeros, written by one CTA each
+  auto zero_rows = [&](int r) {
+    const Req q = request<COLS>(p, r);
+    const long long rows = (long long)q.ql * a.Hq;
+    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)q.qb * a.Hq * D);
+    for (long long i = tid; i < rows * (D / 8); i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (long long i = tid; i < rows; i += C::kThreads) a.lse[(size_t)q.qb * a.Hq + i] = -INFINITY;
+  };
   for (int ch = 0; ch < chunks; ++ch) {
-    if (tid == 0) n_empty = 0;
+    if (!few && tid == 0) n_empty = 0;
     scan(ch);
-    // requests without a key: their rows are zeros, written by one CTA each
-    if (mine.rt > 0 && mine.ng <= 0 && tid % gridDim.x == blockIdx.x) empties[atomicAdd(&n_empty, 1)] = ch * C::kThreads + tid;
-    __syncthreads();
-    for (int k = 0; k < n_empty; ++k) {
-      const Req q = request<COLS>(p, empties[k]);
-      const long long rows = (long long)q.ql * a.Hq;
-      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)q.qb * a.Hq * D);
-      for (long long i = tid; i < rows * (D / 8); i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (long long i = tid; i < rows; i += C::kThreads) a.lse[(size_t)q.qb * a.Hq + i] = -INFINITY;
+    const bool empty = mine.rt > 0 && mine.ng <= 0;
+    if (few) {
+      for (uint32_t m = __ballot_sync(0xffffffffu, empty && lane % gridDim.x == blockIdx.x); m; m &= m - 1)
+        zero_rows(__ffs(m) - 1);
+    } else {
+      if (empty && tid % gridDim.x == blockIdx.x) empties[atomicAdd(&n_empty, 1)] = ch * C::kThreads + tid;
+      __syncthreads();
+      for (int k = 0; k < n_empty; ++k) zero_rows(empties[k]);
+      __syncthreads();
     }
-    __syncthreads();
   }
   if (U == 0) return;
   // equal runs of cost: the first ``rem`` of A_w warps take one more; few
@@ -428,53 +446,72 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   };
   const int gw0 = blockIdx.x * wpc;
   if (gw0 >= A_w) return;
-  // thread w finds where warp w's run starts (wpc: where the last one ends)
-  for (int ch = 0; ch < chunks; ++ch) {
-    if (chunks > 1) {
-      if (ch == 0) T = U = 0;
-      scan(ch);
-    }
-    before_c[tid] = first_c;
-    before_u[tid] = first_u;
-    __syncthreads();
-    if (tid <= wpc) {
-      const long long b = min(begin_of(gw0 + tid), cost - 1);  // the end counts as after the last unit
-      const int n = min(C::kThreads, a.R - ch * C::kThreads);
-      if (b >= before_c[0] && b < T) {  // (T: the cost up to this chunk's end)
-        int lo = 0, hi = n;  // before_c[lo] <= b, the last such: requests that cost nothing share a value
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (before_c[mid] <= b) lo = mid;
-          else hi = mid;
-        }
-        const int r = ch * C::kThreads + lo;
-        const Req q = request<COLS>(p, r);
-        int x;
-        const int k = (int)divmod(b - before_c[lo], q.ng + kItemCost, x);
-        const bool end = begin_of(gw0 + tid) == cost;
-        const int gg = max(0, x - kItemCost) + (end ? 1 : 0);
-        at_r[tid] = r;
-        at_item[tid] = k;
-        at_g[tid] = gg;
-        at_unit[tid] = before_u[lo] + (long long)k * q.ng + gg;
-        at_cost[tid] = before_c[lo];
+  // where cost index b lies, counted from request r (cost fc and units fu before it);
+  // the end of everything counts as after the last unit
+  auto place = [&](long long b, int ng, long long fc, long long fu, int& item, int& unit, long long& units) {
+    int x;
+    item = (int)divmod(min(b, cost - 1) - fc, ng + kItemCost, x);
+    unit = max(0, x - kItemCost) + (b == cost ? 1 : 0);
+    units = fu + (long long)item * ng + unit;
+  };
+  int br, citem, cg;  // this warp's run: request, item within it, unit within that
+  long long ccost, u_lo, u_hi;  // cost before that request; units before the run and before its end
+  if (few) {
+    auto find = [&](long long b, int& r, int& item, int& unit, long long& fc, long long& units) {
+      // the last request that costs anything and starts at or before b
+      r = 31 - __clz(__ballot_sync(0xffffffffu, mine.items(H) > 0 && first_c <= min(b, cost - 1)));
+      fc = __shfl_sync(0xffffffffu, first_c, r);
+      place(b, __shfl_sync(0xffffffffu, mine.ng, r), fc, __shfl_sync(0xffffffffu, first_u, r), item, unit, units);
+    };
+    int xr, xi, xg;
+    long long xc;
+    find(begin_of(gw0 + min(warp, wpc)), br, citem, cg, ccost, u_lo);
+    find(begin_of(gw0 + min(warp + 1, wpc)), xr, xi, xg, xc, u_hi);
+    if (lane == 0 && warp == 0) at_unit[0] = u_lo;
+    if (lane == 0 && warp == wpc - 1) at_unit[wpc] = u_hi;
+  } else {
+    // thread w finds where warp w's run starts (wpc: where the last one ends)
+    for (int ch = 0; ch < chunks; ++ch) {
+      if (chunks > 1) {
+        if (ch == 0) T = U = 0;
+        scan(ch);
       }
+      before_c[tid] = first_c;
+      before_u[tid] = first_u;
+      __syncthreads();
+      if (tid <= wpc) {
+        const long long b = begin_of(gw0 + tid), in = min(b, cost - 1);
+        const int n = min(C::kThreads, a.R - ch * C::kThreads);
+        if (in >= before_c[0] && in < T) {  // (T: the cost up to this chunk's end)
+          int lo = 0, hi = n;  // before_c[lo] <= in, the last such: requests that cost nothing share a value
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before_c[mid] <= in) lo = mid;
+            else hi = mid;
+          }
+          at_r[tid] = ch * C::kThreads + lo;
+          at_cost[tid] = before_c[lo];
+          place(b, request<COLS>(p, at_r[tid]).ng, before_c[lo], before_u[lo], at_item[tid], at_g[tid], at_unit[tid]);
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    const int w = min(warp, wpc);
+    br = at_r[w];
+    citem = at_item[w];
+    cg = at_g[w];
+    ccost = at_cost[w];
+    u_lo = at_unit[w];
+    u_hi = at_unit[min(warp + 1, wpc)];
   }
-  const long long cta_lo = at_unit[0], cta_hi = at_unit[wpc];
 
   // ---------------------------------------------------------------- this warp's run
-  const long long u_lo = at_unit[min(warp, wpc)];
-  const int n_units = warp < wpc ? (int)(at_unit[warp + 1] - u_lo) : 0;
+  const int n_units = (int)(u_hi - u_lo);
   if (n_units > 0) {
     // record addresses, 32 units at a time, one per lane; null for a page outside the cache
-    int br = at_r[warp];
-    long long bo;  // units of request br before the next batch
-    {
-      const Req q = request<COLS>(p, br);
-      bo = (long long)at_item[warp] * q.ng + at_g[warp];
-    }
+    Req q = request<COLS>(p, br);
+    int cr = br;
+    long long bo = (long long)citem * q.ng + cg;  // units of request br before the next batch
     auto addresses = [&](int i0) -> const uint8_t* {
       const uint8_t* ptr = nullptr;
       int r = br;
@@ -521,9 +558,6 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     issue(0, S, 0);
     if (n_units > 32) nxt = addresses(32);
 
-    int cr = at_r[warp], citem = at_item[warp], cg = at_g[warp];
-    long long ccost = at_cost[warp];
-    Req q = request<COLS>(p, cr);
     bool alive = true;
     int i = 0;
     while (i < n_units && alive) {
@@ -631,10 +665,13 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       for (int nt = 0; nt < NT; ++nt) limit[nt][0] = limit[nt][1] = -INFINITY;
 
       // one softmax step over the records i .. i + ng - 1 (where ng < NG, the last
-      // one is taken again with nothing visible)
-      auto step = [&](int k, int ng) {
+      // one is taken again with nothing visible).  PLAIN: every row sees every key
+      // of NG records, factors and units are the usual ones; without the branches
+      // that look after the rest.  Returns false, with nothing done, for a plain
+      // step that meets scales of an unusual size.
+      auto step = [&](auto plain_tag, int k, int ng, uint32_t live) -> bool {
+        constexpr bool PLAIN = decltype(plain_tag)::value;
         constexpr int NG = C::kStep;
-        const uint32_t live = (here >> (i & 31)) & ((1u << ng) - 1u);  // bit r: record r exists
         float sc[NG][NT][4];
         uint32_t vsa[NG][2], vsb[NG][2];  // value scales of tokens 2t, 2t+1 (a, b), plus 8
         const uint8_t* rec[NG];
@@ -644,7 +681,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int coff = 16 * D + (lane >> 4) * (D / 2);
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
-          rec[r] = ring + ((uint32_t)(i + min(r, ng - 1)) % S) * REC;
+          rec[r] = ring + ((uint32_t)(i + (PLAIN ? r : min(r, ng - 1))) % S) * REC;
           const int valid = q.n - (j0 + 16 * r);  // tokens of the record that exist (above 16: all)
           // -------------------------------------------------- scores
 #pragma unroll
@@ -656,7 +693,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t + 8, vsa[r][1], vsb[r][1]);
           uint32_t look = scale_word<NB>(rec[r] + coff, ct);
           const bool gone = !((live >> r) & 1u);  // no record: a page outside the cache
-          if (valid < 16 || gone) {  // what lies past the end is not looked at
+          if (!PLAIN && (valid < 16 || gone)) {  // what lies past the end is not looked at
             const int v = gone ? 0 : valid;
             if (g >= v) ks0 = 0x7F7F7F7Fu;
             if (g + 8 >= v) ks1 = 0x7F7F7F7Fu;
@@ -667,7 +704,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             if (ct >= v) look = 0x7F7F7F7Fu;
           }
           ok &= usual(look);
-          if (shift != 0) {
+          if (!PLAIN && shift != 0) {
             ks0 = shifted_scales(ks0, shift);
             ks1 = shifted_scales(ks1, shift);
           }
@@ -693,8 +730,10 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
         }
         // ---------------------------------------------------- scales of an unusual size
-        bool wide = A.E != 127;
-        if (__any_sync(0xffffffffu, ok != 0x80808080u) || wide) {
+        bool wide = !PLAIN && A.E != 127;
+        const bool unusual = __any_sync(0xffffffffu, ok != 0x80808080u);
+        if (PLAIN && unusual) return false;
+        if (!PLAIN && (unusual || wide)) {
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
             const bool gone = !((live >> r) & 1u);
@@ -729,7 +768,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
         }
         // ---------------------------------------------------- masks
-        if (j0 + 16 * NG > hi_min || j0 < lo_max || live != (1u << NG) - 1u) {
+        if (!PLAIN) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -801,7 +840,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             }
           }
         // ---------------------------------------------------- weighted sum
-        if (!wide) {
+        if (PLAIN || !wide) {
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
             uint32_t vw[2][NB], vs[2][NB];  // vs: scales of tokens (2t, 2t+1) as bf16 pairs, per block
@@ -846,6 +885,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
           A = B;
         }
+        return true;
       };
 
       for (int k = 0; k < len;) {
@@ -858,7 +898,13 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             alive = mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs);
           if (!alive) break;
         }
-        step(k, ng);
+        {
+          const uint32_t live = (here >> (i & 31)) & ((1u << ng) - 1u);  // bit r: record r exists
+          const int j0 = (q.glo + g0 + k) << 4;
+          const bool plain = live == (1u << C::kStep) - 1u && j0 + 16 * C::kStep <= hi_min && j0 >= lo_max && shift == 0 &&
+                             A.E == 127;
+          if (!plain || !step(std::true_type{}, k, ng, live)) step(std::false_type{}, k, ng, live);
+        }
         // the stages are free: the records S units on
         __syncwarp();
         issue(i + S, ng, i >> 5);
@@ -940,6 +986,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     }
   }
   __syncthreads();
+
+  const long long cta_lo = at_unit[0], cta_hi = at_unit[wpc];
 
   // ---------------------------------------------------------------- pieces of one CTA
   // Lane x of every warp looks at piece x (in order of the units): consecutive
