@@ -888,28 +888,46 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         return true;
       };
 
-      for (int k = 0; k < len;) {
-        // both records of a step lie in one batch of 32 addresses
-        const int ng = C::kStep == 2 && k + 2 <= len && (i & 31) != 31 ? 2 : 1;
-        {
-          const uint32_t s0 = (uint32_t)i % S, p0 = ((uint32_t)i / S) & 1u;
-          const uint32_t s1 = (uint32_t)(i + ng - 1) % S, p1 = ((uint32_t)(i + ng - 1) / S) & 1u;
-          if (!mbar_try_wait2(&bar[s0], p0, &bar[s1], p1))
-            alive = mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs);
+      // waits for the records i .. i + n - 1 (1 or 2)
+      auto wait = [&](int n) -> bool {
+        const uint32_t s0 = (uint32_t)i % S, p0 = ((uint32_t)i / S) & 1u;
+        const uint32_t s1 = (uint32_t)(i + n - 1) % S, p1 = ((uint32_t)(i + n - 1) / S) & 1u;
+        return mbar_try_wait2(&bar[s0], p0, &bar[s1], p1) ||
+               (mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs));
+      };
+      for (int k = 0; k < len && alive;) {
+        // plain steps ahead, within this batch of 32 addresses
+        int np = 0;
+        const int j0 = (q.glo + g0 + k) << 4, in = i & 31;
+        if (shift == 0 && A.E == 127 && j0 >= lo_max) {
+          np = min(min(len - k, 32 - in), (hi_min - j0) >> 4) / C::kStep;
+          const uint32_t need = (uint32_t)((1ull << (C::kStep * max(np, 0))) - 1ull) << in;
+          if ((here & need) != need) np = 0;
+        }
+        bool usual_scales = np > 0;
+        for (; np > 0; --np) {
+          alive = wait(C::kStep);
           if (!alive) break;
+          usual_scales = step(std::true_type{}, k, C::kStep, (1u << C::kStep) - 1u);
+          if (!usual_scales) break;
+          // the stages are free: the records S units on
+          __syncwarp();
+          issue(i + S, C::kStep, i >> 5);
+          i += C::kStep;
+          k += C::kStep;
         }
-        {
-          const uint32_t live = (here >> (i & 31)) & ((1u << ng) - 1u);  // bit r: record r exists
-          const int j0 = (q.glo + g0 + k) << 4;
-          const bool plain = live == (1u << C::kStep) - 1u && j0 + 16 * C::kStep <= hi_min && j0 >= lo_max && shift == 0 &&
-                             A.E == 127;
-          if (!plain || !step(std::true_type{}, k, ng, live)) step(std::false_type{}, k, ng, live);
+        if (!alive) break;
+        if (!usual_scales) {
+          // both records of a step lie in one batch
+          const int ng = C::kStep == 2 && k + 2 <= len && (i & 31) != 31 ? 2 : 1;
+          alive = wait(ng);
+          if (!alive) break;
+          step(std::false_type{}, k, ng, (here >> (i & 31)) & ((1u << ng) - 1u));
+          __syncwarp();
+          issue(i + S, ng, i >> 5);
+          i += ng;
+          k += ng;
         }
-        // the stages are free: the records S units on
-        __syncwarp();
-        issue(i + S, ng, i >> 5);
-        i += ng;
-        k += ng;
         if ((i & 31) == 0) {
           cur = nxt;
           here = __ballot_sync(0xffffffffu, cur != nullptr);
