@@ -66,16 +66,6 @@ struct KvAttnArgs {
   uint32_t* status;
   int num_sms;
 };
-// Which kernel takes a request: the streaming one those of at most ``row_limit``
-// rows (query rows x heads per kv head), and those whose rows see at most
-// kFewKeys keys, where a row's result may hang on weights of very unlike size:
-// it holds them to 16 bits at any size, the tensor-core kernel to 11 bits above
-// 2^-25 of the row's largest.
-constexpr int kFewKeys = 256;
-__host__ __device__ inline bool kv_streamed(long long rows, int keys, int window, int row_limit) {
-  return rows <= row_limit || keys <= kFewKeys || (window > 0 && window <= kFewKeys);
-}
-
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
 // per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows
 // (tiles 1 or 2).

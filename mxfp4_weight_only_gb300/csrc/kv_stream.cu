@@ -54,10 +54,13 @@ struct StreamCfg {
   static constexpr int kSmem = kWarps * (kRingBytes + kStash);
 };
 
-// What an item costs beside its units, in units (measured: about 2 us a piece
-// next to 1.3 us a unit and warp on a busy SM).
-constexpr int kItemCost = 2;
-// Least run of a warp, in units: shorter runs only add pieces to merge.
+// What an item costs beside its units, in units.  Measured (us at 2 / 4 / 6 / 8 /
+// 16): 256 requests, 4 kv heads, up to 8192 keys 77.5 / 75.7 / 74.5 / 75.1 / 78.2;
+// 32 of them 23.6 / 22.4 / 22.0 / 21.9 / 23.3; 16 requests x 32 heads of 64, window
+// 1024 21.0 / 21.0 / 19.6 / 20.0 / 20.4.
+constexpr int kItemCost = 6;
+// Least run of a warp, in units: shorter runs only add pieces to merge (1 request
+// of 1,000 keys: 12.2 us at 2, 13.6 at 4).
 constexpr int kMinRun = 2;
 
 // A piece of an item: one warp's (shared memory) or one CTA's (workspace).
@@ -108,10 +111,9 @@ __device__ __forceinline__ Req request(const StreamParams& p, int r) {
   q.qb = min(max(a.query_start[r], 0), a.N);
   q.ql = min(min(max(a.query_start[r + 1], 0), a.N) - q.qb, a.max_q_len);
   const long long cap = (long long)a.max_blocks << a.cache.page_shift;
-  const int full = a.seq_lens[r];
-  q.n = (int)min((long long)max(full, 0), cap);
+  q.n = (int)min((long long)max(a.seq_lens[r], 0), cap);
   const long long rows = (long long)max(q.ql, 0) * p.G;
-  const bool mine = rows > 0 && (kv_streamed(rows, full, a.window, p.row_limit) || (p.odd && p.odd[r] != 0));
+  const bool mine = rows > 0 && (rows <= p.row_limit || (p.odd && p.odd[r] != 0));
   q.rt = mine ? (int)((rows + COLS - 1) / COLS) : 0;
   q.glo = a.window ? max(0, q.n - q.ql - a.window + 1) >> 4 : 0;
   q.ng = mine ? ((q.n + 15) >> 4) - q.glo : 0;
