@@ -244,6 +244,40 @@ __device__ __forceinline__ void kv_quant8(float (&v)[8], uint32_t& codes, uint32
   sbyte = nan ? 255u : s;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The same of eight bf16 values as they are, two at a time: magnitudes compare
+// as integers (NaN above infinity above all), the scaling is exact in bf16
+// (unless far below 0.25, which rounds to 0 either way).
+__device__ __forceinline__ void kv_quant8(const uint4& u, uint32_t& codes, uint32_t& sbyte) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  const uint32_t mm = max_u16x2(max_u16x2(u.x & kAbs, u.y & kAbs), max_u16x2(u.z & kAbs, u.w & kAbs));
+  uint32_t m = max(mm & 0xFFFFu, mm >> 16);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (__any_sync(0xffffffffu, m >= 0x7F80u)) {  // infinite or NaN, rare
+    float x[8] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y),
+                  bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w)};
+    kv_quant8(x, codes, sbyte);
+    return;
+  }
+  const uint32_t eb = m >> 7;
+  sbyte = eb > 2u ? eb - 2u : 0u;
+  const uint32_t rcp = (254u - sbyte) * 0x00800080u;  // 2^(127 - s), twice
+  const uint32_t a = mul_bf16x2(u.x, rcp), b = mul_bf16x2(u.y, rcp), c = mul_bf16x2(u.z, rcp), d = mul_bf16x2(u.w, rcp);
+  const float r[8] = {bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b), bf16_lo(c), bf16_hi(c), bf16_lo(d), bf16_hi(d)};
+  codes = f32x8_to_e2m1x8(r);
+}
+
 template <bool F32>
 struct Raw8;  // eight input values as loaded
 template <>
@@ -252,9 +286,8 @@ struct Raw8<false> {
   __device__ __forceinline__ void load(const void* p, long long at) {
     u = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at));
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+  __device__ __forceinline__ void quant(bool live, uint32_t& codes, uint32_t& sbyte) const {
+    kv_quant8(live ? u : make_uint4(0u, 0u, 0u, 0u), codes, sbyte);
   }
 };
 template <>
@@ -265,17 +298,44 @@ struct Raw8<true> {
     a = __ldcs(q);
     b = __ldcs(q + 1);
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  __device__ __forceinline__ void quant(bool live, uint32_t& codes, uint32_t& sbyte) const {
+    float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = live ? x[q] : 0.f;
+    kv_quant8(x, codes, sbyte);
   }
 };
 
-// Rows a thread keeps in flight: with one, the chain slot -> row -> store of each
-// row stood in the open (append and gather of 16,384 x 8 x 128: 52.9 us).
-constexpr int kRowsInFlight = 4;
+// Rows a thread keeps in flight, and CTAs per SM that the rows are dealt to:
+// enough bytes under way to cover the chain slot -> row -> store (append and
+// gather of 16,384 x 8 x 128: 2 rows, 6 / 8 / 16 CTAs 33.1 / 31.9 / 33.3 us; 4 rows,
+// 3 / 4 / 8 CTAs 34.6 / 33.3 / 34.2; 8 rows, 2 CTAs 37.4).
+constexpr int kRowsInFlight = 2, kRowCtas = 8;
+
+// A walk over rows (token, head) in steps of ``step`` rows: one division each of
+// the first row and of the step, none a row (64-bit divisions took a third of
+// the instructions of both kernels).
+struct RowWalk {
+  int tok, head, dtok, dhead, heads;
+  __device__ __forceinline__ RowWalk(long long row, long long step, int heads_) : heads(heads_) {
+    tok = (int)(row / heads);
+    head = (int)(row - (long long)tok * heads);
+    dtok = (int)(step / heads);
+    dhead = (int)(step - (long long)dtok * heads);
+  }
+  __device__ __forceinline__ void next() {
+    tok += dtok;
+    head += dhead;
+    if (head >= heads) {
+      head -= heads;
+      ++tok;
+    }
+  }
+};
 
 // Quantising write (kv_mxfp4_append).  HBM-bound: 2 or 4 bytes read and 17/32
-// byte written per value.  D / 8 lanes take a token's K and V row of one head;
+// byte written per value (16,384 x 8 x 128, written and read back: 31.9 us, 5.3
+// TB/s of the bytes that both must move).  D / 8 lanes take a token's K and V row of one head;
 // the loop bounds are uniform per warp, so every lane reaches the shuffles.
 // Neighbouring blocks' lanes trade halves of their V words, so that each writes
 // four bytes of one lane's operand.
@@ -287,21 +347,22 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const vo
   const long long rows = (long long)N * c.heads;
   const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
   const long long step = (long long)gridDim.x * (256 / L), first = (long long)blockIdx.x * (256 / L);
+  RowWalk at(first + threadIdx.x / L, step, c.heads);
   for (long long w0 = first; w0 < rows; w0 += step * kRowsInFlight) {
     Raw8<F32> raw[kRowsInFlight][2];
     int slot[kRowsInFlight], head[kRowsInFlight];
 #pragma unroll
     for (int i = 0; i < kRowsInFlight; ++i) {
-      const long long row = w0 + i * step + threadIdx.x / L;
-      const int tok = (int)(row / c.heads);
-      head[i] = (int)(row - (long long)tok * c.heads);
+      const int tok = at.tok;
+      head[i] = at.head;
       slot[i] = -1;
-      if (row < rows) {
+      if (w0 + i * step + threadIdx.x / L < rows) {
         slot[i] = slots[tok];
-        const long long at = (long long)head[i] * D + 8 * sub;
-        raw[i][0].load(k, (long long)tok * ks + at);
-        raw[i][1].load(v, (long long)tok * vs + at);
+        const int in = head[i] * D + 8 * sub;
+        raw[i][0].load(k, (long long)tok * ks + in);
+        raw[i][1].load(v, (long long)tok * vs + in);
       }
+      at.next();
     }
 #pragma unroll
     for (int i = 0; i < kRowsInFlight; ++i) {
@@ -309,16 +370,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const vo
       const bool live = slot[i] >= 0 && (slot[i] >> c.page_shift) < c.num_pages;
       uint32_t code[2], sb[2];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        float x[8];
-        if (live) {
-          raw[i][w].get(x);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) x[q] = 0.f;
-        }
-        kv_quant8(x, code[w], sb[w]);
-      }
+      for (int w = 0; w < 2; ++w) raw[i][w].quant(live, code[w], sb[w]);
       // V: lanes of blocks b and b ^ 1 hold bytes 2 t4 (lower half) and 2 t4 + 1
       // (upper) of their blocks; even b takes the lower halves of both, odd b the upper
       const uint32_t theirs = __shfl_xor_sync(0xffffffffu, code[1], 4);
@@ -342,14 +394,14 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const KvView c, const in
   const long long rows = (long long)N * c.heads;
   const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
   const long long step = (long long)gridDim.x * (256 / L), first = (long long)blockIdx.x * (256 / L);
+  RowWalk at(first + threadIdx.x / L, step, c.heads);
   for (long long w0 = first; w0 < rows; w0 += step * kRowsInFlight) {
     uint32_t code[kRowsInFlight][2], sb[kRowsInFlight][2];
     bool live[kRowsInFlight];
 #pragma unroll
     for (int i = 0; i < kRowsInFlight; ++i) {
-      const long long row = w0 + i * step + threadIdx.x / L;
-      const int tok = (int)(row / c.heads), head = (int)(row - (long long)tok * c.heads);
-      const int slot = row < rows ? slots[tok] : -1;
+      const int head = at.head, slot = w0 + i * step + threadIdx.x / L < rows ? slots[at.tok] : -1;
+      at.next();
       live[i] = slot >= 0 && (slot >> c.page_shift) < c.num_pages;
       code[i][0] = code[i][1] = sb[i][0] = sb[i][1] = 0u;
       if (live[i]) {
@@ -371,17 +423,14 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const KvView c, const in
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint32_t s = sb[i][w];
-        const float X = s == 255u ? __uint_as_float(0x7FC00000u) : e8m0_to_float(s);
-        uint32_t h[4];
+        // 2^(s-127) twice in bf16 (0: subnormal; 255: NaN); values and products are exact
+        const uint32_t x = s == 0u ? 0x00400040u : s == 255u ? 0x7FFF7FFFu : s * 0x00800080u;
+        uint32_t h[4], o[4];
         e2m1x8_to_f16x8(code[i][w], h[0], h[1], h[2], h[3]);
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (live[i]) {
-          o.x = f32x2_to_bf16x2(f16_lo(h[0]) * X, f16_hi(h[0]) * X);
-          o.y = f32x2_to_bf16x2(f16_lo(h[1]) * X, f16_hi(h[1]) * X);
-          o.z = f32x2_to_bf16x2(f16_lo(h[2]) * X, f16_hi(h[2]) * X);
-          o.w = f32x2_to_bf16x2(f16_lo(h[3]) * X, f16_hi(h[3]) * X);
-        }
-        if (row < rows) __stcs((w ? vo : ko) + row * L + sub, o);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[q] = live[i] ? mul_bf16x2(prmt(__float_as_uint(f16_lo(h[q])), __float_as_uint(f16_hi(h[q])), 0x7632u), x) : 0u;
+        if (row < rows) __stcs((w ? vo : ko) + row * L + sub, make_uint4(o[0], o[1], o[2], o[3]));
       }
     }
   }
@@ -409,7 +458,7 @@ cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t
 
 cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool f32, long long ks, long long vs, int N,
                              const int32_t* slots, int num_sms, cudaStream_t s) {
-  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, 4);
+  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, kRowCtas);
   if (c.D == 128) {
     if (f32) kv_append_kernel<128, true><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
     else kv_append_kernel<128, false><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
@@ -422,7 +471,7 @@ cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool
 
 cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* ko, void* vo, int num_sms,
                              cudaStream_t s) {
-  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, 4);
+  const int grid = grid_for((long long)N * c.heads, 256 / (c.D / 8), num_sms, kRowCtas);
   if (c.D == 128)
     kv_gather_kernel<128><<<grid, 256, 0, s>>>(c, slots, N, reinterpret_cast<uint4*>(ko), reinterpret_cast<uint4*>(vo));
   else
