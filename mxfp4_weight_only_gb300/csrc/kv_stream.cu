@@ -666,14 +666,14 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) limit[nt][0] = limit[nt][1] = -INFINITY;
 
-      // one softmax step over the records i .. i + ng - 1 (where ng < NG, the last
-      // one is taken again with nothing visible).  PLAIN: every row sees every key
-      // of NG records, factors and units are the usual ones; without the branches
-      // that look after the rest.  Returns false, with nothing done, for a plain
-      // step that meets scales of an unusual size.
-      auto step = [&](auto plain_tag, int k, int ng, uint32_t live) -> bool {
+      // one softmax step.  PLAIN: over the records i .. i + kStep - 1, every row
+      // sees every key of them, factors and units are the usual ones; without the
+      // branches that look after the rest; returns false, with nothing done, where
+      // it meets scales of an unusual size.  Else over record i, whatever it holds
+      // (``live``: it exists).
+      auto step = [&](auto plain_tag, int k, bool live) -> bool {
         constexpr bool PLAIN = decltype(plain_tag)::value;
-        constexpr int NG = C::kStep;
+        constexpr int NG = PLAIN ? C::kStep : 1;
         float sc[NG][NT][4];
         uint32_t vsa[NG][2], vsb[NG][2];  // value scales of tokens 2t, 2t+1 (a, b), plus 8
         const uint8_t* rec[NG];
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int coff = 16 * D + (lane >> 4) * (D / 2);
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
-          rec[r] = ring + ((uint32_t)(i + (PLAIN ? r : min(r, ng - 1))) % S) * REC;
+          rec[r] = ring + ((uint32_t)(i + r) % S) * REC;
           const int valid = q.n - (j0 + 16 * r);  // tokens of the record that exist (above 16: all)
           // -------------------------------------------------- scores
 #pragma unroll
@@ -694,9 +694,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t, vsa[r][0], vsb[r][0]);
           scale_word2<NB>(rec[r] + 16 * D + D / 2, 2 * t + 8, vsa[r][1], vsb[r][1]);
           uint32_t look = scale_word<NB>(rec[r] + coff, ct);
-          const bool gone = !((live >> r) & 1u);  // no record: a page outside the cache
-          if (!PLAIN && (valid < 16 || gone)) {  // what lies past the end is not looked at
-            const int v = gone ? 0 : valid;
+          if (!PLAIN && (valid < 16 || !live)) {  // what lies past the end, or outside the cache, is not looked at
+            const int v = live ? valid : 0;
             if (g >= v) ks0 = 0x7F7F7F7Fu;
             if (g + 8 >= v) ks1 = 0x7F7F7F7Fu;
             if (2 * t >= v) vsa[r][0] = 0x7F7F7F7Fu;
@@ -738,8 +737,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         if (!PLAIN && (unusual || wide)) {
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
-            const bool gone = !((live >> r) & 1u);
-            const int v = gone ? 0 : q.n - (j0 + 16 * r);
+            const int v = live ? q.n - (j0 + 16 * r) : 0;
             // NaN blocks of keys or values make their token NaN
             const uint8_t* ks = rec[r] + 16 * D;
             const float nan = __uint_as_float(0x7FC00000u);
@@ -782,7 +780,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const int j = j0 + 16 * r + g + 8 * h;
-                  if (j >= hi || j < lo || !((live >> r) & 1u)) sc[r][nt][2 * h + c] = -INFINITY;
+                  if (j >= hi || j < lo || !live) sc[r][nt][2 * h + c] = -INFINITY;
                 }
             }
         }
@@ -877,13 +875,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           Acc<D, NT> B = A;
 #pragma unroll
           for (int r = 0; r < NG; ++r) {
-            const bool gone = !((live >> r) & 1u);
             float w[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) w[nt][c] = sc[r][nt][c];
-            add_group_f32<D, NT>(B, rec[r], lane, w, gone ? 0 : q.n - (j0 + 16 * r));
+            add_group_f32<D, NT>(B, rec[r], lane, w, live ? q.n - (j0 + 16 * r) : 0);
           }
           A = B;
         }
@@ -910,7 +907,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         for (; np > 0; --np) {
           alive = wait(C::kStep);
           if (!alive) break;
-          usual_scales = step(std::true_type{}, k, C::kStep, (1u << C::kStep) - 1u);
+          usual_scales = step(std::true_type{}, k, true);
           if (!usual_scales) break;
           // the stages are free: the records S units on
           __syncwarp();
@@ -920,15 +917,13 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         }
         if (!alive) break;
         if (!usual_scales) {
-          // both records of a step lie in one batch
-          const int ng = C::kStep == 2 && k + 2 <= len && (i & 31) != 31 ? 2 : 1;
-          alive = wait(ng);
+          alive = wait(1);
           if (!alive) break;
-          step(std::false_type{}, k, ng, (here >> (i & 31)) & ((1u << ng) - 1u));
+          step(std::false_type{}, k, (here >> (i & 31)) & 1u);
           __syncwarp();
-          issue(i + S, ng, i >> 5);
-          i += ng;
-          k += ng;
+          issue(i + S, 1, i >> 5);
+          ++i;
+          ++k;
         }
         if ((i & 31) == 0) {
           cur = nxt;
