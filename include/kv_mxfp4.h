@@ -148,7 +148,10 @@ size_t kv_mxfp4_attention_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mx
  *   out          bf16 [N, Hq, head_dim] dense, 16-byte aligned
  *   lse          float32 [N, Hq] or NULL: ln sum exp S
  * A row that sees no key gets zeros (lse -inf).  Scores, softmax statistics
- * and sums are float32; scales of any size are honoured.  A token with a scale
+ * and sums are float32; scales of any size are honoured.  The weights exp(S - m)
+ * enter their product with 16 bits at any size; in requests of many rows
+ * (prompts) whose rows see more than 256 keys with 11 bits, those below about
+ * 2^-23 of the row's largest to a multiple of 2^-34 of it.  A token with a scale
  * byte 255 in its K or V row counts as NaN as a whole: rows that see it are NaN.
  * Rows outside every request are left unwritten.
  */
