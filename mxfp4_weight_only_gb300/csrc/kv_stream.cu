@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     fence_barrier_init();
     ph[2 * warp].units = ph[2 * warp + 1].units = 0;
   }
+  __syncwarp();  // other lanes arrive on the barriers: shuffles and votes order no memory
   if (tid < 2) p.heads[2 * blockIdx.x + tid].units = 0;
   grid_dep_launch_dependents();
 
