@@ -292,8 +292,8 @@ int moe_router_topk(const float* logits, int32_t T, int32_t G, int32_t topk, int
 int moe_read_status(const moe_dims_t* d, void* workspace, uint32_t* status, void* stream);
 
 /*
- * Bounded-wait hook for the next moe_a16w4_mxfp4 / moe_a16w4_int4g32 call made
- * from this host thread (then cleared).  The pages have no counterpart.
+ * Bounded-wait hook for the next moe_a16w4_mxfp4 / moe_a16w4_int4g32 /
+ * kv_mxfp4_attention call made from this host thread (then cleared).  The pages have no counterpart.
  *   limit_ns       limit of every wait inside that call's kernels, instead of
  *                  the default 2 s; a wait that runs out sets
  *                  MOE_STATUS_WAIT_TIMEOUT, the kernels stop and return, and the
@@ -301,7 +301,9 @@ int moe_read_status(const moe_dims_t* d, void* workspace, uint32_t* status, void
  *   extra_waiters  for tests of the give-up path: the fused decode kernel's
  *                  wait for all of its CTAs' gate_up results expects this many
  *                  CTAs more than it launched, so that wait runs out after
- *                  limit_ns (0..64; 0 for normal use)
+ *                  limit_ns; so do, in kv_mxfp4_attention, the waits for the
+ *                  cache's records and for the weights of a tile (0..64; 0 for
+ *                  normal use)
  * Returns MOE_ERR_BAD_DIMS for limit_ns = 0 or extra_waiters outside [0, 64].
  */
 int moe_set_wait_limit(uint64_t limit_ns, int32_t extra_waiters);

@@ -131,6 +131,7 @@ size_t kv_mxfp4_attention_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mx
 int kv_mxfp4_attention(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, const void* q, const int32_t* block_table,
                        const int32_t* seq_lens, const int32_t* query_start, void* out, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream) {
+  const WaitSettings wait = take_wait_settings();  // the hook applies to this call only
   if (!c || !a) return MOE_ERR_NULL;
   if (!cache_valid(c) || !attn_valid(c, a)) return MOE_ERR_BAD_DIMS;
   if (a->R == 0 || a->N == 0 || a->max_q_len == 0) return MOE_OK;
@@ -154,6 +155,7 @@ int kv_mxfp4_attention(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, cons
   g.workspace = reinterpret_cast<uint8_t*>(workspace);
   g.status = reinterpret_cast<uint32_t*>(workspace);
   g.num_sms = sms;
+  g.wait = wait;
   return launch_kv_attention(g, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -5,6 +5,9 @@
 
 #include "../../include/kv_mxfp4.h"
 #include "moe_internal.h"
+#ifdef __CUDACC__
+#include "common.cuh"
+#endif
 
 namespace moe {
 
@@ -21,6 +24,26 @@ inline cudaError_t allow_shared(K kern, int bytes, std::atomic<unsigned long lon
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
+
+#ifdef __CUDACC__
+// mbar_wait by a whole warp, with one result: lanes run out of time (or see the
+// abort flag) one by one, and those that went on would wait in the next
+// collective for those that left.  ``abort`` (may be null): a flag of the CTA
+// that ends a wait in progress.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* status, uint64_t limit_ns,
+                                               const volatile int* abort = nullptr) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 15u) == 15u && abort && __any_sync(0xffffffffu, *abort != 0)) return false;
+    if ((i & 255u) == 255u && __any_sync(0xffffffffu, global_ns() - t0 > limit_ns)) {
+      atomicOr(status, kStatusWaitTimeout);
+      return false;
+    }
+  }
+}
+#endif
 
 // A record: 16 tokens of one kv head (see kv_mxfp4_cache_t for its layout).
 constexpr int kKvGroup = 16;
@@ -65,6 +88,7 @@ struct KvAttnArgs {
   uint8_t* workspace;
   uint32_t* status;
   int num_sms;
+  WaitSettings wait;  // limit of every wait in the kernels
 };
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
 // per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows

@@ -356,7 +356,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         // records of this tile that exist: bit k for keys 16 k ..
         const uint32_t have = __ballot_sync(0xffffffffu, next_page >= 0 && next_page < a.cache.num_pages) & 0xFFu;
         next_page = page_of(j + 1);
-        if (*abort_flag || !mbar_wait(&s_full[x], j & 1, a.status, kWaitLimitNs)) {
+        if (!mbar_wait_warp(&s_full[x], j & 1, a.status, a.wait.limit_ns, abort_flag)) {
           *abort_flag = 1;
           ok = false;
           break;
@@ -442,7 +442,8 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
           if (move && j > 0) {
             // O, after the scores, whose registers it takes (the product before
             // these scores is done: one thread's MMAs complete in order)
-            if (!mbar_wait(&o_done[x], (j - 1) & 1, a.status, kWaitLimitNs)) {
+            if (!mbar_wait_warp(&o_done[x], (j - 1) & 1, a.status, a.wait.limit_ns)) {
+              tc_st_wait();
               *abort_flag = 1;
               ok = false;
               break;
@@ -475,7 +476,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
           l += l0 + l1;
         }
       }
-      if (ok && nt > 0 && !mbar_wait(&o_done[x], (nt - 1) & 1, a.status, kWaitLimitNs)) {
+      if (ok && nt > 0 && !mbar_wait_warp(&o_done[x], (nt - 1) & 1, a.status, a.wait.limit_ns)) {
         *abort_flag = 1;
         ok = false;
       }
@@ -535,15 +536,15 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       };
       // (every lane waits; a wait that runs out in one lane ends the loop in all)
       auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
-      bool ok = all(mbar_wait(q_full, 0, a.status, kWaitLimitNs) && mbar_wait(&k_full[0], 0, a.status, kWaitLimitNs));
+      bool ok = all(mbar_wait(q_full, 0, a.status, a.wait.limit_ns) && mbar_wait(&k_full[0], 0, a.status, a.wait.limit_ns));
       tc_after();
       if (ok) scores(0);
       for (int j = 0; j < nt && ok; ++j) {
         const int s = j % S, s1 = (j + 1) % S;
         // (A's turn j comes after B's j - 1, B's after A's j)
-        ok = all(mbar_wait(&v_full[s], (j / S) & 1, a.status, kWaitLimitNs) &&
-                 mbar_wait(&p_full[x], j & 1, a.status, kWaitLimitNs) &&
-                 (nq == 1 || (x == 0 && j == 0) || mbar_wait(&turn[x], (j - (x == 0)) & 1, a.status, kWaitLimitNs)));
+        ok = all(mbar_wait(&v_full[s], (j / S) & 1, a.status, a.wait.limit_ns) &&
+                 mbar_wait(&p_full[x], j & 1, a.status, a.wait.limit_ns) &&
+                 (nq == 1 || (x == 0 && j == 0) || mbar_wait(&turn[x], (j - (x == 0)) & 1, a.status, a.wait.limit_ns)));
         if (!ok) break;
         tc_after();
         const uint32_t vs = v_lo + s * (C::kTile >> 4);
@@ -560,7 +561,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         }
         __syncwarp();
         if (j + 1 < nt) {
-          ok = all(mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, kWaitLimitNs));
+          ok = all(mbar_wait(&k_full[s1], ((j + 1) / S) & 1, a.status, a.wait.limit_ns));
           if (!ok) break;
           tc_after();
           scores(s1);
@@ -572,7 +573,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       // all issued MMAs complete before tensor memory is released
       if (elect_one()) tc_commit(&drain[x]);
       __syncwarp();
-      mbar_wait(&drain[x], 0, a.status, kWaitLimitNs);
+      mbar_wait_warp(&drain[x], 0, a.status, a.wait.limit_ns);
     }
   } else {
     // ---------------------------------------------------------------- converters: one record of a tile per warp
@@ -644,10 +645,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
     for (int j = 0; j < nt && ok; ++j) {
       const int s = j % S;
       locate(j + 1);
-      if (*abort_flag || (j >= S && !mbar_wait(&k_empty[s], ((j / S) - 1) & 1, a.status, kWaitLimitNs))) {
-        ok = false;
-        break;
-      }
+      ok = *abort_flag == 0 && (j < S || mbar_wait(&k_empty[s], ((j / S) - 1) & 1, a.status, a.wait.limit_ns));
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int krow = cw * 16 + 8 * u + g;
@@ -666,10 +664,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[s]);
       load_k();
-      if (j >= S && !mbar_wait(&v_empty[s], ((j / S) - 1) & 1, a.status, kWaitLimitNs)) {
-        ok = false;
-        break;
-      }
+      ok = (j < S || mbar_wait(&v_empty[s], ((j / S) - 1) & 1, a.status, a.wait.limit_ns)) && ok;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -694,6 +689,10 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[s]);
       load_v();
+      // one vote a tile: a lane whose wait ran out goes on to here, so that no lane
+      // waits for it above (a vote at each wait: prompt of 8192 tokens 480 us, this
+      // 461, lanes leaving one by one, which can hang, 457)
+      ok = __all_sync(0xffffffffu, ok) != 0;
     }
     if (!ok) *abort_flag = 1;
     if (odd) p.odd[r] = 1;
@@ -722,7 +721,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     mbar_init(&sh.q_full, kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sh.s_full[x], 1);
-      mbar_init(&sh.p_full[x], 4);
+      mbar_init(&sh.p_full[x], 4 + a.wait.extra_waiters);
       mbar_init(&sh.turn[x], 1);
       mbar_init(&sh.o_done[x], 1);
       mbar_init(&sh.drain[x], 1);

@@ -40,7 +40,6 @@ namespace moe {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint64_t kKvWaitNs = kWaitLimitNs;
 
 template <int D, int NT>
 struct StreamCfg {
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   float* stash = reinterpret_cast<float*>(smem + W * C::kRingBytes + warp * C::kStash);
 
   if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&bars[warp * S + s], 1);
+    for (int s = 0; s < S; ++s) mbar_init(&bars[warp * S + s], 1 + a.wait.extra_waiters);
     fence_barrier_init();
     ph[2 * warp].units = ph[2 * warp + 1].units = 0;
   }
@@ -897,8 +896,9 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       auto wait = [&](int n) -> bool {
         const uint32_t s0 = (uint32_t)i % S, p0 = ((uint32_t)i / S) & 1u;
         const uint32_t s1 = (uint32_t)(i + n - 1) % S, p1 = ((uint32_t)(i + n - 1) / S) & 1u;
-        return mbar_try_wait2(&bar[s0], p0, &bar[s1], p1) ||
-               (mbar_wait(&bar[s0], p0, a.status, kKvWaitNs) && mbar_wait(&bar[s1], p1, a.status, kKvWaitNs));
+        return __all_sync(0xffffffffu, mbar_try_wait2(&bar[s0], p0, &bar[s1], p1)) ||
+               (mbar_wait_warp(&bar[s0], p0, a.status, a.wait.limit_ns) &&
+                mbar_wait_warp(&bar[s1], p1, a.status, a.wait.limit_ns));
       };
       for (int k = 0; k < len && alive;) {
         // plain steps ahead, within this batch of 32 addresses
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     }
     if (!alive) {
       // a copy did not arrive in time: wait (bounded) for those in flight, leave no piece
-      for (int k = i; k < min(i + S, n_units); ++k) mbar_wait(&bar[k % S], (k / S) & 1, a.status, kKvWaitNs);
+      for (int k = i; k < min(i + S, n_units); ++k) mbar_wait_warp(&bar[k % S], (k / S) & 1, a.status, a.wait.limit_ns);
       __syncwarp();
       if (lane == 0) ph[2 * warp].units = ph[2 * warp + 1].units = 0;
     }
