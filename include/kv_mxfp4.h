@@ -74,7 +74,10 @@ size_t kv_mxfp4_cache_bytes(const kv_mxfp4_cache_t* c);
  *                  tokens of refused requests and past query_start[R]
  *   positions      int32 [max_tokens]  position of each new token in its
  *                  request; -1 past query_start[R]
- *   ring_state_out int32 [2]  the ring afterwards; must not overlap ring_state
+ *   ring_state_out int32 [2]  the ring afterwards
+ * No output (block_table and free_ring among them) may share memory with another
+ * argument: MOE_ERR_OVERLAP.  So lengths are not updated in place: copy seq_lens
+ * over cached_lens after the call.
  * Everything but block_table and free_ring is written whole; with the same
  * inputs a second call writes the same again.
  */

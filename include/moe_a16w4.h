@@ -45,6 +45,7 @@ extern "C" {
 #define MOE_ERR_WORKSPACE (-5)       /* workspace smaller than moe_workspace_bytes()         */
 #define MOE_ERR_CUDA (-6)            /* a CUDA runtime call or launch failed                 */
 #define MOE_ERR_DEVICE (-7)          /* current device is not a compute capability 10.3 GPU  */
+#define MOE_ERR_OVERLAP (-8)         /* an output shares memory with another argument        */
 
 /* Device status bits (moe_read_status). */
 #define MOE_STATUS_WAIT_TIMEOUT 0x1u /* a pipeline wait in a kernel gave up; outputs invalid */

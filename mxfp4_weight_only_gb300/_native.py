@@ -16,6 +16,7 @@ ERRORS = {
     -5: "MOE_ERR_WORKSPACE",
     -6: "MOE_ERR_CUDA",
     -7: "MOE_ERR_DEVICE",
+    -8: "MOE_ERR_OVERLAP",
 }
 MOE_ACT_SWIGLU = 0
 MOE_PATH_AUTO, MOE_PATH_DECODE, MOE_PATH_PREFILL = 0, 1, 2

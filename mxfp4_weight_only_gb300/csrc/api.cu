@@ -423,6 +423,7 @@ const char* moe_error_string(int code) {
     case MOE_ERR_WORKSPACE: return "workspace smaller than moe_workspace_bytes()";
     case MOE_ERR_CUDA: return "CUDA runtime error";
     case MOE_ERR_DEVICE: return "device is not a compute capability 10.3 GPU";
+    case MOE_ERR_OVERLAP: return "an output shares memory with another argument";
     default: return "unknown error";
   }
 }

@@ -28,6 +28,12 @@ int check_device(int* num_sms) {
   return MOE_OK;
 }
 
+// Do ``na`` bytes at a and ``nb`` bytes at b share one?
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
 int shift_of(int page_size) {
   for (int s = 4; s <= 8; ++s)
     if (page_size == 1 << s) return s;
@@ -80,6 +86,20 @@ int kv_mxfp4_page_tables(int32_t R, int32_t page_size, int32_t max_blocks, int32
   const void* all[] = {cached_lens, new_lens, block_table, free_ring, ring_state, seq_lens, query_start, slots, positions, ring_state_out};
   for (const void* p : all)
     if (!aligned(p, 4)) return MOE_ERR_ALIGN;
+  // Every CTA of the launch reads the lengths and the ring's state, the block
+  // table and the ring while others write their outputs: none may share memory.
+  struct Span {
+    const void* p;
+    uint64_t bytes;
+  };
+  const uint64_t r4 = 4ull * (uint64_t)R, t4 = 4ull * (uint64_t)max_tokens;
+  const Span span[] = {{cached_lens, r4}, {new_lens, r4}, {ring_state, 8},  // read
+                       {block_table, r4 * (uint64_t)max_blocks}, {free_ring, 4ull * (uint64_t)ring_size},
+                       {seq_lens, r4}, {query_start, r4 + 4}, {slots, t4}, {positions, t4}, {ring_state_out, 8}};
+  for (int i = 3; i < 10; ++i)
+    for (int j = 0; j < i; ++j)
+      if (span[i].bytes && span[j].bytes && overlap(span[i].p, span[i].bytes, span[j].p, span[j].bytes))
+        return MOE_ERR_OVERLAP;
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
