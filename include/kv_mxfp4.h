@@ -9,7 +9,8 @@
  * Same library (libmoe_a16w4.so), same conventions as moe_a16w4.h: device
  * pointers to caller-owned memory, work enqueued on ``stream``, MOE_OK or a
  * negative MOE_ERR_* code, argument checks before any CUDA call, nothing
- * allocated, no host synchronisation.  The pages this library follows
+ * allocated, no host synchronisation.  What a call writes may not share memory
+ * with anything else that it is given (MOE_ERR_OVERLAP).  The pages this library follows
  * describe no cache; these operators have no counterpart there.
  */
 #ifndef KV_MXFP4_H
@@ -75,9 +76,8 @@ size_t kv_mxfp4_cache_bytes(const kv_mxfp4_cache_t* c);
  *   positions      int32 [max_tokens]  position of each new token in its
  *                  request; -1 past query_start[R]
  *   ring_state_out int32 [2]  the ring afterwards
- * No output (block_table and free_ring among them) may share memory with another
- * argument: MOE_ERR_OVERLAP.  So lengths are not updated in place: copy seq_lens
- * over cached_lens after the call.
+ * block_table and free_ring count as written.  Lengths are not updated in place:
+ * copy seq_lens over cached_lens after the call.
  * Everything but block_table and free_ring is written whole; with the same
  * inputs a second call writes the same again.
  */

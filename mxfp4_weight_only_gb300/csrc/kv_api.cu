@@ -34,6 +34,19 @@ bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return x < y ? y - x < na : x - y < nb;
 }
 
+struct Span {
+  const void* p;
+  uint64_t bytes;
+};
+// Does one of the spans from ``first`` on (the written ones) share memory with any span before it?
+template <int N>
+bool any_overlap(const Span (&s)[N], int first) {
+  for (int i = first; i < N; ++i)
+    for (int j = 0; j < i; ++j)
+      if (s[i].bytes && s[j].bytes && overlap(s[i].p, s[i].bytes, s[j].p, s[j].bytes)) return true;
+  return false;
+}
+
 int shift_of(int page_size) {
   for (int s = 4; s <= 8; ++s)
     if (page_size == 1 << s) return s;
@@ -88,18 +101,11 @@ int kv_mxfp4_page_tables(int32_t R, int32_t page_size, int32_t max_blocks, int32
     if (!aligned(p, 4)) return MOE_ERR_ALIGN;
   // Every CTA of the launch reads the lengths and the ring's state, the block
   // table and the ring while others write their outputs: none may share memory.
-  struct Span {
-    const void* p;
-    uint64_t bytes;
-  };
   const uint64_t r4 = 4ull * (uint64_t)R, t4 = 4ull * (uint64_t)max_tokens;
   const Span span[] = {{cached_lens, r4}, {new_lens, r4}, {ring_state, 8},  // read
                        {block_table, r4 * (uint64_t)max_blocks}, {free_ring, 4ull * (uint64_t)ring_size},
                        {seq_lens, r4}, {query_start, r4 + 4}, {slots, t4}, {positions, t4}, {ring_state_out, 8}};
-  for (int i = 3; i < 10; ++i)
-    for (int j = 0; j < i; ++j)
-      if (span[i].bytes && span[j].bytes && overlap(span[i].p, span[i].bytes, span[j].p, span[j].bytes))
-        return MOE_ERR_OVERLAP;
+  if (any_overlap(span, 3)) return MOE_ERR_OVERLAP;
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
@@ -119,6 +125,10 @@ int kv_mxfp4_append(const kv_mxfp4_cache_t* c, const void* k, const void* v, int
   if (N == 0) return MOE_OK;
   if (!c->data || !k || !v || !slots) return MOE_ERR_NULL;
   if (!aligned(c->data, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return MOE_ERR_ALIGN;
+  const uint64_t size = x_is_f32 ? 4 : 2, n1 = (uint64_t)N - 1;
+  const Span span[] = {{k, size * (n1 * (uint64_t)k_stride + (uint64_t)row)}, {v, size * (n1 * (uint64_t)v_stride + (uint64_t)row)},
+                       {slots, 4ull * (uint64_t)N}, {c->data, kv_mxfp4_cache_bytes(c)}};
+  if (any_overlap(span, 3)) return MOE_ERR_OVERLAP;
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
@@ -135,6 +145,9 @@ int kv_mxfp4_gather(const kv_mxfp4_cache_t* c, const int32_t* slots, int32_t N, 
   if (N == 0) return MOE_OK;
   if (!c->data || !slots || !k_out || !v_out) return MOE_ERR_NULL;
   if (!aligned(c->data, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 4)) return MOE_ERR_ALIGN;
+  const uint64_t rows = 2ull * (uint64_t)N * (uint64_t)c->num_kv_heads * (uint64_t)c->head_dim;
+  const Span span[] = {{slots, 4ull * (uint64_t)N}, {c->data, kv_mxfp4_cache_bytes(c)}, {k_out, rows}, {v_out, rows}};
+  if (any_overlap(span, 2)) return MOE_ERR_OVERLAP;
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
@@ -160,7 +173,15 @@ int kv_mxfp4_attention(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, cons
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(lse, 4))
     return MOE_ERR_ALIGN;
   const KvView view = view_of(c);
-  if (workspace_bytes < kv_attention_workspace(view, a)) return MOE_ERR_WORKSPACE;
+  const size_t need = kv_attention_workspace(view, a);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  // q is read again after rows of out have been written (by the streaming kernel, for marked prompts)
+  const uint64_t heads = (uint64_t)a->N * (uint64_t)a->Hq, D = (uint64_t)c->head_dim;
+  const Span span[] = {{q, 2 * ((uint64_t)(a->N - 1) * (uint64_t)a->q_stride + (uint64_t)a->Hq * D)},
+                       {block_table, 4ull * (uint64_t)a->R * (uint64_t)a->max_blocks}, {seq_lens, 4ull * (uint64_t)a->R},
+                       {query_start, 4ull * (uint64_t)a->R + 4}, {c->data, kv_mxfp4_cache_bytes(c)},
+                       {out, 2 * heads * D}, {lse, lse ? 4 * heads : 0}, {workspace, need}};
+  if (any_overlap(span, 5)) return MOE_ERR_OVERLAP;
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
