@@ -65,7 +65,8 @@ size_t kv_mxfp4_cache_bytes(const kv_mxfp4_cache_t* c);
  *   ring_state     int32 [2]  {head, free pages}
  *   seq_lens       int32 [R]  cached + new; 0 for a finished request; -1 for a
  *                  request that is refused: its tokens do not fit in
- *                  max_tokens, its pages not in its row, or the free pages do
+ *                  max_tokens, its pages not in its row, it would hold more
+ *                  than 2^31 - 1 tokens, or the free pages do
  *                  not last (pages given back in the same call are not taken;
  *                  a refused request's pages are counted for those after it
  *                  only where it was refused for want of free pages, so one
@@ -74,7 +75,7 @@ size_t kv_mxfp4_cache_bytes(const kv_mxfp4_cache_t* c);
  *   slots          int32 [max_tokens]  cache slot of each new token; -1 for
  *                  tokens of refused requests and past query_start[R]
  *   positions      int32 [max_tokens]  position of each new token in its
- *                  request; -1 past query_start[R]
+ *                  request (at most 2^31 - 1); -1 past query_start[R]
  *   ring_state_out int32 [2]  the ring afterwards
  * block_table and free_ring count as written.  Lengths are not updated in place:
  * copy seq_lens over cached_lens after the call.

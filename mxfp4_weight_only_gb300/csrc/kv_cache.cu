@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
   const int tid = threadIdx.x, R = a.R;
   if (tid == 0) taken_sum = 0;
   const int page = 1 << a.page_shift;
+  constexpr long long kMost = 0x7FFFFFFF;  // tokens of a request
   const int per = (R + kTableThreads - 1) / kTableThreads;  // consecutive requests of this thread
   const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
   const int head = ((a.state[0] % a.ring_size) + a.ring_size) % a.ring_size;
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
       const long long have = ((long long)cached[r] + page - 1) >> a.page_shift;
       const long long all = ((long long)cached[r] + max(n, 0) + page - 1) >> a.page_shift;
       if (n < 0) gone += min(have, (long long)a.max_blocks);
-      else if (t + n <= a.max_tokens && all <= a.max_blocks) need += all - have;
+      else if (t + n <= a.max_tokens && all <= a.max_blocks && (long long)cached[r] + n <= kMost) need += all - have;
       t += max(n, 0);
     }
   }
@@ -103,10 +104,11 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     if (n < 0) {
       // finished: its pages go to the ring's end, this thread's share of the
       // CTAs' work below; the offset is kept as -2 - offset
-      o = -2 - (int)gone;
+      // (within the ring's size where the requests claim more pages than it can hold)
+      o = -2 - (int)(gone >> 30 ? gone % a.ring_size : gone);
       gone += min(have, (long long)a.max_blocks);
     } else {
-      bool ok = tok + n <= a.max_tokens && all <= a.max_blocks;
+      bool ok = tok + n <= a.max_tokens && all <= a.max_blocks && (long long)cached[r] + n <= kMost;
       const long long want = ok ? all - have : 0;
       ok = ok && (want == 0 || need + want <= avail);
       if (ok) {
@@ -135,8 +137,10 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     a.state_out[1] = (int)(avail - taken_all + gone_all);
   }
 
-  const int nt = gridDim.x * kTableThreads;
-  for (int t = blockIdx.x * kTableThreads + tid; t < a.max_tokens; t += nt) {
+  const uint32_t nt = gridDim.x * kTableThreads;
+  // (unsigned: the step past the last of up to 2^31 - 1 tokens leaves an int)
+  for (uint32_t ut = blockIdx.x * kTableThreads + tid; ut < (uint32_t)a.max_tokens; ut += nt) {
+    const int t = (int)ut;
     int slot = -1, pos = -1;
     if (t < start[R]) {
       int lo = 0, hi = R;  // start[lo] <= t < start[hi]
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
         if (start[mid] <= t) lo = mid;
         else hi = mid;
       }
-      pos = cached[lo] + (t - start[lo]);
+      pos = (int)min((uint32_t)cached[lo] + (uint32_t)(t - start[lo]), (uint32_t)kMost);  // (more: refused)
       const int o = ofs[lo];
       if (o >= 0) {
         const int b = pos >> a.page_shift;

@@ -42,7 +42,7 @@ def page_tables(cached, new, table, ring, state, page, max_tokens):
                 back += 1
             continue
         every = -(-(c + n) // page)
-        ok = start[r] + n <= max_tokens and every <= mb
+        ok = start[r] + n <= max_tokens and every <= mb and c + n <= 2 ** 31 - 1
         if ok:
             need = every - have
             ok = need == 0 or claimed + need <= free
@@ -56,7 +56,7 @@ def page_tables(cached, new, table, ring, state, page, max_tokens):
             t = start[r] + i
             if t >= max_tokens:
                 break
-            positions[t] = c + i
+            positions[t] = min(c + i, 2 ** 31 - 1)
             if ok:
                 slots[t] = table[r, (c + i) // page] * page + (c + i) % page
     return seq, start, slots, positions, np.array([(head + taken) % C, free - taken + back], np.int32)
