@@ -75,6 +75,14 @@ cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool
 cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* k_out, void* v_out, int num_sms,
                              cudaStream_t s);
 
+struct KvAttnArgs;
+// A request as the attention kernels take it: its rows that are written (those
+// in q, at most max_q_len), its keys, and the position of its first row, which
+// its true number of rows gives.
+struct KvRequest {
+  int qb, ql, n, first;
+};
+
 struct KvAttnArgs {
   KvView cache;
   int R, N, Hq, max_blocks, max_q_len;
@@ -90,6 +98,16 @@ struct KvAttnArgs {
   int num_sms;
   WaitSettings wait;  // limit of every wait in the kernels
 };
+__device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
+  KvRequest q;
+  const int end = a.query_start[r + 1];
+  q.qb = min(max(a.query_start[r], 0), a.N);
+  q.ql = min(min(max(end, 0), a.N) - q.qb, a.max_q_len);
+  q.n = (int)min((long long)max(a.seq_lens[r], 0), (long long)a.max_blocks << a.cache.page_shift);
+  q.first = q.n - (max(end, q.qb) - q.qb);
+  return q;
+}
+
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
 // per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows
 // (tiles 1 or 2).

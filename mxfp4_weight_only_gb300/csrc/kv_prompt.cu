@@ -281,11 +281,10 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   volatile int* abort_flag = &sh.abort_flag;
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int qb = min(max(a.query_start[r], 0), a.N);
-  const int ql = min(min(max(a.query_start[r + 1], 0), a.N) - qb, a.max_q_len);
+  const KvRequest rq = kv_request(a, r);
+  const int qb = rq.qb, ql = rq.ql, n = rq.n;
   const int rows = min(ql * p.G - row0, 256);  // rows of this CTA
-  const int n = (int)min((long long)max(a.seq_lens[r], 0), (long long)a.max_blocks << a.cache.page_shift);
-  const int first_pos = n - ql + row0 / p.G, last_pos = n - ql + (row0 + rows - 1) / p.G;
+  const int first_pos = rq.first + row0 / p.G, last_pos = rq.first + (row0 + rows - 1) / p.G;
   const int key_hi = a.causal ? min(n, last_pos + 1) : n;
   const int key_lo = a.window ? max(0, first_pos - a.window + 1) : 0;
   const int t0 = key_lo / kKeys, nt = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - t0 : 0;
@@ -337,7 +336,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
-    const int pos = n - ql + i;
+    const int pos = rq.first + i;
     const int hi = a.causal ? min(n, pos + 1) : n;           // keys [lo, hi) are seen
     const int lo = a.window ? max(0, pos - a.window + 1) : 0;
     const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + C::kSCol + 128 * x;

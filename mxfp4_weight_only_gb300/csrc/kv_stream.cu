@@ -91,8 +91,8 @@ struct StreamParams {
 };
 
 // What a request asks for: rows, the record range any of its rows can see.
-struct Req {
-  int qb, ql, n, glo, ng, rt;
+struct Req : KvRequest {
+  int glo, ng, rt;
   __device__ __forceinline__ int items(int heads) const { return ng > 0 ? heads * rt : 0; }
 };
 
@@ -112,15 +112,13 @@ template <int COLS>
 __device__ __forceinline__ Req request(const StreamParams& p, int r) {
   const KvAttnArgs& a = p.a;
   Req q;
-  q.qb = min(max(a.query_start[r], 0), a.N);
-  q.ql = min(min(max(a.query_start[r + 1], 0), a.N) - q.qb, a.max_q_len);
-  const long long cap = (long long)a.max_blocks << a.cache.page_shift;
-  q.n = (int)min((long long)max(a.seq_lens[r], 0), cap);
+  static_cast<KvRequest&>(q) = kv_request(a, r);
   const long long rows = (long long)max(q.ql, 0) * p.G;
   const bool mine = rows > 0 && (rows <= p.row_limit || (p.odd && p.odd[r] != 0));
   q.rt = mine ? (int)((rows + COLS - 1) / COLS) : 0;
-  q.glo = a.window ? max(0, q.n - q.ql - a.window + 1) >> 4 : 0;
-  q.ng = mine ? ((q.n + 15) >> 4) - q.glo : 0;
+  q.glo = a.window ? max(0, q.first - a.window + 1) >> 4 : 0;
+  const int hi = a.causal ? min(q.n, max(0, q.first + q.ql)) : q.n;  // keys past the last row's are not looked at
+  q.ng = mine ? ((hi + 15) >> 4) - q.glo : 0;
   return q;
 }
 
@@ -641,7 +639,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       }
       // keys [lo, hi) that row c of the request sees (rows past the last: all)
       auto sees = [&](int c, int& lo, int& hi) {
-        const int pos = q.n - q.ql + c / p.G;
+        const int pos = q.first + c / p.G;
         const bool real = c < q.ql * p.G;
         hi = real && a.causal ? min(q.n, pos + 1) : q.n;
         lo = real && a.window ? max(0, pos - a.window + 1) : 0;
