@@ -108,6 +108,11 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   return q;
 }
 
+// First key that a row at ``pos`` sees (no sum leaves an int, whatever the window).
+__device__ __forceinline__ int kv_first_key(int pos, int window) {
+  return window && pos >= window ? pos - window + 1 : 0;
+}
+
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
 // per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows
 // (tiles 1 or 2).

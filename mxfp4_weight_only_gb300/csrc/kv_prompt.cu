@@ -286,7 +286,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   const int rows = min(ql * p.G - row0, 256);  // rows of this CTA
   const int first_pos = rq.first + row0 / p.G, last_pos = rq.first + (row0 + rows - 1) / p.G;
   const int key_hi = a.causal ? min(n, last_pos + 1) : n;
-  const int key_lo = a.window ? max(0, first_pos - a.window + 1) : 0;
+  const int key_lo = kv_first_key(first_pos, a.window);
   const int t0 = key_lo / kKeys, nt = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - t0 : 0;
   const int nq = rows > 128 ? 2 : 1;
   const int32_t* table = a.table + (size_t)r * a.max_blocks;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
     }
     const int pos = rq.first + i;
     const int hi = a.causal ? min(n, pos + 1) : n;           // keys [lo, hi) are seen
-    const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+    const int lo = kv_first_key(pos, a.window);
     const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + C::kSCol + 128 * x;
     const uint32_t tO = tmem + ((uint32_t)(32 * quad) << 16) + C::kOCol + 128 * x;
     float m = -INFINITY, mf = 0.f, l = 0.f;  // reference of the scores, times f; sum of weights (2^kWeightExp times)

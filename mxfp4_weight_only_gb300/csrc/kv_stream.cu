@@ -116,7 +116,7 @@ __device__ __forceinline__ Req request(const StreamParams& p, int r) {
   const long long rows = (long long)max(q.ql, 0) * p.G;
   const bool mine = rows > 0 && (rows <= p.row_limit || (p.odd && p.odd[r] != 0));
   q.rt = mine ? (int)((rows + COLS - 1) / COLS) : 0;
-  q.glo = a.window ? max(0, q.first - a.window + 1) >> 4 : 0;
+  q.glo = kv_first_key(q.first, a.window) >> 4;
   const int hi = a.causal ? min(q.n, max(0, q.first + q.ql)) : q.n;  // keys past the last row's are not looked at
   q.ng = mine ? ((hi + 15) >> 4) - q.glo : 0;
   return q;
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int pos = q.first + c / p.G;
         const bool real = c < q.ql * p.G;
         hi = real && a.causal ? min(q.n, pos + 1) : q.n;
-        lo = real && a.window ? max(0, pos - a.window + 1) : 0;
+        lo = real ? kv_first_key(pos, a.window) : 0;
       };
       int lo_max = 0, hi_min = q.n;  // over the tile's rows: the last sees the latest first key, the first the fewest
       {

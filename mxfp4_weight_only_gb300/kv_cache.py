@@ -233,7 +233,8 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
-    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, window, st[0] if N > 1 else Hq * D,
+    # (a window past the C ABI's int hides nothing: no request has that many keys)
+    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, min(window, 2 ** 31 - 1), st[0] if N > 1 else Hq * D,
                      D ** -0.5 if scale is None else scale)
     lib = _native.load()
     ref = ctypes.byref(a)
