@@ -153,9 +153,9 @@ size_t kv_mxfp4_attention_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mx
  *   lse          float32 [N, Hq] or NULL: ln sum exp S
  * A row that sees no key gets zeros (lse -inf).  Scores, softmax statistics
  * and sums are float32; scales of any size are honoured.  The weights exp(S - m)
- * enter their product with 16 bits at any size; in requests of many rows
- * (prompts) whose rows see more than 256 keys with 11 bits, those below about
- * 2^-23 of the row's largest to a multiple of 2^-34 of it.  A token with a scale
+ * enter their product with 16 bits at any size; those of a row that sees more
+ * than 256 positions, in a request of many rows (a prompt), may have 11 bits, below
+ * 2^-23 of the row's largest multiples of 2^-33 of it.  A token with a scale
  * byte 255 in its K or V row counts as NaN as a whole: rows that see it are NaN.
  * Rows outside every request are left unwritten.
  */

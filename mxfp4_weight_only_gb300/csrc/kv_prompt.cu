@@ -21,7 +21,8 @@
 // request with any other scale byte (NaN among them) is marked and done again by
 // the streaming kernel, which runs next.  Queries enter as f16 times a power of two
 // per row (exact: 8 significant bits), weights as f16 of p 2^9 (11 bits down to
-// p = 2^-23 of the reference).
+// p = 2^-23 of the reference, multiples of 2^-33 below), in items with few keys
+// as two bf16 (kFewKeys).
 // While one tile's softmax runs, the tensor core works on the other tile.  Each
 // query tile has an issuing thread of its own: a thread that issues MMAs keeps
 // only a short queue, so its barrier probes and commits (about 100 cycles each)
@@ -47,8 +48,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // row's reference moves (at most 2^15 in f16), which rescales O.
 constexpr float kSlack = 6.f, kWeightExp = 9.f;
 // Where a row sees few keys, all with a value may weigh next to nothing beside
-// one without: in requests whose rows see at most this many, weights enter as the
-// sum of two bf16 (16 bits at any size, as in the streaming kernel) and V as bf16,
+// one without: in items with a row that sees at most this many (its first row
+// sees the fewest: short requests and windows, the start of a prompt), weights
+// enter as the sum of two bf16 (16 bits at any size, as in the streaming kernel) and V as bf16,
 // in two products.  (64 query and 8 kv heads, 256 keys: 32 requests of 64 tokens 70
 // us, with one f16 weight 64, in the streaming kernel 225; 16 of 256 tokens 115,
 // 105 and 524.)
@@ -754,7 +756,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         item[0] = r;
         item[1] = (int)(off % H);
         item[2] = qt * 256;
-        item[3] = min(a.seq_lens[r], a.window ? a.window : a.seq_lens[r]) <= kFewKeys;
+        const KvRequest rq = kv_request(a, r);
+        const int seen = a.causal ? min(rq.n, rq.first + item[2] / p.G + 1) : rq.n;
+        item[3] = min(seen, a.window ? a.window : seen) <= kFewKeys;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
       if (before > (long long)blockIdx.x) break;
