@@ -108,6 +108,40 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   return q;
 }
 
+// Queries as f16 times a power of two a row (and kv head): the largest magnitude
+// goes into [2^14, 2^15), so elements down to 2^-31 of it keep their 8 significant
+// bits.  Those below lose some, the less the smaller they are: ``rest`` is the sum
+// of what a row's elements lose, in units of 2^e.  A key of scale byte s moves its
+// score (units of log2, factor fs = |scale| log2 e) by at most
+// fs 2^e rest 6 2^(s - 127), which stays below 2^-16 for s up to kv_key_top();
+// larger keys are multiplied in float32 (streaming kernel) or mark the request
+// (tensor-core kernel).  An element below 2^-31 of a row's largest is rare, and its
+// keys' limit lies high: queries of size 1, 128 wide: s = 146, keys of 2^19.
+constexpr int kQueryExp = 14;
+struct KvQueryRange {  // of some of a row's elements
+  uint32_t largest = 0u, least = 0xFFFFFFFFu;  // magnitudes as bits, two at a time; ``least`` minus 1, zeros left out
+  __device__ __forceinline__ void add(uint32_t w) {
+    const uint32_t x = w & 0x7FFF7FFFu;
+    uint32_t y;
+    asm("max.u16x2 %0, %0, %1;" : "+r"(largest) : "r"(x));
+    asm("add.u16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xFFFFFFFFu));
+    asm("min.u16x2 %0, %0, %1;" : "+r"(least) : "r"(y));
+  }
+  __device__ __forceinline__ uint32_t most() const { return max(largest & 0xFFFFu, largest >> 16); }
+  // does an element lose bits beside a largest of ``m`` (bits)?
+  __device__ __forceinline__ bool loses(uint32_t m) const {
+    const uint32_t l = min(least & 0xFFFFu, least >> 16) + 1u;
+    return m < 0x7F80u && (m >> 7) > 17u + kQueryExp && l < ((m >> 7) - 17u - kQueryExp) << 7;
+  }
+};
+// the row's e from its largest magnitude's bits
+__device__ __forceinline__ int kv_query_exp(uint32_t m) { return m > 0u && m < 0x7F80u ? (int)(m >> 7) - 127 - kQueryExp : 0; }
+__device__ __forceinline__ int kv_exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255u) - 127; }
+__device__ __forceinline__ int kv_key_top(float rest, float fs, int e) {
+  // (mantissas of rest and fs below 2 each, 6 < 8: five powers of two)
+  return rest > 0.f ? 127 - 16 - 5 - (kv_exponent(rest) + kv_exponent(fs) + e) : 255;
+}
+
 // First key that a row at ``pos`` sees (no sum leaves an int, whatever the window).
 __device__ __forceinline__ int kv_first_key(int pos, int window) {
   return window && pos >= window ? pos - window + 1 : 0;

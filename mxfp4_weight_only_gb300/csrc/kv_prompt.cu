@@ -20,7 +20,8 @@
 // K-major and V as the MN-major operand, both with the 128-byte swizzle.  A
 // request with any other scale byte (NaN among them) is marked and done again by
 // the streaming kernel, which runs next.  Queries enter as f16 times a power of two
-// per row (exact: 8 significant bits), weights as f16 of p 2^9 (11 bits down to
+// per row (exact down to 2^-31 of the row's largest; a row with smaller ones that
+// could tell marks its request: see kQueryExp), weights as f16 of p 2^9 (11 bits down to
 // p = 2^-23 of the reference, multiples of 2^-33 below), in items with few keys
 // as two bf16 (kFewKeys).
 // While one tile's softmax runs, the tensor core works on the other tile.  Each
@@ -55,6 +56,7 @@ constexpr float kSlack = 6.f, kWeightExp = 9.f;
 // us, with one f16 weight 64, in the streaming kernel 225; 16 of 256 tokens 115,
 // 105 and 524.)
 constexpr int kFewKeys = 256;
+constexpr int kTopScale = 140;  // the largest scale byte that f16 operands hold
 
 template <int D>
 struct PromptCfg {
@@ -303,25 +305,35 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
     const int i = row / p.G, hq = kvh * p.G + row - i * p.G;
     float f = 1.f;
     {
-      // the row's query, f16 times a power of two that puts its largest magnitude in [8, 16)
+      // the row's query, f16 times a power of two
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(qb + i) * a.q_stride + (size_t)hq * D);
       uint4 u[D / 8];
-      float mx = 0.f;
+      KvQueryRange range;
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) u[c] = real ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+        for (int k = 0; k < 4; ++k) range.add(w[k]);
       }
-      const int e = mx > 0.f && mx < INFINITY ? (int)(__float_as_uint(mx) >> 23) - 127 - 3 : 0;
-      f = mul_pow2(fabsf(a.scale) * kLog2e, e);
+      const int e = kv_query_exp(range.most());
+      const float fs = fabsf(a.scale) * kLog2e;
+      f = mul_pow2(fs, e);
       // 2^-e in two factors (either alone may leave the range); none where the scores are all 0
       float e0 = exp2_int((-e) >> 1), e1 = exp2_int(-e - ((-e) >> 1));
       if (f == 0.f) {
         f = 1.f;
         e0 = 0.f;
+      }
+      if (range.loses(range.most())) {  // rare
+        float rest = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          const float v = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + c) << 16) * e0 * e1;
+          rest += fabsf(v - f16_lo(f32x2_to_f16x2(v, 0.f)));
+        }
+        if (kv_key_top(rest, fs, e) < kTopScale) p.odd[r] = 1;
       }
       const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
       uint8_t* dst = smem + x * C::kQBytes + trow * 128;

@@ -15,8 +15,8 @@
 //                                     folded into the weights, per 32 dims
 // The record is laid out so that every lane finds its operands of these MMAs in
 // two 16-byte words of keys and two of values (conflict-free shared loads, no
-// shuffles).  Queries enter as f16 scaled by a power of two per row (exact: 8
-// significant bits), keys as f16 (exact).  Weights enter as the sum of two bf16
+// shuffles).  Queries enter as f16 scaled by a power of two per row (exact down to
+// 2^-31 of the row's largest; see kQueryExp), keys as f16 (exact).  Weights enter as the sum of two bf16
 // (16 bits, two MMAs: the tensor pipe has room), which keeps a weight of any
 // size where the heavier keys' values are zero (one f16 weight, 11 bits, loses
 // those below 2^-32; one bf16 weight has 8 bits).  Value scales outside
@@ -312,6 +312,45 @@ __device__ __noinline__ void add_group_f32(Acc<D, NT>& A, const uint8_t* rec, in
   }
 }
 
+// The scores of one record in float32 from the queries themselves, in the units of
+// the MMAs' (times 2^(shift - e) of each row): for rows whose elements f16 cannot
+// hold beside keys large enough to tell.  Lane (g, t): tokens g, g + 8, rows 2t,
+// 2t + 1 of each tile.
+template <int D, int NT>
+__device__ __noinline__ void scores_f32(const KvAttnArgs& a, const uint8_t* rec, int lane, int qb, int rows, int col0, int kvh,
+                                        int G, int shift, float (&sc)[NT][4]) {
+  constexpr int NB = D / 32;
+  const int g = lane >> 2, t = lane & 3;
+  for (int i = 0; i < 2 * NT; ++i) {
+    const int c = col0 + (i >> 1) * 8 + 2 * t + (i & 1);
+    float s[2] = {0.f, 0.f};
+    if (c < rows) {
+      const int row = c / G;
+      const uint16_t* q = a.q + (size_t)(qb + row) * a.q_stride + (size_t)(kvh * G + c - row * G) * D;
+      KvQueryRange range;
+      for (int k = 0; k < D / 2; ++k) range.add(__ldg(reinterpret_cast<const uint32_t*>(q) + k));
+      const int e = kv_query_exp(range.most());
+      for (int b = 0; b < NB; ++b) {
+        float d[2] = {0.f, 0.f};  // times 2^-8: sums of 32 products stay below 2^128
+        for (int k = 0; k < 16; ++k) {  // two elements: row byte 16 b + k
+          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + 16 * b + k);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[4];
+            e2m1x8_to_f16x8(rec[(((h * 8 + g) * 4 + (k >> 2)) * NB + b) * 4 + (k & 3)], x[0], x[1], x[2], x[3]);
+            d[h] = fmaf(bf16_lo(w) * 0x1p-8f, f16_lo(x[0]), d[h]);
+            d[h] = fmaf(bf16_hi(w) * 0x1p-8f, f16_hi(x[0]), d[h]);
+          }
+        }
+        for (int h = 0; h < 2; ++h)
+          s[h] += mul_pow2(d[h], (int)rec[16 * D + (8 * h + g) * NB + b] - 127 + shift - e + 8);
+      }
+    }
+    const bool neg = a.scale < 0.f;
+    sc[i >> 1][i & 1] = neg ? -s[0] : s[0];
+    sc[i >> 1][2 + (i & 1)] = neg ? -s[1] : s[1];
+  }
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -580,14 +619,15 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       uint32_t qf[NT][NB][4];
       float f[NT][2];
       int shift = 0;
+      int key_top = 255;  // the largest scale byte of keys that the queries' f16 will do for
       {
         const int rows = q.ql * p.G;
-        float fcol[NT];
-        int fe = -127;
+        const float fs = fabsf(a.scale) * kLog2e;
+        int e[NT], fe = -1000;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int c = rt * COLS + nt * 8 + g;
-          float mx = 0.f;
+          KvQueryRange range;
           uint4 u[NB];
 #pragma unroll
           for (int b = 0; b < NB; ++b) u[b] = make_uint4(0, 0, 0, 0);
@@ -601,36 +641,54 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           for (int b = 0; b < NB; ++b) {
             const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+            for (int k = 0; k < 4; ++k) range.add(w[k]);
           }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // largest magnitude into [8, 16)
-          const int e = mx > 0.f && mx < INFINITY ? (int)(__float_as_uint(mx) >> 23) - 127 - 3 : 0;
+          uint32_t most = range.most();
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          e[nt] = kv_query_exp(most);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              qf[nt][b][k] = f32x2_to_f16x2(mul_pow2(bf16_lo(w[k]), -e), mul_pow2(bf16_hi(w[k]), -e)) ^
-                             (a.scale < 0.f ? 0x80008000u : 0u);
+              qf[nt][b][k] = f32x2_to_f16x2(mul_pow2(bf16_lo(w[k]), -e[nt]), mul_pow2(bf16_hi(w[k]), -e[nt]));
+          }
+          if (__any_sync(0xffffffffu, range.loses(most))) {  // rare
+            float rest = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                rest += fabsf(mul_pow2(bf16_lo(w[k]), -e[nt]) - f16_lo(qf[nt][b][k])) +
+                        fabsf(mul_pow2(bf16_hi(w[k]), -e[nt]) - f16_hi(qf[nt][b][k]));
+            }
+            rest += __shfl_xor_sync(0xffffffffu, rest, 1);
+            rest += __shfl_xor_sync(0xffffffffu, rest, 2);
+            key_top = min(key_top, __reduce_min_sync(0xffffffffu, kv_key_top(rest, fs, e[nt])));
           }
           // (a negative scale's sign goes into the queries: factors are positive)
-          fcol[nt] = mul_pow2(fabsf(a.scale) * kLog2e, e);
-          if (fcol[nt] == 0.f) {  // scores of 0: by the queries, so that hidden keys stay at -inf
-            fcol[nt] = 1.f;
+          if (a.scale < 0.f) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b) qf[nt][b][0] = qf[nt][b][1] = qf[nt][b][2] = qf[nt][b][3] = 0u;
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) qf[nt][b][k] ^= 0x80008000u;
           }
-          if (c < rows) fe = max(fe, (int)((__float_as_uint(fcol[nt]) >> 23) & 255u) - 127);
+          if (c < rows) fe = max(fe, kv_exponent(fs) + e[nt]);
         }
         // factors of an unusual size go into the key scales, so that partial sums
         // stay near the scores' size
         fe = __reduce_max_sync(0xffffffffu, fe);
-        shift = fe > 40 || fe < -40 ? min(max(fe, -126), 126) : 0;
+        shift = fs > 0.f && (fe > 40 - kQueryExp || fe < -40 - kQueryExp) ? min(max(fe, -126), 126) : 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float v = mul_pow2(fcol[nt], -shift);
+          float v = mul_pow2(fs, e[nt] - shift);
+          if (v == 0.f) {  // scores of 0: by the queries, so that hidden keys stay at -inf
+            v = 1.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qf[nt][b][0] = qf[nt][b][1] = qf[nt][b][2] = qf[nt][b][3] = 0u;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             f[nt][k] = __shfl_sync(0xffffffffu, v, 4 * (2 * t + k));
@@ -651,6 +709,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         sees(rt * COLS, x, hi_min);
       }
 
+      // plain steps look for key scale bytes above key_top too: 191 after this
+      const uint32_t key_add = lane < 16 && key_top < 191 ? (uint32_t)(191 - max(key_top, 127)) * 0x01010101u : 0u;
       Acc<D, NT> A;
       A.E = 127;
 #pragma unroll
@@ -707,7 +767,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             if (2 * t + 9 >= v) vsb[r][1] = 0x7F7F7F7Fu;
             if (ct >= v) look = 0x7F7F7F7Fu;
           }
-          ok &= usual(look);
+          // (from 127 on, key_top adds 64 at most: what passes 255 lands below 64)
+          ok &= usual(PLAIN ? look + key_add : look);
           if (!PLAIN && shift != 0) {
             ks0 = shifted_scales(ks0, shift);
             ks1 = shifted_scales(ks1, shift);
@@ -731,6 +792,19 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
               sc[r][nt][2] = fmaf(d[2], s1, sc[r][nt][2]);
               sc[r][nt][3] = fmaf(d[3], s1, sc[r][nt][3]);
             }
+          }
+        }
+        if (!PLAIN && key_top < 255) {
+          const int v = live ? q.n - j0 : 0;
+          const int top = max(g < v ? largest_scale(scale_word<NB>(rec[0] + 16 * D, g)) : 0,
+                              g + 8 < v ? largest_scale(scale_word<NB>(rec[0] + 16 * D, g + 8)) : 0);
+          if (__reduce_max_sync(0xffffffffu, top) > key_top) {
+            float s[NT][4];
+            scores_f32<D, NT>(a, rec[0], lane, q.qb, q.ql * p.G, rt * COLS, kvh, p.G, shift, s);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sc[0][nt][c] = s[nt][c];
           }
         }
         // ---------------------------------------------------- scales of an unusual size
@@ -902,7 +976,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         // plain steps ahead, within this batch of 32 addresses
         int np = 0;
         const int j0 = (q.glo + g0 + k) << 4, in = i & 31;
-        if (shift == 0 && A.E == 127 && j0 >= lo_max) {
+        if (shift == 0 && A.E == 127 && key_top >= 127 && j0 >= lo_max) {
           np = min(min(len - k, 32 - in), (hi_min - j0) >> 4) / C::kStep;
           const uint32_t need = (uint32_t)((1ull << (C::kStep * max(np, 0))) - 1ull) << in;
           if ((here & need) != need) np = 0;
