@@ -134,8 +134,12 @@ struct KvQueryRange {  // of some of a row's elements
     return m < 0x7F80u && (m >> 7) > 17u + kQueryExp && l < ((m >> 7) - 17u - kQueryExp) << 7;
   }
 };
+// A row with an infinite or NaN element has no finite softmax over any key:
+// infinite scores of one sign would pass for hidden keys, so all of its f16
+// elements become NaN (and with them the scores of the keys that it sees).
+__device__ __forceinline__ bool kv_query_finite(uint32_t m) { return m < 0x7F80u; }
 // the row's e from its largest magnitude's bits
-__device__ __forceinline__ int kv_query_exp(uint32_t m) { return m > 0u && m < 0x7F80u ? (int)(m >> 7) - 127 - kQueryExp : 0; }
+__device__ __forceinline__ int kv_query_exp(uint32_t m) { return m > 0u && kv_query_finite(m) ? (int)(m >> 7) - 127 - kQueryExp : 0; }
 __device__ __forceinline__ int kv_exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255u) - 127; }
 __device__ __forceinline__ int kv_key_top(float rest, float fs, int e) {
   // (mantissas of rest and fs below 2 each, 6 < 8: five powers of two)

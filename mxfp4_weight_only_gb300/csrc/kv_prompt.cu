@@ -335,6 +335,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         }
         if (kv_key_top(rest, fs, e) < kTopScale) p.odd[r] = 1;
       }
+      if (!kv_query_finite(range.most())) e0 = __uint_as_float(0x7FC00000u);
       const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
       uint8_t* dst = smem + x * C::kQBytes + trow * 128;
 #pragma unroll

@@ -330,6 +330,7 @@ __device__ __noinline__ void scores_f32(const KvAttnArgs& a, const uint8_t* rec,
       KvQueryRange range;
       for (int k = 0; k < D / 2; ++k) range.add(__ldg(reinterpret_cast<const uint32_t*>(q) + k));
       const int e = kv_query_exp(range.most());
+      if (!kv_query_finite(range.most())) s[0] = s[1] = __uint_as_float(0x7FC00000u);
       for (int b = 0; b < NB; ++b) {
         float d[2] = {0.f, 0.f};  // times 2^-8: sums of 32 products stay below 2^128
         for (int k = 0; k < 16; ++k) {  // two elements: row byte 16 b + k
@@ -624,6 +625,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int rows = q.ql * p.G;
         const float fs = fabsf(a.scale) * kLog2e;
         int e[NT], fe = -1000;
+        bool bad[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int c = rt * COLS + nt * 8 + g;
@@ -668,6 +670,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             rest += __shfl_xor_sync(0xffffffffu, rest, 2);
             key_top = min(key_top, __reduce_min_sync(0xffffffffu, kv_key_top(rest, fs, e[nt])));
           }
+          bad[nt] = !kv_query_finite(most);
           // (a negative scale's sign goes into the queries: factors are positive)
           if (a.scale < 0.f) {
 #pragma unroll
@@ -688,6 +691,10 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             v = 1.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) qf[nt][b][0] = qf[nt][b][1] = qf[nt][b][2] = qf[nt][b][3] = 0u;
+          }
+          if (bad[nt]) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) qf[nt][b][0] = qf[nt][b][1] = qf[nt][b][2] = qf[nt][b][3] = 0x7FFF7FFFu;
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
