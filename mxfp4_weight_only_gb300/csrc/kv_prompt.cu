@@ -18,7 +18,8 @@
 // block's 2^(s-127), exact for scale bytes 104 .. 140 (and 0, blocks below
 // 2^-124, as zeros); K rows and V rows go to shared memory as they are, K as the
 // K-major and V as the MN-major operand, both with the 128-byte swizzle.  A
-// request with any other scale byte (NaN among them) is marked and done again by
+// request with any other scale byte (NaN among them), or with scores from kFarScore
+// on, is marked and done again by
 // the streaming kernel, which runs next.  Queries enter as f16 times a power of two
 // per row (exact down to 2^-31 of the row's largest; a row with smaller ones that
 // could tell marks its request: see kQueryExp), weights as f16 of p 2^9 (11 bits down to
@@ -56,6 +57,10 @@ constexpr float kSlack = 6.f, kWeightExp = 9.f;
 // us, with one f16 weight 64, in the streaming kernel 225; 16 of 256 tokens 115,
 // 105 and 524.)
 constexpr int kFewKeys = 256;
+// A weight is off by up to a unit in the last place of its row's reference
+// (products S f unrounded, the reference and its sum with kWeightExp rounded): from
+// here on by more than f16 has room for above 2^(kSlack + kWeightExp).
+constexpr float kFarScore = 0x1p22f;
 constexpr int kTopScale = 140;  // the largest scale byte that f16 operands hold
 
 template <int D>
@@ -320,6 +325,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       const int e = kv_query_exp(range.most());
       const float fs = fabsf(a.scale) * kLog2e;
       f = mul_pow2(fs, e);
+      if (!(f < 0x1p100f)) p.odd[r] = 1;  // (f itself may have overflowed)
       // 2^-e in two factors (either alone may leave the range); none where the scores are all 0
       float e0 = exp2_int((-e) >> 1), e1 = exp2_int(-e - ((-e) >> 1));
       if (f == 0.f) {
@@ -418,7 +424,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
           al = m == -INFINITY ? 0.f : ex2(mf - mf1);
           m = mx;
           mf = mf1;
-          l *= al;
+          l = fabsf(mf1) < kFarScore ? l * al : __uint_as_float(0x7FC00000u);
         }
         {
           const uint64_t f2 = pack2(f, f), off2 = pack2(kWeightExp - mf, kWeightExp - mf);
@@ -495,6 +501,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         ok = false;
       }
       if (ok) {
+        if (l != l) p.odd[r] = 1;  // beyond kFarScore on the way (or NaN)
         tc_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(qb + i) * a.Hq + hq;

@@ -58,6 +58,15 @@ struct StreamCfg {
   static constexpr int kSmem = kWarps * (kRingBytes + kStash);
 };
 
+// Weights are 2^(S f - m f) with the product S f unrounded and m f rounded, so the
+// largest is 2^r with r up to half a unit in the last place of m f: 2^4 at this
+// size.  Beyond, both products are rounded (largest weight 1), and taken by a
+// quarter: units of log2 would leave float32 before the scores do.
+constexpr float kFar = 0x1p28f;
+// Plain steps take shifts of the key scales up to this either way: bytes of 64 ..
+// 191 stay within 1 .. 254.
+constexpr int kPlainShift = 56;
+
 // What an item costs beside its units, in units.  Measured (us at 2 / 4 / 6 / 8 /
 // 16): 256 requests, 4 kv heads, up to 8192 keys 77.5 / 75.7 / 74.5 / 75.1 / 78.2;
 // 32 of them 23.6 / 22.4 / 22.0 / 21.9 / 23.3; 16 requests x 32 heads of 64, window
@@ -172,6 +181,9 @@ __device__ __forceinline__ float lg2(float v) {
   return r;
 }
 
+// A score (or reference) v times its factor f, in units of 4 log2.
+__device__ __forceinline__ float quarter(float v, float f) { return __fmul_rn(v, 0.25f * f); }
+
 // 2^e for any e: two factors, so that results below the normal range and up to 2^254 apart work out.
 __device__ __forceinline__ float mul_pow2(float v, int e) {
   const int c = min(max(e, -252), 252), h = c >> 1;
@@ -229,7 +241,7 @@ __device__ __forceinline__ void e8m0x4_to_bf16x4(uint32_t w, uint32_t& lo, uint3
 // Top bit of a byte set where the byte lies in 64 .. 191 (its two top bits differ).
 __device__ __forceinline__ uint32_t usual(uint32_t w) { return w ^ (w << 1); }
 
-// Key scale bytes plus ``shift`` (255 stays), within 0 .. 254: for factors of an unusual size.
+// Key scale bytes plus ``shift`` (255 stays), within 0 .. 254: for factors beyond kPlainShift.
 __device__ __noinline__ uint32_t shifted_scales(uint32_t w, int shift) {
   uint32_t r = 0;
   for (int b = 0; b < 4; ++b) {
@@ -370,9 +382,9 @@ __device__ __forceinline__ void store4(const KvAttnArgs& a, size_t row, int d, c
   *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
 }
 
-// lse from the sum of weights and their reference m (units of log2).
+// lse from the sum of weights and their reference m (units of 4 log2).
 __device__ __forceinline__ void store_lse(const KvAttnArgs& a, size_t row, float l, float m) {
-  if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m == -INFINITY ? l : (m + lg2(l)) * 0.6931471805599453f;
+  if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m == -INFINITY ? l : fmaf(m, 2.772588722239781f, lg2(l) * 0.6931471805599453f);
 }
 
 template <int D, int NT>
@@ -620,7 +632,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       uint32_t qf[NT][NB][4];
       float f[NT][2];
       int shift = 0;
-      int key_top = 255;  // the largest scale byte of keys that the queries' f16 will do for
+      // the largest scale byte of keys that the queries' f16 will do for, and plain steps
+      int key_top = 255, plain_top;
       {
         const int rows = q.ql * p.G;
         const float fs = fabsf(a.scale) * kLog2e;
@@ -680,10 +693,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
           if (c < rows) fe = max(fe, kv_exponent(fs) + e[nt]);
         }
-        // factors of an unusual size go into the key scales, so that partial sums
-        // stay near the scores' size
+        // the largest factor's power of two goes into the key scales, so that partial sums
+        // stay near the scores' size (a quarter of it, in units of log2)
         fe = __reduce_max_sync(0xffffffffu, fe);
-        shift = fs > 0.f && (fe > 40 - kQueryExp || fe < -40 - kQueryExp) ? min(max(fe, -126), 126) : 0;
+        shift = fs > 0.f ? min(max(fe - 2, -126), 126) : 0;
+        // keys up to this byte leave scores (f 2^(kQueryExp + 1) 6 D 2^(s - 127) at most) below kFar
+        plain_top = min(key_top, 127 + 28 - (kQueryExp + 1) - 3 - 7 - (fe + 1));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float v = mul_pow2(fs, e[nt] - shift);
@@ -716,8 +731,9 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         sees(rt * COLS, x, hi_min);
       }
 
-      // plain steps look for key scale bytes above key_top too: 191 after this
-      const uint32_t key_add = lane < 16 && key_top < 191 ? (uint32_t)(191 - max(key_top, 127)) * 0x01010101u : 0u;
+      // plain steps look for key scale bytes above plain_top too: 191 after this
+      const uint32_t key_add = lane < 16 && plain_top < 191 ? (uint32_t)(191 - max(plain_top, 127)) * 0x01010101u : 0u;
+      const bool plain = plain_top >= 127 && shift >= -kPlainShift && shift <= kPlainShift;
       Acc<D, NT> A;
       A.E = 127;
 #pragma unroll
@@ -731,6 +747,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         A.mf[nt][0] = A.mf[nt][1] = 0.f;
       }
 
+      bool far = false;  // a reference beyond kFar
       // a score above its limit moves the reference: 8 above it in units of log2
       float limit[NT][2];
 #pragma unroll
@@ -739,7 +756,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       // one softmax step.  PLAIN: over the records i .. i + kStep - 1, every row
       // sees every key of them, factors and units are the usual ones; without the
       // branches that look after the rest; returns false, with nothing done, where
-      // it meets scales of an unusual size.  Else over record i, whatever it holds
+      // it meets scales of an unusual size (those that could lead beyond kFar among
+      // them).  Else over record i, whatever it holds
       // (``live``: it exists).
       auto step = [&](auto plain_tag, int k, bool live) -> bool {
         constexpr bool PLAIN = decltype(plain_tag)::value;
@@ -774,11 +792,17 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             if (2 * t + 9 >= v) vsb[r][1] = 0x7F7F7F7Fu;
             if (ct >= v) look = 0x7F7F7F7Fu;
           }
-          // (from 127 on, key_top adds 64 at most: what passes 255 lands below 64)
+          // (from 127 on, plain_top adds 64 at most: what passes 255 lands below 64)
           ok &= usual(PLAIN ? look + key_add : look);
-          if (!PLAIN && shift != 0) {
+          float unit = 1.f;  // what the scales as float32 still need
+          if (PLAIN) {  // (bytes of 64 .. 191: none carries)
+            ks0 += (uint32_t)(shift * 0x01010101);
+            ks1 += (uint32_t)(shift * 0x01010101);
+          } else if (shift < -kPlainShift || shift > kPlainShift) {
             ks0 = shifted_scales(ks0, shift);
             ks1 = shifted_scales(ks1, shift);
+          } else {
+            unit = exp2_int(shift);
           }
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -786,8 +810,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             e2m1x8_to_f16x8(kw[0][b], x[0], x[1], x[2], x[3]);
             e2m1x8_to_f16x8(kw[1][b], y[0], y[1], y[2], y[3]);
             // byte -> 2^(s-127): 0 gives 0 (for 2^-127); 255 is seen to below
-            const float s0 = __uint_as_float((b < 3 ? ks0 << (23 - 8 * b) : ks0 >> 1) & 0x7F800000u);
-            const float s1 = __uint_as_float((b < 3 ? ks1 << (23 - 8 * b) : ks1 >> 1) & 0x7F800000u);
+            float s0 = __uint_as_float((b < 3 ? ks0 << (23 - 8 * b) : ks0 >> 1) & 0x7F800000u);
+            float s1 = __uint_as_float((b < 3 ? ks1 << (23 - 8 * b) : ks1 >> 1) & 0x7F800000u);
+            if (!PLAIN) {  // (finite, so that products of 0 stay 0)
+              s0 = fminf(s0 * unit, 3.402823466e38f);
+              s1 = fminf(s1 * unit, 3.402823466e38f);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
@@ -886,6 +914,17 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             grow |= v > limit[nt][c];
           }
         if (__any_sync(0xffffffffu, grow)) {
+          if (!PLAIN) {
+            bool beyond = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float m1 = fmaxf(A.m[nt][c], mn[nt][c]);
+                beyond |= m1 != -INFINITY && fabsf(m1 * f[nt][c]) > kFar;
+              }
+            far |= (bool)__any_sync(0xffffffffu, beyond);
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float al[2];
@@ -893,6 +932,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             for (int c = 0; c < 2; ++c) {
               const float m1 = fmaxf(A.m[nt][c], mn[nt][c]), mf1 = m1 == -INFINITY ? 0.f : m1 * f[nt][c];
               al[c] = A.m[nt][c] == -INFINITY ? 0.f : ex2(A.mf[nt][c] - mf1);
+              if (!PLAIN && far && al[c] != 0.f) al[c] = ex2(4.f * __fsub_rn(quarter(A.m[nt][c], f[nt][c]), quarter(m1, f[nt][c])));
               A.l[nt][c] *= al[c];
               A.m[nt][c] = m1;
               A.mf[nt][c] = mf1;
@@ -911,7 +951,9 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              sc[r][nt][c] = ex2(fmaf(sc[r][nt][c], f[nt][c & 1], -A.mf[nt][c & 1]));
+              const float s = sc[r][nt][c], ff = f[nt][c & 1], m = A.m[nt][c & 1];
+              sc[r][nt][c] = ex2(!PLAIN && far ? 4.f * __fsub_rn(quarter(s, ff), m == -INFINITY ? 0.f : quarter(m, ff))
+                                               : fmaf(s, ff, -A.mf[nt][c & 1]));
               A.l[nt][c & 1] += sc[r][nt][c];
             }
 #pragma unroll
@@ -983,7 +1025,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         // plain steps ahead, within this batch of 32 addresses
         int np = 0;
         const int j0 = (q.glo + g0 + k) << 4, in = i & 31;
-        if (shift == 0 && A.E == 127 && key_top >= 127 && j0 >= lo_max) {
+        if (plain && A.E == 127 && !far && j0 >= lo_max) {
           np = min(min(len - k, 32 - in), (hi_min - j0) >> 4) / C::kStep;
           const uint32_t need = (uint32_t)((1ull << (C::kStep * max(np, 0))) - 1ull) << in;
           if ((here & need) != need) np = 0;
@@ -1029,12 +1071,12 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           l += __shfl_xor_sync(0xffffffffu, l, 16);
           A.l[nt][c] = l;
         }
-      // from here on m is in units of log2
+      // from here on m is in units of 4 log2
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (A.m[nt][c] != -INFINITY) A.m[nt][c] = A.mf[nt][c];
+          if (A.m[nt][c] != -INFINITY) A.m[nt][c] = quarter(A.m[nt][c], f[nt][c]);
       if (g0 == 0 && len == q.ng) {
         const int rows = q.ql * p.G;
 #pragma unroll
@@ -1129,7 +1171,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
     for (uint32_t x = run; x; x &= x - 1) {
       const int y = __ffs(x) - 1;
       const float* pc = floats(y);
-      const float w = ex2(pc[COLS * (D + 4) + col] - mb);
+      const float w = ex2(4.f * (pc[COLS * (D + 4) + col] - mb));
       l = fmaf(pc[COLS * (D + 4) + COLS + col], w, l);
       const int de = ph[y].E - E;
 #pragma unroll
@@ -1208,7 +1250,7 @@ __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
 #pragma unroll 4
   for (int c = c0 + team; c <= c1; c += kTeams) {
     const float* pc = p.parts + slot_of(c) * part_floats(COLS, D);
-    const float w = ex2(pc[COLS * D + col] - mb);
+    const float w = ex2(4.f * (pc[COLS * D + col] - mb));
     l = fmaf(pc[COLS * D + COLS + col], w, l);
     const float4 v = *reinterpret_cast<const float4*>(pc + col * D + 4 * x);
     const int de = p.heads[slot_of(c)].E - E;
