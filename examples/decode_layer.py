@@ -97,7 +97,8 @@ class Server:
         hidden = x + attn.view(N, L.heads * L.head_dim) @ L.wo.T
         ids, weights = m.moe_router_topk((hidden @ L.router.T).float(), L.topk)
         moe = m.moe_a16w4_mxfp4(hidden, ids, weights, L.w13, L.s13, L.w2, L.s2)
-        self.lens.copy_(tables.seq_lens)
+        # a refused request (-1) keeps its length and pages: the caller gives its tokens again
+        self.lens.copy_(torch.where(tables.seq_lens < 0, self.lens, tables.seq_lens))
         self.ring_state.copy_(tables.ring_state)
         return hidden + moe, StepTrace(tables, k, v, q, attn, hidden, ids, weights, moe)
 

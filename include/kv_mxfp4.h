@@ -78,7 +78,7 @@ size_t kv_mxfp4_cache_bytes(const kv_mxfp4_cache_t* c);
  *                  request (at most 2^31 - 1); -1 past query_start[R]
  *   ring_state_out int32 [2]  the ring afterwards
  * block_table and free_ring count as written.  Lengths are not updated in place:
- * copy seq_lens over cached_lens after the call.
+ * copy seq_lens over cached_lens after the call, but for -1.
  * Everything but block_table and free_ring is written whole; with the same
  * inputs a second call writes the same again.
  */

@@ -112,7 +112,7 @@ def kv_page_tables(cached_lens, new_lens, block_table, free_ring, ring_state, pa
     ``query_start`` [R+1], ``slots`` and ``positions`` [max_tokens] (-1 padding)
     and the ring's new state; pass that state into the next step.  Outputs may not
     share memory with one another or with an input (``seq_lens`` is not
-    ``cached_lens``: copy it over them after the call)."""
+    ``cached_lens``: copy it over them after the call, but for -1)."""
     dev = _cuda(cached_lens, "cached_lens")
     R = cached_lens.shape[0]
     if block_table.dim() != 2 or free_ring.dim() != 1:
