@@ -77,6 +77,12 @@ class Server:
         self.free_ring = torch.arange(pages, **i32)
         self.ring_state = torch.tensor([0, pages], **i32)
         self.lens = torch.zeros(requests, **i32)
+        self.workspace = torch.zeros(0, dtype=torch.uint8, device="cuda")
+
+    def check(self):
+        """Raises if a wait of an attention since the last check ran out (its outputs are invalid)."""
+        if self.workspace.numel() and m.attention_read_status(self.workspace):
+            raise RuntimeError("an attention kernel gave up waiting")
 
     def rotary(self, x, positions):
         angle = positions.clamp(min=0).float()[:, None, None] * self.layer.freq
@@ -93,7 +99,12 @@ class Server:
         q, k = turned[:, :L.heads], turned[:, L.heads:]
         v = qkv[:, L.heads + L.kv_heads:]
         m.kv_append_mxfp4(self.cache, k, v, tables.slots)
-        attn = m.attention_kv_mxfp4(q, self.cache, self.block_table, tables.seq_lens, tables.query_start, max_q_len)
+        need = m.attention_workspace_bytes(self.cache, len(self.lens), N, L.heads, self.block_table.shape[1], max_q_len)
+        if self.workspace.numel() < need:
+            self.check()
+            self.workspace = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        attn = m.attention_kv_mxfp4(q, self.cache, self.block_table, tables.seq_lens, tables.query_start, max_q_len,
+                                    workspace=self.workspace)
         hidden = x + attn.view(N, L.heads * L.head_dim) @ L.wo.T
         ids, weights = m.moe_router_topk((hidden @ L.router.T).float(), L.topk)
         moe = m.moe_a16w4_mxfp4(hidden, ids, weights, L.w13, L.s13, L.w2, L.s2)
@@ -139,6 +150,7 @@ def main():
     end.record()
     end.synchronize()
     ms = begin.elapsed_time(end) / args.new
+    server.check()
     lens = server.lens.cpu()
     assert (lens == args.prompt + args.new + 1).all(), lens
     assert torch.isfinite(state.float()).all()

@@ -206,7 +206,9 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     sits at position seq_len - q + i; ``window``: only the last ``window`` keys.
     ``lse`` float32 [N, Hq], when given, receives ln sum exp of the scores.  A row
     without a visible key gets zeros (lse -inf).  Pass ``workspace`` (uint8,
-    ``attention_workspace_bytes``, first 4 bytes zeroed once) to allocate nothing."""
+    ``attention_workspace_bytes``, first 4 bytes zeroed once) to allocate nothing,
+    and to learn of waits that ran out (``attention_read_status``): those of a
+    workspace made here go unseen."""
     dev = cache.device
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
