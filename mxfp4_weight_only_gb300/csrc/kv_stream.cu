@@ -868,7 +868,11 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
             int mx = max(max(largest_scale(vsa[r][0]), largest_scale(vsb[r][0])),
                          max(largest_scale(vsa[r][1]), largest_scale(vsb[r][1])));
             mx = __reduce_max_sync(0xffffffffu, mx);
-            if (wide && mx > A.E + 60) {  // sums of values this large would overflow in the present unit
+            // sums (weights up to 2^8, values below 8 2^(mx - 127), q.n keys) have to
+            // stay below 2^128 in units of 2^(E - 127); no larger a unit than that, as
+            // other blocks and keys may be small
+            mx += 11 + 32 - __clz(q.n) - 128;
+            if (wide && mx > A.E) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
