@@ -48,8 +48,8 @@ __device__ __forceinline__ void block_exclusive2(long long& a, long long& b, lon
 }
 
 // Page tables and slot maps (kv_mxfp4_page_tables).  Latency-bound: a few KB
-// of lengths in, 8 bytes per new token out (8 requests 3.8 us, 1,000 with 36,000
-// new tokens 6.9).  Every CTA redoes the two prefix
+// of lengths in, 8 bytes per new token out (8 requests 3.9 us, 1,000 with 36,000
+// new tokens 7.1).  Every CTA redoes the two prefix
 // sums over the requests (tokens, then pages) in shared memory, so one launch
 // needs no grid-wide step; the CTAs then share the tokens and the finished
 // requests.  A token whose position starts a page that its request does not
@@ -339,7 +339,7 @@ struct RowWalk {
 };
 
 // Quantising write (kv_mxfp4_append).  HBM-bound: 2 or 4 bytes read and 17/32
-// byte written per value (16,384 x 8 x 128, written and read back: 31.9 us, 5.3
+// byte written per value (16,384 x 8 x 128, written and read back: 31.4 us, 5.4
 // TB/s of the bytes that both must move).  D / 8 lanes take a token's K and V row of one head;
 // the loop bounds are uniform per warp, so every lane reaches the shuffles.
 // Neighbouring blocks' lanes trade halves of their V words, so that each writes

@@ -1,7 +1,7 @@
 // Attention over the 4-bit KV cache, many query rows per request (prompts):
 // tcgen05 MMAs (kv_mxfp4_attention).
 //
-// Measured: a prompt of 8192 tokens, 28 / 4 heads of 128: 457 us, 1052 TFLOP/s (54 %
+// Measured: a prompt of 8192 tokens, 28 / 4 heads of 128: 459 us, 1048 TFLOP/s (54 %
 // of the library's bf16 matrix product): a tile's chain scores - softmax - product
 // is longer than the MMAs of the other tile beside it.
 //

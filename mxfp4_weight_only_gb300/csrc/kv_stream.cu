@@ -2,9 +2,9 @@
 // streamed once (kv_mxfp4_attention, decode and short drafts).
 //
 // Measured: 256 requests of up to 8192 keys, 28 / 4 heads of 128: 73 us, 3.8 TB/s
-// (56 % of the copy rate), bound by the issue of the exact conversions (60 % of
-// the slots, 53 % of the ALU pipe); 2 requests of 262,139 keys, 32 / 2 heads: 62 us;
-// one of 1,000 keys: 11.8 us, latency.
+// (56 % of the copy rate), bound by the issue of the exact conversions (61 % of
+// the slots, 54 % of the ALU pipe); 2 requests of 262,139 keys, 32 / 2 heads: 62 us;
+// one of 1,000 keys: 12.3 us, latency.
 //
 // One pass with a running maximum and sum per query row.  A warp takes 16-token
 // records of one (request, kv head, row tile of 8 NT rows) one after another:
