@@ -154,12 +154,12 @@ size_t kv_mxfp4_attention_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mx
  * A row that sees no key gets zeros (lse -inf).  Scores, softmax statistics
  * and sums are float32; scales of any size are honoured.  Elements of q below 2^-31
  * of their row's largest may lose bits, where that moves no score by more than
- * 2^-16 (units of log2).  The weights exp(S - m)
- * enter their product with 16 bits down to 2^-126; those of a row that sees more
- * than 256 positions, in a request of many rows (a prompt), may have 11 bits, below
- * 2^-23 of the row's largest multiples of 2^-33 of it.  A token with a scale
- * byte 255 in its K or V row counts as NaN as a whole: rows that see it are NaN.
- * So are rows of q with an infinite or NaN element that see a key.
+ * 2^-16 (units of log2).  The weights exp(S - m) enter their product with 16 bits
+ * down to 2^-126; those of a row that sees more than 256 positions, in a request of
+ * many rows (a prompt), may have 11 bits, below 2^-23 of the row's largest multiples
+ * of 2^-33 of it.  A token with a scale byte 255 in its K or V row counts as NaN as a
+ * whole: rows that see it are NaN.  So are rows of q with an infinite or NaN element
+ * that see a key.
  * Rows outside every request are left unwritten.
  */
 int kv_mxfp4_attention(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, const void* q, const int32_t* block_table,

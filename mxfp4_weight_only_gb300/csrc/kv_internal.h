@@ -134,6 +134,9 @@ struct KvQueryRange {  // of some of a row's elements
     return m < 0x7F80u && (m >> 7) > 17u + kQueryExp && l < ((m >> 7) - 17u - kQueryExp) << 7;
   }
 };
+// What a row that loses bits loses at least: elements below 2^-149 in units of 2^e
+// are gone from its float32 differences too, 128 of them less than this.
+constexpr float kQueryRest = 0x1p-120f;
 // A row with an infinite or NaN element has no finite softmax over any key:
 // infinite scores of one sign would pass for hidden keys, so all of its f16
 // elements become NaN (and with them the scores of the keys that it sees).

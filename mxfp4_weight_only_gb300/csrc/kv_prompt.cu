@@ -19,12 +19,11 @@
 // 2^-124, as zeros); K rows and V rows go to shared memory as they are, K as the
 // K-major and V as the MN-major operand, both with the 128-byte swizzle.  A
 // request with any other scale byte (NaN among them), or with scores from kFarScore
-// on, is marked and done again by
-// the streaming kernel, which runs next.  Queries enter as f16 times a power of two
-// per row (exact down to 2^-31 of the row's largest; a row with smaller ones that
-// could tell marks its request: see kQueryExp), weights as f16 of p 2^9 (11 bits down to
-// p = 2^-23 of the reference, multiples of 2^-33 below), in items with few keys
-// as two bf16 (kFewKeys).
+// on, is marked and done again by the streaming kernel, which runs next.  Queries
+// enter as f16 times a power of two per row (exact down to 2^-31 of the row's
+// largest; a row with smaller ones that could tell marks its request: see
+// kQueryExp), weights as f16 of p 2^9 (11 bits down to p = 2^-23 of the reference,
+// multiples of 2^-33 below), in items with few keys as two bf16 (kFewKeys).
 // While one tile's softmax runs, the tensor core works on the other tile.  Each
 // query tile has an issuing thread of its own: a thread that issues MMAs keeps
 // only a short queue, so its barrier probes and commits (about 100 cycles each)
@@ -333,7 +332,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         e0 = 0.f;
       }
       if (range.loses(range.most())) {  // rare
-        float rest = 0.f;
+        float rest = kQueryRest;
 #pragma unroll 1
         for (int c = 0; c < D; ++c) {
           const float v = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + c) << 16) * e0 * e1;

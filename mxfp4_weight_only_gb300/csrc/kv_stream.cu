@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
               qf[nt][b][k] = f32x2_to_f16x2(mul_pow2(bf16_lo(w[k]), -e[nt]), mul_pow2(bf16_hi(w[k]), -e[nt]));
           }
           if (__any_sync(0xffffffffu, range.loses(most))) {  // rare
-            float rest = 0.f;
+            float rest = range.loses(most) ? kQueryRest : 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               const uint32_t w[4] = {u[b].x, u[b].y, u[b].z, u[b].w};

@@ -106,3 +106,15 @@ def test_zero_scale_and_zero_rows(m, kind):  # noqa: F811
     p["q"][::2] = 0
     out, lse = run(m, p, -0.3)
     compare(p, out, lse, -0.3)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("large,small,keys,scale", [(120, -128, 250, 0.5), (110, -40, 163, 0.5), (60, -126, 252, 2.0)])
+def test_elements_that_vanish_beside_the_largest(m, kind, large, small, keys, scale):  # noqa: F811
+    # more than 2^149 below it: nothing is left of them in float32 after the row's power of two either
+    p = problem(**kind, seed=11, bands=((keys, keys), (120, 127)))
+    p["q"] = (p["q"].double() * 2.0 ** small).to(torch.bfloat16)
+    p["q"][:, :, 5] = 2.0 ** large
+    key_codes(p, 5, 0)
+    out, lse = run(m, p, scale)
+    compare(p, out, lse, scale)
