@@ -1,4 +1,5 @@
-"""ctypes view of ``libmoe_a16w4.so`` (declarations of include/moe_a16w4.h and include/kv_mxfp4.h)."""
+"""ctypes view of ``libmoe_a16w4.so`` (declarations of include/moe_a16w4.h, include/kv_mxfp4.h and
+include/block_mxfp4.h)."""
 
 from __future__ import annotations
 
@@ -54,8 +55,21 @@ class KvAttnStruct(ctypes.Structure):
                 ("window", _i32), ("q_stride", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
+class LinearStruct(ctypes.Structure):
+    _fields_ = [("T", _i32), ("K", _i32), ("N", _i32), ("act", _i32), ("out_is_f32", _i32), ("x_stride", ctypes.c_int64),
+                ("res_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class KvRopeStruct(ctypes.Structure):
+    _fields_ = [("N", _i32), ("Hq", _i32), ("x_is_f32", _i32), ("rotary_dim", _i32), ("interleaved", _i32),
+                ("max_positions", _i32), ("position_offset", _i32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
 _CacheP = ctypes.POINTER(KvCacheStruct)
 _AttnP = ctypes.POINTER(KvAttnStruct)
+_LinearP = ctypes.POINTER(LinearStruct)
+_RopeP = ctypes.POINTER(KvRopeStruct)
 
 SIGNATURES = {
     "moe_workspace_bytes": (ctypes.c_size_t, [_DimsP]),
@@ -86,6 +100,10 @@ SIGNATURES = {
     "kv_mxfp4_attention_workspace_bytes": (ctypes.c_size_t, [_CacheP, _AttnP]),
     "kv_mxfp4_attention": (ctypes.c_int, [_CacheP, _AttnP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "kv_mxfp4_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
+    "linear_mxfp4_workspace_bytes": (ctypes.c_size_t, [_LinearP]),
+    "linear_a16w4_mxfp4": (ctypes.c_int, [_LinearP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "linear_mxfp4_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
+    "kv_mxfp4_append_rope": (ctypes.c_int, [_CacheP, _RopeP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_abi_version": (ctypes.c_int, []),
 }

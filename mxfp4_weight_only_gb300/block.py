@@ -1,0 +1,158 @@
+"""Python binding of the attention block's operators (include/block_mxfp4.h).
+
+As the cache's binding: tensors are checked, outputs and the workspace are made
+with PyTorch when the caller passes none, and the C ABI is called with raw
+device pointers on the current CUDA stream of the tensors' device.  Everything
+is computed in the library's kernels.
+
+One layer's attention block: ``linear_a16w4_mxfp4`` (queries, keys and values) ->
+``kv_append_rope_mxfp4`` (rotated, keys and values quantised to their slots) ->
+``attention_kv_mxfp4`` -> ``linear_a16w4_mxfp4`` (output, added to the residual
+stream).
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _native
+from ._native import KvRopeStruct, LinearStruct
+from .kv_cache import KvCacheMxfp4, _empty, _need, _rows, _stream
+
+_ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
+
+
+def linear_workspace_bytes(T: int, N: int, K: int) -> int:
+    """Bytes of workspace for ``linear_a16w4_mxfp4`` calls of these sizes."""
+    d = LinearStruct(T, K, N, 0, 0, -(-K // 8) * 8, N, N)
+    return int(_native.load().linear_mxfp4_workspace_bytes(ctypes.byref(d)))
+
+
+def _matrix(t, name, dtypes, shape, device):
+    """Checks a matrix of dense rows; returns the rows' stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    st = t.stride()
+    if shape[1] > 1 and st[1] != 1:
+        raise ValueError(f"{name}: rows must be dense")
+    return st[0] if shape[0] > 1 else shape[1]
+
+
+def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=None, out_dtype=torch.bfloat16,
+                       workspace=None, stream=None):
+    """``act(x @ W.T + bias) + residual`` on an MXFP4 weight, float32 sums, rounded once.
+
+    ``x`` bf16 [T, K] (rows may be strided by a multiple of 8 elements), ``w`` uint8
+    [N, K / 2] (packed E2M1), ``w_scale`` uint8 [N, K / 32] (E8M0), ``bias`` bf16 [N].
+    ``act``: None, "silu", "gelu" (erf) or "swiglu" (SiLU of the first N / 2 columns times the
+    others: N / 2 columns).  ``residual`` bf16 [T, columns], rows strided at will.
+    Returns ``out`` [T, columns], bf16 or float32 (``out_dtype``, or that of the ``out`` given, whose
+    rows may be strided; a bf16 ``out`` may be ``residual`` itself).  Pass ``workspace``
+    (uint8, ``linear_workspace_bytes``, first 4 bytes zeroed once) to allocate nothing
+    but a missing ``out``, and to learn of waits that ran out (``linear_read_status``)."""
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("x and w must be torch.Tensors")
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [T, K] and w [N, K / 2]")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
+    (T, K), N, dev, code = x.shape, w.shape[0], x.device, _ACTS[act]
+    if code == 3 and N % 2:
+        raise ValueError(f"swiglu needs an even number of weight rows, got {N}")
+    cols = N // 2 if code == 3 else N
+    xs = _matrix(x, "x", (torch.bfloat16,), (T, K), dev)
+    if T <= 1:
+        xs = -(-K // 8) * 8
+    _need(w, "w", torch.uint8, (N, K // 2), dev)
+    _need(w_scale, "w_scale", torch.uint8, (N, K // 32), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, (N,), dev)
+    rs = cols if residual is None else _matrix(residual, "residual", (torch.bfloat16,), (T, cols), dev)
+    if out is None:
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+        out = _empty((T, cols), out_dtype, dev, stream)
+    os = _matrix(out, "out", (torch.bfloat16, torch.float32), (T, cols), dev)
+    lib = _native.load()
+    d = LinearStruct(T, K, N, code, 1 if out.dtype == torch.float32 else 0, xs, rs, os)
+    ref = ctypes.byref(d)
+    if workspace is None:
+        workspace = _empty(max(256, lib.linear_mxfp4_workspace_bytes(ref)), torch.uint8, dev, stream)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                                None if bias is None else bias.data_ptr(),
+                                None if residual is None else residual.data_ptr(), out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), _stream(stream, x))
+    _native.check("linear_a16w4_mxfp4", rc)
+    return out
+
+
+def linear_read_status(workspace, stream=None) -> int:
+    """Read and clear the status word of a linear layer's workspace (synchronises the stream)."""
+    v = ctypes.c_uint32(0)
+    rc = _native.load().linear_mxfp4_read_status(workspace.data_ptr(), ctypes.byref(v), _stream(stream, workspace))
+    _native.check("linear_mxfp4_read_status", rc)
+    return int(v.value)
+
+
+def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin, interleaved: bool = False,
+                         position_offset: int = 0, q_out=None, stream=None):
+    """Rotate ``q`` [N, Hq, head_dim] and ``k`` [N, kv heads, head_dim] by their positions, write the rotated keys
+    and ``v``, quantised, to ``slots`` int32 [N] (-1: not written), and return the rotated queries, bf16 [N, Hq, head_dim].
+
+    q, k, v: bf16 or float32, token rows may be strided (slices of a fused
+    projection); ``q`` may be None.  ``positions`` int32 [N], each plus ``position_offset``
+    (the length of a prefix that the requests share); a negative one is padding (a row
+    of zeros, nothing written).  ``cos_sin`` float32 [positions, rotary_dim]: a position's cosines,
+    then its sines; rotary_dim, a multiple of 16, leading elements of a head are rotated, in pairs
+    (i, i + rotary_dim / 2) or, with ``interleaved``, (2i, 2i + 1).  A position past the table
+    makes its token NaN."""
+    if not isinstance(positions, torch.Tensor) or not isinstance(cos_sin, torch.Tensor):
+        raise TypeError("positions and cos_sin must be torch.Tensors")
+    dev = cache.device
+    N = positions.shape[0]
+    _need(positions, "positions", torch.int32, (N,), dev)
+    _need(slots, "slots", torch.int32, (N,), dev)
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [positions, rotary_dim]")
+    _need(cos_sin, "cos_sin", torch.float32, cos_sin.shape, dev)
+    ks = _rows(k, "k", cache, N, (torch.bfloat16, torch.float32))
+    vs = _rows(v, "v", cache, N, (k.dtype,))
+    Hq, qs, D = 0, 0, cache.head_dim
+    if q is not None:
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
+        if q.dim() != 3 or q.shape[0] != N or q.shape[2] != D:
+            raise ValueError(f"q must have shape [{N}, Hq, {D}], got {tuple(q.shape)}")
+        if q.dtype != k.dtype:
+            raise TypeError(f"q must be {k.dtype}, got {q.dtype}")
+        if q.device != dev:
+            raise ValueError(f"q must be on {dev}, got {q.device}")
+        Hq, st = q.shape[1], q.stride()
+        if st[2] != 1 or (Hq > 1 and st[1] != D):
+            raise ValueError("q: a token's heads must be dense")
+        qs = st[0] if N > 1 else Hq * D
+        if q_out is None:
+            q_out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
+        _need(q_out, "q_out", torch.bfloat16, (N, Hq, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    r = KvRopeStruct(N, Hq, 1 if k.dtype == torch.float32 else 0, cos_sin.shape[1], 1 if interleaved else 0,
+                     min(cos_sin.shape[0], 2 ** 31 - 1), position_offset, qs, ks, vs)
+    rc = _native.load().kv_mxfp4_append_rope(
+        cache._ref, ctypes.byref(r), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), None if q_out is None else q_out.data_ptr(),
+        _stream(stream, positions))
+    _native.check("kv_mxfp4_append_rope", rc)
+    return q_out

@@ -1,0 +1,102 @@
+// C ABI entry points of the attention block: argument checks and dispatch.
+#include "kv_checks.h"
+#include "linear.cuh"
+
+using namespace moe;
+
+namespace {
+
+constexpr size_t kLinearWorkspace = 256;  // the status word
+
+bool linear_valid(const linear_mxfp4_t* d) {
+  if (d->T < 0 || d->T > (1 << 24) || d->K < 32 || d->K > 65536 || d->K % 32 || d->N < 1 || d->N > (1 << 20)) return false;
+  if (d->act < LINEAR_ACT_NONE || d->act > LINEAR_ACT_SWIGLU || (d->out_is_f32 != 0 && d->out_is_f32 != 1)) return false;
+  if (d->act == LINEAR_ACT_SWIGLU && d->N % 2) return false;
+  if ((long long)d->T * d->N > 1ll << 36) return false;
+  const int64_t cols = d->act == LINEAR_ACT_SWIGLU ? d->N / 2 : d->N, most = 1ll << 40;
+  return d->x_stride % 8 == 0 && d->x_stride >= d->K && d->x_stride <= most && d->res_stride >= cols &&
+         d->res_stride <= most && d->out_stride >= cols && d->out_stride <= most;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t linear_mxfp4_workspace_bytes(const linear_mxfp4_t* d) { return d && linear_valid(d) ? kLinearWorkspace : 0; }
+
+int linear_a16w4_mxfp4(const linear_mxfp4_t* d, const void* x, const uint8_t* w, const uint8_t* w_scale, const void* bias,
+                       const void* residual, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const WaitSettings wait = take_wait_settings();  // the hook applies to this call only
+  if (!d) return MOE_ERR_NULL;
+  if (!linear_valid(d)) return MOE_ERR_BAD_DIMS;
+  if (d->T == 0) return MOE_OK;
+  if (!x || !w || !w_scale || !out || !workspace) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 2) || !aligned(residual, 2) ||
+      !aligned(out, d->out_is_f32 ? 4 : 2) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes < kLinearWorkspace) return MOE_ERR_WORKSPACE;
+  const uint64_t cols = d->act == LINEAR_ACT_SWIGLU ? d->N / 2 : d->N, n1 = (uint64_t)d->T - 1, N = (uint64_t)d->N;
+  // each value of a residual that is ``out`` itself is read by the thread that writes it
+  const bool in_place = residual == out && !d->out_is_f32 && d->res_stride == d->out_stride;
+  const Span span[] = {{x, 2 * (n1 * (uint64_t)d->x_stride + (uint64_t)d->K)}, {w, N * (uint64_t)d->K / 2},
+                       {w_scale, N * (uint64_t)d->K / 32}, {bias, bias ? 2 * N : 0},
+                       {residual, residual && !in_place ? 2 * (n1 * (uint64_t)d->res_stride + cols) : 0},
+                       {out, (d->out_is_f32 ? 4 : 2) * (n1 * (uint64_t)d->out_stride + cols)},
+                       {workspace, kLinearWorkspace}};
+  if (any_overlap(span, 5)) return MOE_ERR_OVERLAP;
+  int sms = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_OK) return rc;
+  LinearArgs a{};
+  a.T = d->T; a.K = d->K; a.N = d->N; a.cols = (int)cols; a.act = d->act; a.f32 = d->out_is_f32 == 1;
+  a.x_stride = d->x_stride; a.res_stride = d->res_stride; a.out_stride = d->out_stride;
+  a.x = reinterpret_cast<const uint16_t*>(x);
+  a.w = w; a.ws = w_scale;
+  a.bias = reinterpret_cast<const uint16_t*>(bias);
+  a.res = reinterpret_cast<const uint16_t*>(residual);
+  a.out = out;
+  a.status = reinterpret_cast<uint32_t*>(workspace);
+  a.num_sms = sms;
+  a.wait = wait;
+  return launch_linear(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int linear_mxfp4_read_status(void* workspace, uint32_t* status, void* stream) {
+  return kv_mxfp4_read_status(workspace, status, stream);
+}
+
+int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, const void* q, const void* k, const void* v,
+                         const int32_t* positions, const int32_t* slots, const float* cos_sin, void* q_out, void* stream) {
+  if (!c || !r) return MOE_ERR_NULL;
+  if (!cache_valid(c) || r->N < 0 || r->N > (1 << 24) || r->Hq < 0 || r->Hq > 16384 ||
+      (r->x_is_f32 != 0 && r->x_is_f32 != 1) || r->rotary_dim < 16 || r->rotary_dim > c->head_dim || r->rotary_dim % 16 ||
+      (r->interleaved != 0 && r->interleaved != 1) || r->max_positions < 1 || r->position_offset < 0)
+    return MOE_ERR_BAD_DIMS;
+  const int64_t row = (int64_t)c->num_kv_heads * c->head_dim, q_row = (int64_t)r->Hq * c->head_dim;
+  const int64_t unit = r->x_is_f32 ? 4 : 8, most = 1ll << 40;
+  auto stride_ok = [&](int64_t s, int64_t least) { return s >= least && s % unit == 0 && s <= most; };
+  if (!stride_ok(r->k_stride, row) || !stride_ok(r->v_stride, row) || (r->Hq && !stride_ok(r->q_stride, q_row)))
+    return MOE_ERR_BAD_DIMS;
+  if (r->N == 0) return MOE_OK;
+  if (!c->data || !k || !v || !positions || !slots || !cos_sin || (r->Hq && (!q || !q_out))) return MOE_ERR_NULL;
+  if (!aligned(c->data, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(positions, 4) || !aligned(slots, 4) ||
+      !aligned(cos_sin, 16) || (r->Hq && (!aligned(q, 16) || !aligned(q_out, 16))))
+    return MOE_ERR_ALIGN;
+  const uint64_t size = r->x_is_f32 ? 4 : 2, n1 = (uint64_t)r->N - 1, N = (uint64_t)r->N;
+  const Span span[] = {{k, size * (n1 * (uint64_t)r->k_stride + (uint64_t)row)}, {v, size * (n1 * (uint64_t)r->v_stride + (uint64_t)row)},
+                       {q, r->Hq ? size * (n1 * (uint64_t)r->q_stride + (uint64_t)q_row) : 0}, {positions, 4 * N}, {slots, 4 * N},
+                       {cos_sin, 4ull * (uint64_t)r->max_positions * (uint64_t)r->rotary_dim},
+                       {c->data, kv_mxfp4_cache_bytes(c)}, {q_out, r->Hq ? 2 * N * (uint64_t)q_row : 0}};
+  if (any_overlap(span, 6)) return MOE_ERR_OVERLAP;
+  int sms = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_OK) return rc;
+  const RopeArgs a{r->N, r->Hq, r->rotary_dim, r->max_positions, r->position_offset, r->q_stride, r->k_stride, r->v_stride,
+                   q, k, v, positions, slots, cos_sin, reinterpret_cast<uint16_t*>(q_out)};
+  return launch_kv_append_rope(view_of(c), a, r->x_is_f32 == 1, r->interleaved == 1, sms,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

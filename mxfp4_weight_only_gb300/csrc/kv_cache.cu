@@ -1,5 +1,8 @@
 // The 4-bit KV cache outside attention: page tables and slot maps from request
 // lengths, the quantising write of new rows, and the read-back.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv_internal.h"
 
@@ -294,6 +297,19 @@ struct Raw8<false> {
   __device__ __forceinline__ void quant(bool live, uint32_t& codes, uint32_t& sbyte) const {
     kv_quant8(live ? u : make_uint4(0u, 0u, 0u, 0u), codes, sbyte);
   }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+  // the values of lane ``src``
+  __device__ __forceinline__ Raw8 of_lane(int src) const {
+    return Raw8{make_uint4(__shfl_sync(0xffffffffu, u.x, src), __shfl_sync(0xffffffffu, u.y, src),
+                           __shfl_sync(0xffffffffu, u.z, src), __shfl_sync(0xffffffffu, u.w, src))};
+  }
 };
 template <>
 struct Raw8<true> {
@@ -308,6 +324,18 @@ struct Raw8<true> {
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[q] = live ? x[q] : 0.f;
     kv_quant8(x, codes, sbyte);
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ __forceinline__ Raw8 of_lane(int src) const {
+    Raw8 r;
+    r.a = make_float4(__shfl_sync(0xffffffffu, a.x, src), __shfl_sync(0xffffffffu, a.y, src),
+                      __shfl_sync(0xffffffffu, a.z, src), __shfl_sync(0xffffffffu, a.w, src));
+    r.b = make_float4(__shfl_sync(0xffffffffu, b.x, src), __shfl_sync(0xffffffffu, b.y, src),
+                      __shfl_sync(0xffffffffu, b.z, src), __shfl_sync(0xffffffffu, b.w, src));
+    return r;
   }
 };
 
@@ -338,19 +366,38 @@ struct RowWalk {
   }
 };
 
+// Writes a lane's codes of a K and a V row and the row's scale bytes to its slot
+// (the whole warp calls it; ``live``: the slot exists).  Neighbouring blocks' lanes
+// trade halves of their V words, so that each writes four bytes of one lane's operand.
+template <int D>
+__device__ __forceinline__ void store_row(const KvView& c, int slot, int head, bool live, const uint32_t (&code)[2],
+                                          const uint32_t (&sb)[2]) {
+  constexpr int L = D / 8, NB = D / 32;
+  const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
+  // V: lanes of blocks b and b ^ 1 hold bytes 2 t4 (lower half) and 2 t4 + 1
+  // (upper) of their blocks; even b takes the lower halves of both, odd b the upper
+  const uint32_t theirs = __shfl_xor_sync(0xffffffffu, code[1], 4);
+  const uint32_t vw = (b & 1) ? prmt(theirs, code[1], 0x7632u) : prmt(code[1], theirs, 0x5410u);
+  if (live) {
+    const int off = slot & ((1 << c.page_shift) - 1), t = off & 15;
+    uint8_t* rec = c.data + c.record(slot >> c.page_shift, head, off >> 4);
+    *reinterpret_cast<uint32_t*>(rec + k_byte<D>(t, 4 * sub)) = code[0];
+    *reinterpret_cast<uint32_t*>(rec + v_byte<D>(t, 4 * t4 + 2 * (b & 1) + 16 * (b & ~1))) = vw;
+    if (t4 < 2) rec[16 * D + t4 * (D / 2) + t * NB + b] = (uint8_t)sb[t4];
+  }
+}
+
 // Quantising write (kv_mxfp4_append).  HBM-bound: 2 or 4 bytes read and 17/32
 // byte written per value (16,384 x 8 x 128, written and read back: 31.4 us, 5.4
 // TB/s of the bytes that both must move).  D / 8 lanes take a token's K and V row of one head;
 // the loop bounds are uniform per warp, so every lane reaches the shuffles.
-// Neighbouring blocks' lanes trade halves of their V words, so that each writes
-// four bytes of one lane's operand.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const void* __restrict__ k,
                                                         const void* __restrict__ v, long long ks, long long vs, int N,
                                                         const int32_t* __restrict__ slots) {
-  constexpr int L = D / 8, NB = D / 32;  // lanes per row
+  constexpr int L = D / 8;  // lanes per row
   const long long rows = (long long)N * c.heads;
-  const int sub = threadIdx.x % L, b = sub >> 2, t4 = sub & 3;
+  const int sub = threadIdx.x % L;
   const long long step = (long long)gridDim.x * (256 / L), first = (long long)blockIdx.x * (256 / L);
   RowWalk at(first + threadIdx.x / L, step, c.heads);
   for (long long w0 = first; w0 < rows; w0 += step * kRowsInFlight) {
@@ -376,17 +423,137 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvView c, const vo
       uint32_t code[2], sb[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) raw[i][w].quant(live, code[w], sb[w]);
-      // V: lanes of blocks b and b ^ 1 hold bytes 2 t4 (lower half) and 2 t4 + 1
-      // (upper) of their blocks; even b takes the lower halves of both, odd b the upper
-      const uint32_t theirs = __shfl_xor_sync(0xffffffffu, code[1], 4);
-      const uint32_t vw = (b & 1) ? prmt(theirs, code[1], 0x7632u) : prmt(code[1], theirs, 0x5410u);
-      if (live) {
-        const int off = slot[i] & ((1 << c.page_shift) - 1), t = off & 15;
-        uint8_t* rec = c.data + c.record(slot[i] >> c.page_shift, head[i], off >> 4);
-        *reinterpret_cast<uint32_t*>(rec + k_byte<D>(t, 4 * sub)) = code[0];
-        *reinterpret_cast<uint32_t*>(rec + v_byte<D>(t, 4 * t4 + 2 * (b & 1) + 16 * (b & ~1))) = vw;
-        if (t4 < 2) rec[16 * D + t4 * (D / 2) + t * NB + b] = (uint8_t)sb[t4];
+      store_row<D>(c, slot[i], head[i], live, code, sb);
+    }
+  }
+}
+
+// The rotation of a lane's 8 values of a row, x, by the position's cosines and
+// sines: pairs (i, i + rot / 2) of the row, or with PAIRS (2i, 2i + 1).  Float32,
+// every product and sum rounded (so that codes of the rotated keys do not depend on how a
+// compiler contracts them).  Elements from ``rot`` on stay.
+struct Turn {
+  float c[8], s[8];  // of the lane's elements, the sine with the sign that the partner's product takes
+  int partner;       // lane that holds the partners
+  bool on;
+};
+template <int D, bool PAIRS>
+__device__ __forceinline__ Turn load_turn(const float* __restrict__ row, int rot) {
+  constexpr int L = D / 8;
+  const int sub = threadIdx.x % L, half = rot >> 1;
+  Turn r;
+  r.on = 8 * sub < rot;
+  r.partner = threadIdx.x & 31;
+  if (PAIRS) {
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.on && row) {
+      c = __ldg(reinterpret_cast<const float4*>(row + 4 * sub));
+      s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * sub));
+    }
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r.c[2 * k] = r.c[2 * k + 1] = cc[k];
+      r.s[2 * k] = -ss[k];
+      r.s[2 * k + 1] = ss[k];
+    }
+  } else {
+    const bool upper = 8 * sub >= half;
+    if (r.on) r.partner += upper ? -(half >> 3) : half >> 3;
+    const int i = upper ? 8 * sub - half : 8 * sub;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r.on && row) {
+        c = __ldg(reinterpret_cast<const float4*>(row + i) + k);
+        s = __ldg(reinterpret_cast<const float4*>(row + half + i) + k);
       }
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r.c[4 * k + j] = cc[j];
+        r.s[4 * k + j] = upper ? ss[j] : -ss[j];
+      }
+    }
+  }
+  return r;
+}
+// (the whole warp calls it)
+template <bool PAIRS, bool F32>
+__device__ __forceinline__ void turn8(const Turn& r, const Raw8<F32>& raw, float (&x)[8]) {
+  float a[8], p[8];
+  raw.values(a);
+  if (PAIRS) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = a[k ^ 1];
+  } else {
+    raw.of_lane(r.partner).values(p);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = r.on ? __fadd_rn(__fmul_rn(a[k], r.c[k]), __fmul_rn(p[k], r.s[k])) : a[k];
+}
+
+// Rotated queries and the quantising write of rotated keys and of values
+// (kv_mxfp4_append_rope).  HBM-bound: 2 or 4 bytes read a value, 2 bytes written of
+// a query and 17/32 of a key or value.  D / 8 lanes take a unit: up to kQueryRows
+// query heads of one token, which share its cosines and sines, or the K and V row of
+// one head.  Warps up to ``q_warps`` of the grid take queries, the others keys and
+// values (the loop bounds are uniform per warp).
+constexpr int kQueryRows = 4;
+template <int D, bool F32, bool PAIRS>
+__global__ void __launch_bounds__(256) kv_append_rope_kernel(const KvView c, const RopeArgs a, int q_warps) {
+  constexpr int L = D / 8, W = 32 / L;  // lanes a unit, units a warp
+  const int lane = threadIdx.x & 31, sub = lane % L;
+  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
+  const bool queries = warp < q_warps;
+  const int per = queries ? (a.Hq + kQueryRows - 1) / kQueryRows : c.heads;  // units a token
+  const long long units = (long long)a.N * per;
+  const long long step = (long long)(queries ? q_warps : warps - q_warps) * W;
+  long long w0 = (long long)(queries ? warp : warp - q_warps) * W;
+  if (w0 >= units) return;
+  RowWalk at(w0 + lane / L, step, per);
+  for (; w0 < units; w0 += step, at.next()) {
+    const bool there = w0 + lane / L < units;
+    const int tok = at.tok;
+    const int p0 = there ? a.positions[tok] : -1;
+    const long long pos = (long long)p0 + a.position_offset;
+    const bool known = p0 >= 0 && pos < a.max_positions;
+    if (queries) {
+      const int h0 = at.head * kQueryRows;
+      Raw8<F32> raw[kQueryRows];
+#pragma unroll
+      for (int i = 0; i < kQueryRows; ++i)
+        if (there && h0 + i < a.Hq) raw[i].load(a.q, (long long)tok * a.q_stride + (h0 + i) * D + 8 * sub);
+      const Turn turn = load_turn<D, PAIRS>(known ? a.cos_sin + pos * a.rotary_dim : nullptr, a.rotary_dim);
+#pragma unroll
+      for (int i = 0; i < kQueryRows; ++i) {
+        float x[8];
+        turn8<PAIRS>(turn, raw[i], x);
+        if (there && h0 + i < a.Hq) {
+          uint4 o = make_uint4(f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
+                               f32x2_to_bf16x2(x[6], x[7]));
+          // padding: zeros; a position past the table: NaN
+          if (!known) o.x = o.y = o.z = o.w = p0 < 0 ? 0u : 0x7FFF7FFFu;
+          __stcs(reinterpret_cast<uint4*>(a.q_out + ((size_t)tok * a.Hq + h0 + i) * D + 8 * sub), o);
+        }
+      }
+    } else {
+      const int head = at.head, slot = there ? a.slots[tok] : -1;
+      const bool live = slot >= 0 && (slot >> c.page_shift) < c.num_pages && p0 >= 0;
+      Raw8<F32> raw[2];
+      if (live) {
+        raw[0].load(a.k, (long long)tok * a.k_stride + head * D + 8 * sub);
+        raw[1].load(a.v, (long long)tok * a.v_stride + head * D + 8 * sub);
+      }
+      const Turn turn = load_turn<D, PAIRS>(known ? a.cos_sin + pos * a.rotary_dim : nullptr, a.rotary_dim);
+      float x[8];
+      turn8<PAIRS>(turn, raw[0], x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = !live ? 0.f : known ? x[k] : __uint_as_float(0x7FC00000u);
+      uint32_t code[2], sb[2];
+      kv_quant8(x, code[0], sb[0]);
+      raw[1].quant(live, code[1], sb[1]);
+      store_row<D>(c, slot, head, live, code, sb);
     }
   }
 }
@@ -471,6 +638,34 @@ cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool
     if (f32) kv_append_kernel<64, true><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
     else kv_append_kernel<64, false><<<grid, 256, 0, s>>>(c, k, v, ks, vs, N, slots);
   }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append_rope(const KvView& c, const RopeArgs& a, bool f32, bool pairs, int num_sms, cudaStream_t s) {
+  const int W = 256 / c.D;  // units a warp
+  const long long q_units = (long long)a.N * ((a.Hq + kQueryRows - 1) / kQueryRows), kv_units = (long long)a.N * c.heads;
+  // the grid's warps dealt to both kinds by their number of units
+  const long long most = (long long)num_sms * kRowCtas * 8;
+  long long qw = (q_units + W - 1) / W, kw = (kv_units + W - 1) / W;
+  if (qw + kw > most) {
+    const long long share = std::max<long long>(1, most * qw / (qw + kw));
+    qw = qw ? std::min(share, most - 1) : 0;
+    kw = most - qw;
+  }
+  const int grid = (int)((qw + kw + 7) / 8);
+  auto go = [&](auto d, auto wide, auto p) {
+    kv_append_rope_kernel<decltype(d)::value, decltype(wide)::value, decltype(p)::value><<<grid, 256, 0, s>>>(c, a, (int)qw);
+  };
+  auto of_dim = [&](auto wide, auto p) {
+    if (c.D == 128) go(std::integral_constant<int, 128>{}, wide, p);
+    else go(std::integral_constant<int, 64>{}, wide, p);
+  };
+  auto of_type = [&](auto p) {
+    if (f32) of_dim(std::true_type{}, p);
+    else of_dim(std::false_type{}, p);
+  };
+  if (pairs) of_type(std::true_type{});
+  else of_type(std::false_type{});
   return cudaGetLastError();
 }
 

@@ -72,6 +72,15 @@ cudaError_t launch_page_tables(const PageTableArgs& a, int num_sms, cudaStream_t
 
 cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool f32, long long k_stride,
                              long long v_stride, int N, const int32_t* slots, int num_sms, cudaStream_t s);
+struct RopeArgs {
+  int N, Hq, rotary_dim, max_positions, position_offset;
+  long long q_stride, k_stride, v_stride;
+  const void *q, *k, *v;
+  const int32_t *positions, *slots;
+  const float* cos_sin;
+  uint16_t* q_out;
+};
+cudaError_t launch_kv_append_rope(const KvView& c, const RopeArgs& a, bool f32, bool pairs, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvView& c, const int32_t* slots, int N, void* k_out, void* v_out, int num_sms,
                              cudaStream_t s);
 
