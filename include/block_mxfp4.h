@@ -104,6 +104,40 @@ typedef struct kv_mxfp4_rope {
 int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, const void* q, const void* k, const void* v,
                          const int32_t* positions, const int32_t* slots, const float* cos_sin, void* q_out, void* stream);
 
+/*
+ * Attention of a batch whose requests share a cached prefix, which is read once for
+ * all of them.  The prefix has pages of its own, as has what each request holds
+ * after it (so a request's own keys begin on a page of their own, numbered from 0).
+ *   a              as in kv_mxfp4_attention; max_blocks, seq_lens, query_start and
+ *                  positions are those of the requests' own tokens; window is 0
+ *   shared_blocks  entries of shared_table, >= 1
+ */
+
+/* Bytes of workspace that kv_mxfp4_attention_shared needs (256-byte aligned; 0 for
+ * invalid sizes): as kv_mxfp4_attention's, but it grows with N * Hq * head_dim (a
+ * float32 sum of each row, for its own keys and for every slice of the prefix). */
+size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks);
+
+/*
+ * out = softmax over the prefix's keys and the request's own, as kv_mxfp4_attention
+ * (its types, formulas, precision and status word):
+ *   shared_table  int32 [shared_blocks]  pages of the prefix; a page id outside the
+ *                 cache makes its tokens invisible
+ *   shared_len    int32 [1]  keys of the prefix (at most shared_blocks * page_size
+ *                 are looked at, negative = none)
+ *   block_table   int32 [R, max_blocks], seq_lens int32 [R]: the requests' own pages
+ *                 and keys; every row sees the whole prefix, and its own keys as
+ *                 without one.  Length 0: only the prefix.  A negative length: the
+ *                 request sees nothing, not the prefix either (an empty place in the
+ *                 batch: zeros, lse -inf).
+ *   query_start   int32 [R+1], not descending
+ * The rest as in kv_mxfp4_attention.
+ */
+int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks, const void* q,
+                              const int32_t* shared_table, const int32_t* shared_len, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* query_start, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,8 +7,8 @@ is computed in the library's kernels.
 
 One layer's attention block: ``linear_a16w4_mxfp4`` (queries, keys and values) ->
 ``kv_append_rope_mxfp4`` (rotated, keys and values quantised to their slots) ->
-``attention_kv_mxfp4`` -> ``linear_a16w4_mxfp4`` (output, added to the residual
-stream).
+``attention_kv_mxfp4``, or ``attention_kv_mxfp4_shared`` behind a common prefix ->
+``linear_a16w4_mxfp4`` (output, added to the residual stream).
 """
 
 from __future__ import annotations
@@ -18,8 +18,8 @@ import ctypes
 import torch
 
 from . import _native
-from ._native import KvRopeStruct, LinearStruct
-from .kv_cache import KvCacheMxfp4, _empty, _need, _rows, _stream
+from ._native import KvAttnStruct, KvRopeStruct, LinearStruct
+from .kv_cache import KvCacheMxfp4, _empty, _i32, _need, _queries, _rows, _stream
 
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 
@@ -131,18 +131,9 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
     vs = _rows(v, "v", cache, N, (k.dtype,))
     Hq, qs, D = 0, 0, cache.head_dim
     if q is not None:
-        if not isinstance(q, torch.Tensor):
-            raise TypeError("q must be a torch.Tensor")
-        if q.dim() != 3 or q.shape[0] != N or q.shape[2] != D:
+        rows, Hq, qs = _queries(q, cache, k.dtype)
+        if rows != N:
             raise ValueError(f"q must have shape [{N}, Hq, {D}], got {tuple(q.shape)}")
-        if q.dtype != k.dtype:
-            raise TypeError(f"q must be {k.dtype}, got {q.dtype}")
-        if q.device != dev:
-            raise ValueError(f"q must be on {dev}, got {q.device}")
-        Hq, st = q.shape[1], q.stride()
-        if st[2] != 1 or (Hq > 1 and st[1] != D):
-            raise ValueError("q: a token's heads must be dense")
-        qs = st[0] if N > 1 else Hq * D
         if q_out is None:
             q_out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
         _need(q_out, "q_out", torch.bfloat16, (N, Hq, D), dev)
@@ -156,3 +147,54 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
         _stream(stream, positions))
     _native.check("kv_mxfp4_append_rope", rc)
     return q_out
+
+
+def attention_shared_workspace_bytes(cache: KvCacheMxfp4, R: int, N: int, Hq: int, max_blocks: int, max_q_len: int,
+                                     shared_blocks: int) -> int:
+    """Bytes of workspace for ``attention_kv_mxfp4_shared`` calls of these sizes."""
+    D = cache.head_dim
+    a = KvAttnStruct(R, N, Hq, max_blocks, max_q_len, 1, 0, Hq * D, 1.0)
+    return int(_native.load().kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ctypes.byref(a), shared_blocks))
+
+
+def attention_kv_mxfp4_shared(q, cache: KvCacheMxfp4, shared_table, shared_len, block_table, seq_lens, query_start,
+                              max_q_len: int, scale=None, causal: bool = True, out=None, lse=None, workspace=None,
+                              stream=None):
+    """Attention of ``q`` bf16 [N, Hq, head_dim] over a prefix that all requests share and each request's own keys.
+
+    ``shared_table`` int32 [shared blocks] and ``shared_len`` int32 [1]: the prefix's pages
+    and keys, read once for the whole batch.  ``block_table`` int32 [R, max_blocks] and
+    ``seq_lens`` int32 [R]: what each request holds after it, on pages of its own, positions
+    from 0 (the step's new tokens included); 0: only the prefix, negative: an empty
+    place in the batch, whose rows are zeros (lse -inf).  Every row sees the whole prefix.  The rest as
+    ``attention_kv_mxfp4``; the workspace's size is ``attention_shared_workspace_bytes``, its status
+    is read by ``attention_read_status``."""
+    dev = cache.device
+    N, Hq, qs = _queries(q, cache, torch.bfloat16)
+    D = cache.head_dim
+    if not isinstance(block_table, torch.Tensor) or not isinstance(shared_table, torch.Tensor) or not isinstance(seq_lens, torch.Tensor):
+        raise TypeError("shared_table, block_table and seq_lens must be torch.Tensors")
+    if block_table.dim() != 2 or shared_table.dim() != 1 or seq_lens.dim() != 1:
+        raise ValueError("block_table must be [R, max_blocks], shared_table [shared blocks], seq_lens [R]")
+    R, mb, sb = seq_lens.shape[0], block_table.shape[1], shared_table.shape[0]
+    for t, name, shape in ((shared_table, "shared_table", (sb,)), (shared_len, "shared_len", (1,)),
+                           (block_table, "block_table", (R, mb)), (seq_lens, "seq_lens", (R,)),
+                           (query_start, "query_start", (R + 1,))):
+        _need(t, name, _i32, shape, dev)
+    if out is None:
+        out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
+    _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (N, Hq), dev)
+    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, 0, qs, D ** -0.5 if scale is None else scale)
+    lib, ref = _native.load(), ctypes.byref(a)
+    if workspace is None:
+        workspace = _empty(max(256, lib.kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ref, sb)), torch.uint8, dev, stream)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    rc = lib.kv_mxfp4_attention_shared(cache._ref, ref, sb, q.data_ptr(), shared_table.data_ptr(), shared_len.data_ptr(),
+                                       block_table.data_ptr(), seq_lens.data_ptr(), query_start.data_ptr(), out.data_ptr(),
+                                       None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _stream(stream, q))
+    _native.check("kv_mxfp4_attention_shared", rc)
+    return out

@@ -23,7 +23,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libmoe_a16w4.so"
 CHECK_LIB_NAME = "libmoe_a16w4_check.so"
 SOURCES = ["api.cu", "route.cu", "requant.cu", "decode.cu", "prefill.cu", "noalloc.cu", "actquant.cu",
-           "kv_api.cu", "kv_cache.cu", "kv_attn.cu", "kv_stream.cu", "kv_prompt.cu", "block_api.cu", "linear.cu"]
+           "kv_api.cu", "kv_cache.cu", "kv_attn.cu", "kv_stream.cu", "kv_prompt.cu", "kv_shared.cu", "block_api.cu",
+           "linear.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "moe_internal.h", "kv_internal.h", "kv_checks.h", "linear.cuh")] + [
     os.path.join(ROOT, "include", h) for h in ("moe_a16w4.h", "kv_mxfp4.h", "block_mxfp4.h")
 ]

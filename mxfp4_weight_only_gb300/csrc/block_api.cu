@@ -18,6 +18,11 @@ bool linear_valid(const linear_mxfp4_t* d) {
          d->res_stride <= most && d->out_stride >= cols && d->out_stride <= most;
 }
 
+bool shared_valid(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t blocks) {
+  return cache_valid(c) && a && attn_valid(c, a) && a->window == 0 && blocks >= 1 &&
+         (long long)blocks * c->page_size <= 0x7FFFFFFFll;
+}
+
 }  // namespace
 
 extern "C" {
@@ -97,6 +102,44 @@ int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, co
                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
+}
+
+size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks) {
+  return shared_valid(c, a, shared_blocks) ? kv_shared_workspace(view_of(c), a, shared_blocks) : 0;
+}
+
+int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks, const void* q,
+                              const int32_t* shared_table, const int32_t* shared_len, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* query_start, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const WaitSettings wait = take_wait_settings();  // the hook applies to this call only
+  if (!c || !a) return MOE_ERR_NULL;
+  if (!shared_valid(c, a, shared_blocks)) return MOE_ERR_BAD_DIMS;
+  if (a->R == 0 || a->N == 0 || a->max_q_len == 0) return MOE_OK;
+  if (!c->data || !q || !shared_table || !shared_len || !block_table || !seq_lens || !query_start || !out || !workspace)
+    return MOE_ERR_NULL;
+  if (!aligned(c->data, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) ||
+      !aligned(shared_table, 4) || !aligned(shared_len, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(query_start, 4) || !aligned(lse, 4))
+    return MOE_ERR_ALIGN;
+  const KvView view = view_of(c);
+  const size_t need = kv_shared_workspace(view, a, shared_blocks);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  const uint64_t heads = (uint64_t)a->N * (uint64_t)a->Hq, D = (uint64_t)c->head_dim, R = (uint64_t)a->R;
+  const Span span[] = {{q, 2 * ((uint64_t)(a->N - 1) * (uint64_t)a->q_stride + (uint64_t)a->Hq * D)},
+                       {shared_table, 4ull * (uint64_t)shared_blocks}, {shared_len, 4},
+                       {block_table, 4 * R * (uint64_t)a->max_blocks}, {seq_lens, 4 * R}, {query_start, 4 * R + 4},
+                       {c->data, kv_mxfp4_cache_bytes(c)}, {out, 2 * heads * D}, {lse, lse ? 4 * heads : 0}, {workspace, need}};
+  if (any_overlap(span, 7)) return MOE_ERR_OVERLAP;
+  int sms = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_OK) return rc;
+  KvAttnArgs g = attn_args(view, a, q, block_table, seq_lens, query_start, out, lse, workspace, sms, wait);
+  g.sh.splits = kv_shared_splits(view, a, shared_blocks);
+  g.sh.blocks = shared_blocks;
+  g.sh.table = shared_table;
+  g.sh.len = shared_len;
+  return launch_kv_shared(g, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

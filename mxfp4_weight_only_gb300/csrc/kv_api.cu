@@ -109,18 +109,7 @@ int kv_mxfp4_attention(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, cons
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
-  KvAttnArgs g{};
-  g.cache = view;
-  g.R = a->R; g.N = a->N; g.Hq = a->Hq; g.max_blocks = a->max_blocks; g.max_q_len = a->max_q_len;
-  g.causal = a->causal; g.window = a->window; g.q_stride = a->q_stride; g.scale = a->scale;
-  g.q = reinterpret_cast<const uint16_t*>(q);
-  g.table = block_table; g.seq_lens = seq_lens; g.query_start = query_start;
-  g.out = reinterpret_cast<uint16_t*>(out);
-  g.lse = lse;
-  g.workspace = reinterpret_cast<uint8_t*>(workspace);
-  g.status = reinterpret_cast<uint32_t*>(workspace);
-  g.num_sms = sms;
-  g.wait = wait;
+  const KvAttnArgs g = attn_args(view, a, q, block_table, seq_lens, query_start, out, lse, workspace, sms, wait);
   return launch_kv_attention(g, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

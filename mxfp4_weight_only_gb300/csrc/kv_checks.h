@@ -73,4 +73,22 @@ inline bool attn_valid(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a) {
   return isfinite(a->scale);
 }
 
+inline KvAttnArgs attn_args(const KvView& view, const kv_mxfp4_attn_t* a, const void* q, const int32_t* block_table,
+                            const int32_t* seq_lens, const int32_t* query_start, void* out, float* lse, void* workspace,
+                            int sms, const WaitSettings& wait) {
+  KvAttnArgs g{};
+  g.cache = view;
+  g.R = a->R; g.N = a->N; g.Hq = a->Hq; g.max_blocks = a->max_blocks; g.max_q_len = a->max_q_len;
+  g.causal = a->causal; g.window = a->window; g.q_stride = a->q_stride; g.scale = a->scale;
+  g.q = reinterpret_cast<const uint16_t*>(q);
+  g.table = block_table; g.seq_lens = seq_lens; g.query_start = query_start;
+  g.out = reinterpret_cast<uint16_t*>(out);
+  g.lse = lse;
+  g.workspace = reinterpret_cast<uint8_t*>(workspace);
+  g.status = reinterpret_cast<uint32_t*>(workspace);
+  g.num_sms = sms;
+  g.wait = wait;
+  return g;
+}
+
 }  // namespace moe

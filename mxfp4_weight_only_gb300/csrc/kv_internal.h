@@ -90,6 +90,24 @@ struct KvAttnArgs;
 // its true number of rows gives.
 struct KvRequest {
   int qb, ql, n, first;
+  int causal;
+  int base;  // position of its first key in its pages' table (slices of a shared prefix)
+  int part;  // where its results go, for calls with a shared prefix
+};
+
+// A prefix that all requests of a call share (kv_mxfp4_attention_shared).  It is cut
+// into ``splits`` slices, each a request of its own (numbers R ..) of all query rows,
+// whose keys every row sees.  Results, of the requests' own keys (part 0) and of
+// each slice (part 1 ..), are sums that kv_join_kernel puts together.
+constexpr int kMaxSplits = 31;   // (a lane of a warp looks at each part)
+constexpr int kSliceKeys = 128;  // slices start at multiples of this
+struct KvShared {
+  int splits = 0;  // 0: no prefix, one result a row
+  int blocks = 0;  // entries of table
+  int row_limit = 0;  // slices with more rows than this go to the tensor-core kernel
+  const int32_t *table = nullptr, *len = nullptr;
+  float* o = nullptr;    // [part][N * Hq][D]: weighted sums of values, in units of 2^(E - 127)
+  float4* ml = nullptr;  // [part][N * Hq]: reference (units of 4 log2), sum of weights, E, unused
 };
 
 struct KvAttnArgs {
@@ -106,9 +124,32 @@ struct KvAttnArgs {
   uint32_t* status;
   int num_sms;
   WaitSettings wait;  // limit of every wait in the kernels
+  KvShared sh;
 };
+#ifdef __CUDACC__
+// Keys of the shared prefix.
+__device__ __forceinline__ int kv_prefix(const KvAttnArgs& a) {
+  return (int)min((long long)max(*a.sh.len, 0), (long long)a.sh.blocks << a.cache.page_shift);
+}
+template <bool SHARED>
 __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   KvRequest q;
+  q.base = 0;
+  q.part = 0;
+  q.causal = a.causal;
+  if (SHARED && r >= a.R) {
+    const int P = kv_prefix(a);
+    const int slice = (int)(((long long)P + (long long)a.sh.splits * kSliceKeys - 1) / ((long long)a.sh.splits * kSliceKeys)) * kSliceKeys;
+    const long long base = (long long)(r - a.R) * slice;
+    q.base = (int)min(base, (long long)P);
+    q.part = 1 + r - a.R;
+    q.causal = 0;
+    q.qb = 0;
+    q.ql = min(max(a.query_start[a.R], 0), a.N);
+    q.n = min(P - q.base, slice);
+    q.first = q.n;
+    return q;
+  }
   const int end = a.query_start[r + 1];
   q.qb = min(max(a.query_start[r], 0), a.N);
   q.ql = min(min(max(end, 0), a.N) - q.qb, a.max_q_len);
@@ -116,6 +157,17 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   q.first = q.n - (max(end, q.qb) - q.qb);
   return q;
 }
+// Page and place in it of key ``key`` of request r.
+template <bool SHARED>
+__device__ __forceinline__ int kv_page(const KvAttnArgs& a, const KvRequest& q, int r, int key) {
+  if (SHARED && r >= a.R) return a.sh.table[(q.base + key) >> a.cache.page_shift];
+  return a.table[(size_t)r * a.max_blocks + (key >> a.cache.page_shift)];
+}
+template <bool SHARED>
+__device__ __forceinline__ int kv_group(const KvAttnArgs& a, const KvRequest& q, int key) {
+  return (((SHARED ? q.base : 0) + key) & ((1 << a.cache.page_shift) - 1)) >> 4;
+}
+#endif
 
 // Queries as f16 times a power of two a row (and kv head): the largest magnitude
 // goes into [2^14, 2^15), so elements down to 2^-31 of it keep their 8 significant
@@ -173,6 +225,14 @@ cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, const int32_t* 
 // Tensor-core kernel: requests of more than ``row_limit`` rows; marks in odd [R]
 // those whose scales it cannot hold, for launch_kv_stream to do over.
 cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, cudaStream_t s);
+
+// Rows of one request (query rows x heads per kv head) up to which it is streamed.
+int kv_stream_rows(const KvAttnArgs& a);
+
+// Attention with a shared prefix: how it is cut, its workspace, the call.
+int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
+size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
+cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s);
 
 size_t kv_attention_workspace(const KvView& c, const kv_mxfp4_attn_t* a);
 cudaError_t launch_kv_attention(const KvAttnArgs& a, cudaStream_t s);

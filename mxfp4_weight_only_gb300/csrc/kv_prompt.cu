@@ -279,7 +279,8 @@ struct PromptShared {
 };
 
 // One item: the rows of request r from row0 on, of kv head kvh.  FEW: see kFewKeys.
-template <int D, bool FEW>
+// SHARED: the call's requests share a prefix (KvShared); results are sums.
+template <int D, bool FEW, bool SHARED = false>
 __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem, uint32_t tmem, int r, int kvh, int row0) {
   using C = PromptCfg<D>;
   constexpr int NB = D / 32, S = C::kStages;
@@ -289,15 +290,15 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   volatile int* abort_flag = &sh.abort_flag;
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const KvRequest rq = kv_request(a, r);
+  const KvRequest rq = kv_request<SHARED>(a, r);
   const int qb = rq.qb, ql = rq.ql, n = rq.n;
   const int rows = min(ql * p.G - row0, 256);  // rows of this CTA
   const int first_pos = rq.first + row0 / p.G, last_pos = rq.first + (row0 + rows - 1) / p.G;
-  const int key_hi = a.causal ? min(n, last_pos + 1) : n;
+  const int key_hi = rq.causal ? min(n, last_pos + 1) : n;
   const int key_lo = kv_first_key(first_pos, a.window);
   const int t0 = key_lo / kKeys, nt = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - t0 : 0;
   const int nq = rows > 128 ? 2 : 1;
-  const int32_t* table = a.table + (size_t)r * a.max_blocks;
+  const int32_t* table = SHARED && r >= a.R ? a.sh.table : a.table + (size_t)r * a.max_blocks;
 
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -357,7 +358,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       if (lane == 0) mbar_arrive(q_full);
     }
     const int pos = rq.first + i;
-    const int hi = a.causal ? min(n, pos + 1) : n;           // keys [lo, hi) are seen
+    const int hi = rq.causal ? min(n, pos + 1) : n;           // keys [lo, hi) are seen
     const int lo = kv_first_key(pos, a.window);
     const uint32_t tS = tmem + ((uint32_t)(32 * quad) << 16) + C::kSCol + 128 * x;
     const uint32_t tO = tmem + ((uint32_t)(32 * quad) << 16) + C::kOCol + 128 * x;
@@ -366,7 +367,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
     // page of record ``lane`` of tile j, -1 for none; looked up a tile ahead
     auto page_of = [&](int j) -> int {
       const int key = (t0 + j) * kKeys + 16 * lane;
-      return lane < 8 && j < nt && key < n ? table[key >> a.cache.page_shift] : -1;
+      return lane < 8 && j < nt && key < n ? table[((SHARED ? rq.base : 0) + key) >> a.cache.page_shift] : -1;
     };
     int next_page = page_of(0);
     if (x < nq) {
@@ -502,6 +503,24 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       if (ok) {
         if (l != l) p.odd[r] = 1;  // beyond kFarScore on the way (or NaN)
         tc_after();
+        if constexpr (SHARED) {
+          const size_t to = (size_t)rq.part * a.N * a.Hq + (size_t)(qb + i) * a.Hq + hq;
+          // (weights are 2^(S f + (kWeightExp - mf)): that is their reference)
+          if (real) a.sh.ml[to] = make_float4(l == 0.f ? -INFINITY : -0.25f * (kWeightExp - mf), l, __int_as_float(127), 0.f);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            if (nt > 0) {
+              tc_ld32(tO + 32 * c, v);
+              tc_ld_wait32(v);
+            }
+            if (real && nt > 0) {
+              uint4* dst = reinterpret_cast<uint4*>(a.sh.o + to * D + 32 * c);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+        } else {
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t at = (size_t)(qb + i) * a.Hq + hq;
 #pragma unroll
@@ -526,6 +545,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
           }
         }
         if (real && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (mf + lg2(l) - kWeightExp) * 0.6931471805599453f;
+        }
       }
     }
   } else if (warp >= kMmaWarp) {
@@ -612,9 +632,9 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       rec = nullptr;
       valid = 0;
       if (j < nt && key < n) {
-        const int pg = table[key >> a.cache.page_shift];
+        const int pg = table[((SHARED ? rq.base : 0) + key) >> a.cache.page_shift];
         if (pg >= 0 && pg < a.cache.num_pages) {
-          rec = a.cache.data + a.cache.record(pg, kvh, (key & ((1 << a.cache.page_shift) - 1)) >> 4);
+          rec = a.cache.data + a.cache.record(pg, kvh, kv_group<SHARED>(a, rq, key));
           valid = min(16, n - key);
         }
       }
@@ -719,7 +739,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   }
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const PromptParams p) {
   using C = PromptCfg<D>;
   constexpr int S = C::kStages;
@@ -755,14 +775,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     // this CTA's item: the last row tiles of a request first (they see the most keys), heads innermost
     __syncwarp();
     long long before = 0;
-    for (int r0 = 0; r0 < a.R; r0 += 32) {
+    const int R = SHARED ? a.R + a.sh.splits : a.R;
+    for (int r0 = 0; r0 < R; r0 += 32) {
       const int r = r0 + lane;
       long long rows = 0;
-      if (r < a.R) {
+      if (SHARED && r >= a.R && r < R) {
+        rows = (long long)kv_request<SHARED>(a, r).ql * p.G;
+      } else if (r < R) {
         const int qb = min(max(a.query_start[r], 0), a.N);
         rows = (long long)max(min(min(max(a.query_start[r + 1], 0), a.N) - qb, a.max_q_len), 0) * p.G;
       }
-      const int tiles = rows > p.row_limit ? (int)((rows + 255) / 256) : 0;
+      const int limit = SHARED && r >= a.R ? a.sh.row_limit : p.row_limit;
+      const int tiles = rows > limit ? (int)((rows + 255) / 256) : 0;
       long long incl = (long long)tiles * H;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -775,8 +799,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         item[0] = r;
         item[1] = (int)(off % H);
         item[2] = qt * 256;
-        const KvRequest rq = kv_request(a, r);
-        const int seen = a.causal ? min(rq.n, rq.first + item[2] / p.G + 1) : rq.n;
+        const KvRequest rq = kv_request<SHARED>(a, r);
+        const int seen = rq.causal ? min(rq.n, rq.first + item[2] / p.G + 1) : rq.n;
         item[3] = min(seen, a.window ? a.window : seen) <= kFewKeys;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
@@ -789,8 +813,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_slot, 0);
   const int r = item[0];
   if (r >= 0) {
-    if (item[3]) prompt_item<D, true>(p, smem, tmem, r, item[1], item[2]);
-    else prompt_item<D, false>(p, smem, tmem, r, item[1], item[2]);
+    if constexpr (SHARED) {
+      if (item[3]) prompt_item<D, true, true>(p, smem, tmem, r, item[1], item[2]);
+      else prompt_item<D, false, true>(p, smem, tmem, r, item[1], item[2]);
+    } else {
+      if (item[3]) prompt_item<D, true>(p, smem, tmem, r, item[1], item[2]);
+      else prompt_item<D, false>(p, smem, tmem, r, item[1], item[2]);
+    }
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -800,22 +829,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   }
 }
 
-template <int D>
+template <int D, bool SHARED>
 cudaError_t launch_prompt(const PromptParams& p, unsigned grid, cudaStream_t s) {
   using C = PromptCfg<D>;
   // the register split draws on what the kernel is launched with: never launch it with less
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes attr;
-    const cudaError_t e = cudaFuncGetAttributes(&attr, kv_prompt_kernel<D>);
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kv_prompt_kernel<D, SHARED>);
     if (e != cudaSuccess) return e;
     regs.store(attr.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) < kLaunchRegs) return cudaErrorInvalidConfiguration;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_shared(kv_prompt_kernel<D>, C::kSmem, done);
+  const cudaError_t e = allow_shared(kv_prompt_kernel<D, SHARED>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  kv_prompt_kernel<D><<<grid, kPromptThreads, C::kSmem, s>>>(p);
+  kv_prompt_kernel<D, SHARED><<<grid, kPromptThreads, C::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -827,14 +856,20 @@ cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, c
   p.G = a.Hq / a.cache.heads;
   p.row_limit = row_limit;
   p.odd = odd;
-  cudaError_t e = cudaMemsetAsync(odd, 0, sizeof(int32_t) * a.R, s);
+  cudaError_t e = cudaMemsetAsync(odd, 0, sizeof(int32_t) * (a.R + a.sh.splits), s);
   if (e != cudaSuccess) return e;
   // at most one tile per 256 rows, and one partial tile per request that has more rows than the limit
   const long long rows = (long long)a.N * p.G;
   const long long most = rows / (row_limit + 1) < a.R ? rows / (row_limit + 1) : a.R;
-  const long long grid = (rows / 256 + most) * a.cache.heads;
+  long long grid = (rows / 256 + most) * a.cache.heads;
+  if (a.sh.splits > 0) {
+    // a slice of a shared prefix has all rows
+    if (rows > a.sh.row_limit) grid += (rows + 255) / 256 * a.sh.splits * a.cache.heads;
+    if (grid == 0) return cudaSuccess;
+    return a.cache.D == 128 ? launch_prompt<128, true>(p, (unsigned)grid, s) : launch_prompt<64, true>(p, (unsigned)grid, s);
+  }
   if (grid == 0) return cudaSuccess;
-  return a.cache.D == 128 ? launch_prompt<128>(p, (unsigned)grid, s) : launch_prompt<64>(p, (unsigned)grid, s);
+  return a.cache.D == 128 ? launch_prompt<128, false>(p, (unsigned)grid, s) : launch_prompt<64, false>(p, (unsigned)grid, s);
 }
 
 }  // namespace moe

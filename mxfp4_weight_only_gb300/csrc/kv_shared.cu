@@ -1,0 +1,149 @@
+// Attention of a batch that shares a cached prefix (kv_mxfp4_attention_shared).
+//
+// With the prefix's keys j < P and a request's own keys after them, a row's softmax
+// over both is joined from sums over any cut of the keys: part i has the reference
+// m_i, l_i = sum 2^(s - m_i) and o_i = sum 2^(s - m_i) v, and with M = max m_i
+//   out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+// The prefix is read once for all rows of the batch: it is cut into slices, each a
+// request of its own whose rows are all query rows of the call, which the two
+// attention kernels take as they take any other request (few rows: streamed;
+// many: tensor cores, one CTA per 256 rows, kv head and slice).  The requests' own
+// keys are parts too.  kv_join_kernel joins a row's parts.
+#include <algorithm>
+
+#include "kv_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+// The plan is made for a GB300's SMs, so that a workspace's size depends on the sizes alone.
+constexpr int kPlanSms = 152;
+// Rows (tokens x query heads per kv head) up to which the prefix is streamed.
+constexpr int kSharedStreamRows = 32;
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// One warp a row (token x query head).
+template <int D>
+__global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
+  constexpr int V = D / 32;  // dims of a lane
+  grid_dep_wait();
+  const int r = blockIdx.x, lane = threadIdx.x & 31;
+  const KvRequest q = kv_request<true>(a, r);
+  const bool gone = a.seq_lens[r] < 0;  // an empty place in the batch
+  const int parts = 1 + a.sh.splits;
+  const long long rows = (long long)max(q.ql, 0) * a.Hq, all = (long long)a.N * a.Hq;
+  for (long long i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
+    const long long row = (long long)q.qb * a.Hq + i;
+    // lane p: part p
+    float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    if (lane < parts && !gone) ml = a.sh.ml[lane * all + row];
+    const bool some = ml.y != 0.f;  // (NaN too)
+    const int E0 = some ? __float_as_int(ml.z) : -100000;
+    const int E = __reduce_max_sync(0xffffffffu, E0);
+    float M = some ? ml.x : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float w = some ? exp2f(4.f * (ml.x - (M == -INFINITY ? 0.f : M))) : 0.f;
+    float l = some ? w * ml.y : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (some && E0 != E) w *= exp2f((float)max(E0 - E, -300));
+    uint32_t there = __ballot_sync(0xffffffffu, some);
+    float o[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.f;
+    for (; there; there &= there - 1) {
+      const int p = __ffs(there) - 1;
+      const float wp = __shfl_sync(0xffffffffu, w, p);
+      const float* src = a.sh.o + ((size_t)p * all + row) * D + V * lane;
+      float v[V];
+      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = fmaf(v[k], wp, o[k]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      o[k] *= inv;
+      if (l != 0.f && E != 127) {  // two factors: either alone may leave the range
+        const int e = min(max(E - 127, -252), 252), h = e >> 1;
+        o[k] = o[k] * exp2_int(h) * exp2_int(e - h);
+      }
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + V * lane);
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+    else *dst = f32x2_to_bf16x2(o[0], o[1]);
+    if (lane == 0 && a.lse)
+      a.lse[row] = l == 0.f ? -INFINITY : M == -INFINITY ? l : fmaf(M, 2.772588722239781f, logf(l));
+  }
+}
+
+struct SharedLayout {
+  size_t odd, ml, o, total;
+};
+SharedLayout shared_layout(int D, int R, int N, int Hq, int splits) {
+  SharedLayout L;
+  const size_t rows = (size_t)N * Hq * (1 + splits);
+  L.odd = kStatusBytes + align256(kv_stream_workspace(D));
+  L.ml = L.odd + align256(sizeof(int32_t) * ((size_t)R + splits));
+  L.o = L.ml + align256(sizeof(float4) * rows);
+  L.total = L.o + sizeof(float) * rows * D;
+  return L;
+}
+
+}  // namespace
+
+// Slices of a prefix of up to ``blocks`` pages: as many as shorten the tensor-core
+// kernel's waves (a CTA takes about 16 ns a key and some 5 us besides), against what
+// a slice's sums cost to write and read (about 4 bytes a picosecond).
+int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
+  const long long rows = (long long)a->N * (a->Hq / c.heads);
+  if (rows <= kSharedStreamRows) return 1;
+  const long long tiles = (rows + 255) / 256 * c.heads, keys = (long long)blocks << c.page_shift;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxSplits; ++s) {
+    const long long slice = (keys + (long long)s * kSliceKeys - 1) / ((long long)s * kSliceKeys) * kSliceKeys;
+    const double t = (double)((tiles * s + kPlanSms - 1) / kPlanSms) * (16e-9 * slice + 5e-6) +
+                     (double)s * a->N * a->Hq * c.D * 8 / 4e12;
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
+  return shared_layout(c.D, a->R, a->N, a->Hq, kv_shared_splits(c, a, blocks)).total;
+}
+
+cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s) {
+  const int G = a.Hq / a.cache.heads;
+  const SharedLayout L = shared_layout(a.cache.D, a.R, a.N, a.Hq, a.sh.splits);
+  a.sh.row_limit = kSharedStreamRows;
+  a.sh.ml = reinterpret_cast<float4*>(a.workspace + L.ml);
+  a.sh.o = reinterpret_cast<float*>(a.workspace + L.o);
+  uint8_t* ws = a.workspace + kStatusBytes;
+  const long long all = (long long)a.N * G, own = (long long)a.max_q_len * G;
+  const int limit = kv_stream_rows(a);
+  int32_t* odd = nullptr;
+  cudaError_t e;
+  if (all > kSharedStreamRows || own > limit) {
+    odd = reinterpret_cast<int32_t*>(a.workspace + L.odd);
+    if ((e = launch_kv_prompt(a, limit, odd, s)) != cudaSuccess) return e;
+  }
+  // (row tiles as without a prefix; a streamed prefix has most of the keys)
+  const long long streamed = all <= kSharedStreamRows ? all : own <= limit ? own : G;
+  if ((e = launch_kv_stream(a, limit, odd, streamed <= 8 ? 1 : 2, ws, s)) != cudaSuccess) return e;
+  const long long want = (std::min<long long>(a.max_q_len, a.N) * a.Hq + 7) / 8;
+  const dim3 grid((unsigned)a.R, (unsigned)std::min<long long>(std::max<long long>(want, 1), 65535));
+  auto kern = a.cache.D == 128 ? kv_join_kernel<128> : kv_join_kernel<64>;
+  return launch_kernel(kern, grid, dim3(256), 0, s, true, false, a);
+}
+
+}  // namespace moe

@@ -85,6 +85,7 @@ struct PartHead {
   int starts;      // workspace: 1 = the item starts in this CTA and ends in a later one
   int last_cta;    // the CTA of its last unit
   int E;           // O is in units of 2^(E - 127)
+  int part;        // KvRequest's
 };
 
 __host__ __device__ constexpr size_t part_floats(int cols, int D) { return (size_t)cols * D + 2 * cols; }
@@ -117,16 +118,17 @@ __device__ __forceinline__ long long divmod(long long a, int b, int& rem) {
   return q;
 }
 
-template <int COLS>
+template <int COLS, bool SHARED>
 __device__ __forceinline__ Req request(const StreamParams& p, int r) {
   const KvAttnArgs& a = p.a;
   Req q;
-  static_cast<KvRequest&>(q) = kv_request(a, r);
+  static_cast<KvRequest&>(q) = kv_request<SHARED>(a, r);
   const long long rows = (long long)max(q.ql, 0) * p.G;
-  const bool mine = rows > 0 && (rows <= p.row_limit || (p.odd && p.odd[r] != 0));
+  const int limit = SHARED && r >= a.R ? a.sh.row_limit : p.row_limit;
+  const bool mine = rows > 0 && (rows <= limit || (p.odd && p.odd[r] != 0));
   q.rt = mine ? (int)((rows + COLS - 1) / COLS) : 0;
   q.glo = kv_first_key(q.first, a.window) >> 4;
-  const int hi = a.causal ? min(q.n, max(0, q.first + q.ql)) : q.n;  // keys past the last row's are not looked at
+  const int hi = q.causal ? min(q.n, max(0, q.first + q.ql)) : q.n;  // keys past the last row's are not looked at
   q.ng = mine ? ((hi + 15) >> 4) - q.glo : 0;
   return q;
 }
@@ -370,24 +372,34 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Dims d .. d + 3 of output row ``row`` (token x query head): O (units of 2^(E - 127)) over the sum of weights.
-template <int D>
-__device__ __forceinline__ void store4(const KvAttnArgs& a, size_t row, int d, const float4& o, float l, int E) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  if (E != 127) {
+// Dims d .. d + 3 of output row ``row`` (token x query head): O (units of 2^(E - 127)) over the sum of
+// weights; with a shared prefix O itself, to part ``part``.
+template <int D, bool SHARED>
+__device__ __forceinline__ void store4(const KvAttnArgs& a, int part, size_t row, int d, const float4& o, float l, int E) {
+  if constexpr (SHARED) {
+    *reinterpret_cast<float4*>(a.sh.o + ((size_t)part * a.N * a.Hq + row) * D + d) = o;
+  } else {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    if (E != 127) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = mul_pow2(v[k], E - 127);
+      for (int k = 0; k < 4; ++k) v[k] = mul_pow2(v[k], E - 127);
+    }
+    *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
   }
-  *reinterpret_cast<uint2*>(a.out + row * D + d) = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
 }
 
-// lse from the sum of weights and their reference m (units of 4 log2).
-__device__ __forceinline__ void store_lse(const KvAttnArgs& a, size_t row, float l, float m) {
-  if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m == -INFINITY ? l : fmaf(m, 2.772588722239781f, lg2(l) * 0.6931471805599453f);
+// lse from the sum of weights and their reference m (units of 4 log2); with a shared prefix both, and E.
+template <bool SHARED>
+__device__ __forceinline__ void store_lse(const KvAttnArgs& a, int part, size_t row, float l, float m, int E) {
+  if constexpr (SHARED) {
+    a.sh.ml[(size_t)part * a.N * a.Hq + row] = make_float4(m, l, __int_as_float(E), 0.f);
+  } else {
+    if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m == -INFINITY ? l : fmaf(m, 2.772588722239781f, lg2(l) * 0.6931471805599453f);
+  }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kernel(const StreamParams p) {
   using C = StreamCfg<D, NT>;
   constexpr int NB = C::NB, W = C::kWarps, S = C::kStages, REC = C::kRec, COLS = C::kCols;
@@ -421,15 +433,16 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   // Up to 32 requests every warp finds its own place, one request a lane, and the
   // CTA does not meet before its pieces are merged; beyond, the CTA's threads scan
   // the requests together, a chunk at a time.
-  const bool few = a.R <= 32;
-  const int chunks = few ? 1 : (a.R + C::kThreads - 1) / C::kThreads;
+  const int R = SHARED ? a.R + a.sh.splits : a.R;
+  const bool few = R <= 32;
+  const int chunks = few ? 1 : (R + C::kThreads - 1) / C::kThreads;
   long long T = 0, U = 0;          // totals so far
   long long first_c = 0, first_u = 0;  // before this thread's request of the last chunk scanned
   Req mine{};
   auto scan = [&](int ch) {
     const int r = few ? lane : ch * C::kThreads + tid;
     mine = Req{};
-    if (r < a.R) mine = request<COLS>(p, r);
+    if (r < R) mine = request<COLS, SHARED>(p, r);
     const long long it = mine.items(H), c = it * (mine.ng + kItemCost), u = it * mine.ng;
     long long ic = c, iu = u;
 #pragma unroll
@@ -466,8 +479,13 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   };
   // requests without a key: their rows are zeros, written by one CTA each
   auto zero_rows = [&](int r) {
-    const Req q = request<COLS>(p, r);
+    const Req q = request<COLS, SHARED>(p, r);
     const long long rows = (long long)q.ql * a.Hq;
+    if constexpr (SHARED) {  // sums of nothing
+      for (long long i = tid; i < rows; i += C::kThreads)
+        store_lse<SHARED>(a, q.part, (size_t)q.qb * a.Hq + i, 0.f, -INFINITY, 127);
+      return;
+    }
     uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)q.qb * a.Hq * D);
     for (long long i = tid; i < rows * (D / 8); i += C::kThreads) o[i] = make_uint4(0, 0, 0, 0);
     if (a.lse)
@@ -538,7 +556,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       __syncthreads();
       if (tid <= wpc) {
         const long long b = begin_of(gw0 + tid), in = min(b, cost - 1);
-        const int n = min(C::kThreads, a.R - ch * C::kThreads);
+        const int n = min(C::kThreads, R - ch * C::kThreads);
         if (in >= before_c[0] && in < T) {  // (T: the cost up to this chunk's end)
           int lo = 0, hi = n;  // before_c[lo] <= in, the last such: requests that cost nothing share a value
           while (hi - lo > 1) {
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
           }
           at_r[tid] = ch * C::kThreads + lo;
           at_cost[tid] = before_c[lo];
-          place(b, request<COLS>(p, at_r[tid]).ng, before_c[lo], before_u[lo], at_item[tid], at_g[tid], at_unit[tid]);
+          place(b, request<COLS, SHARED>(p, at_r[tid]).ng, before_c[lo], before_u[lo], at_item[tid], at_g[tid], at_unit[tid]);
         }
       }
       __syncthreads();
@@ -566,7 +584,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
   const int n_units = (int)(u_hi - u_lo);
   if (n_units > 0) {
     // record addresses, 32 units at a time, one per lane; null for a page outside the cache
-    Req q = request<COLS>(p, br);
+    Req q = request<COLS, SHARED>(p, br);
     int cr = br;
     long long bo = (long long)citem * q.ng + cg;  // units of request br before the next batch
     auto addresses = [&](int i0) -> const uint8_t* {
@@ -574,19 +592,18 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       int r = br;
       long long off = bo + lane;
       if (i0 + lane < n_units) {
-        Req q = request<COLS>(p, r);
+        Req q = request<COLS, SHARED>(p, r);
         long long u = (long long)q.items(H) * q.ng;
         while (off >= u) {
           off -= u;
-          q = request<COLS>(p, ++r);
+          q = request<COLS, SHARED>(p, ++r);
           u = (long long)q.items(H) * q.ng;
         }
         int gi;
         const int item = (int)divmod(off, q.ng, gi);
         const int tok = (q.glo + gi) << 4;
-        const int pg = a.table[(size_t)r * a.max_blocks + (tok >> a.cache.page_shift)];
-        if (pg >= 0 && pg < a.cache.num_pages)
-          ptr = a.cache.data + a.cache.record(pg, item / q.rt, (tok & ((1 << a.cache.page_shift) - 1)) >> 4);
+        const int pg = kv_page<SHARED>(a, q, r, tok);
+        if (pg >= 0 && pg < a.cache.num_pages) ptr = a.cache.data + a.cache.record(pg, item / q.rt, kv_group<SHARED>(a, q, tok));
       }
       // the next 32 start after lane 31's
       br = __shfl_sync(0xffffffffu, r, 31);
@@ -621,7 +638,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       // ------------------------------------------------------------ next item
       while (citem >= q.items(H)) {
         ccost += (long long)q.items(H) * (q.ng + kItemCost);
-        q = request<COLS>(p, ++cr);
+        q = request<COLS, SHARED>(p, ++cr);
         citem = 0;
       }
       const int g0 = cg;
@@ -721,7 +738,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
       auto sees = [&](int c, int& lo, int& hi) {
         const int pos = q.first + c / p.G;
         const bool real = c < q.ql * p.G;
-        hi = real && a.causal ? min(q.n, pos + 1) : q.n;
+        hi = real && q.causal ? min(q.n, pos + 1) : q.n;
         lo = real ? kv_first_key(pos, a.window) : 0;
       };
       int lo_max = 0, hi_min = q.n;  // over the tile's rows: the last sees the latest first key, the first the fewest
@@ -1093,10 +1110,10 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
               const size_t at = (size_t)(q.qb + row) * a.Hq + hq;
 #pragma unroll
               for (int b = 0; b < NB; ++b)
-                store4<D>(a, at, 32 * b + 4 * g,
+                store4<D, SHARED>(a, q.part, at, 32 * b + 4 * g,
                           make_float4(A.o[nt][b][0][c], A.o[nt][b][0][2 + c], A.o[nt][b][1][c], A.o[nt][b][1][2 + c]),
                           A.l[nt][c], A.E);
-              if (g == 0) store_lse(a, at, A.l[nt][c], A.m[nt][c]);
+              if (g == 0) store_lse<SHARED>(a, q.part, at, A.l[nt][c], A.m[nt][c], A.E);
             }
           }
       } else {
@@ -1121,7 +1138,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         if (lane == 0)
           ph[2 * warp + (last ? 1 : 0)] =
               PartHead{item, q.ng, q.qb, q.ql * p.G, kvh * p.G, rt * COLS, 0,
-                       cta_of(ccost + (long long)(citem - 1) * (q.ng + kItemCost) + kItemCost + q.ng - 1), A.E};
+                       cta_of(ccost + (long long)(citem - 1) * (q.ng + kItemCost) + kItemCost + q.ng - 1), A.E, q.part};
       }
     }
     if (!alive) {
@@ -1194,8 +1211,8 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
         const int row = c / p.G;
         const size_t dst = (size_t)(h.qb + row) * a.Hq + h.hq0 + c - row * p.G;
 #pragma unroll
-        for (int d = 0; d < N; ++d) store4<D>(a, dst, 4 * x8 + 32 * d, o[d], l, E);
-        if (x8 == 0) store_lse(a, dst, l, m);
+        for (int d = 0; d < N; ++d) store4<D, SHARED>(a, h.part, dst, 4 * x8 + 32 * d, o[d], l, E);
+        if (x8 == 0) store_lse<SHARED>(a, h.part, dst, l, m, E);
       }
     } else {
       const int slot = h.item <= cta_lo ? 0 : 1;
@@ -1219,7 +1236,7 @@ __global__ void __launch_bounds__(StreamCfg<D, NT>::kThreads, 1) kv_stream_kerne
 // Items cut between CTAs: block (c, col) joins row ``col`` of the item that
 // starts in CTA c and ends in a later one, from the parts of every CTA it
 // reaches, in order.
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
   using C = StreamCfg<D, NT>;
   constexpr int COLS = C::kCols;
@@ -1280,21 +1297,21 @@ __global__ void __launch_bounds__(128) kv_merge_kernel(const StreamParams p) {
     }
     const int row = cc / p.G;
     const size_t dst = (size_t)(h.qb + row) * p.a.Hq + h.hq0 + cc - row * p.G;
-    store4<D>(p.a, dst, 4 * x, o, l, E);
-    if (x == 0) store_lse(p.a, dst, l, m);
+    store4<D, SHARED>(p.a, h.part, dst, 4 * x, o, l, E);
+    if (x == 0) store_lse<SHARED>(p.a, h.part, dst, l, m, E);
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 cudaError_t launch_stream(const StreamParams& p, cudaStream_t s) {
   using C = StreamCfg<D, NT>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_shared(kv_stream_kernel<D, NT>, C::kSmem, done);
+  cudaError_t e = allow_shared(kv_stream_kernel<D, NT, SHARED>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   const int grid = p.max_ctas;
-  e = launch_kernel(kv_stream_kernel<D, NT>, dim3(grid), dim3(C::kThreads), C::kSmem, s, false, false, p);
+  e = launch_kernel(kv_stream_kernel<D, NT, SHARED>, dim3(grid), dim3(C::kThreads), C::kSmem, s, false, false, p);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kv_merge_kernel<D, NT>, dim3(grid, C::kCols), dim3(128), 0, s, true, false, p);
+  return launch_kernel(kv_merge_kernel<D, NT, SHARED>, dim3(grid, C::kCols), dim3(128), 0, s, true, false, p);
 }
 
 constexpr int kMaxStreamCtas = 256;
@@ -1315,8 +1332,12 @@ cudaError_t launch_kv_stream(const KvAttnArgs& a, int row_limit, const int32_t* 
   p.max_ctas = a.num_sms < kMaxStreamCtas ? a.num_sms : kMaxStreamCtas;
   p.heads = reinterpret_cast<PartHead*>(ws);
   p.parts = reinterpret_cast<float*>(ws + sizeof(PartHead) * 2 * kMaxStreamCtas);
-  if (a.cache.D == 128) return tiles == 1 ? launch_stream<128, 1>(p, s) : launch_stream<128, 2>(p, s);
-  return tiles == 1 ? launch_stream<64, 1>(p, s) : launch_stream<64, 2>(p, s);
+  if (a.sh.splits > 0) {
+    if (a.cache.D == 128) return tiles == 1 ? launch_stream<128, 1, true>(p, s) : launch_stream<128, 2, true>(p, s);
+    return tiles == 1 ? launch_stream<64, 1, true>(p, s) : launch_stream<64, 2, true>(p, s);
+  }
+  if (a.cache.D == 128) return tiles == 1 ? launch_stream<128, 1, false>(p, s) : launch_stream<128, 2, false>(p, s);
+  return tiles == 1 ? launch_stream<64, 1, false>(p, s) : launch_stream<64, 2, false>(p, s);
 }
 
 }  // namespace moe

@@ -157,6 +157,23 @@ def _rows(x, name, cache, N, dtypes):
     return st[0] if N > 1 else H * D
 
 
+def _queries(q, cache, dtype):
+    """Checks queries [N, Hq, head_dim] with any token stride; returns N, Hq and that stride in elements."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dtype != dtype:
+        raise TypeError(f"q must be {dtype}, got {q.dtype}")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must have shape [N, Hq, {cache.head_dim}], got {tuple(q.shape)}")
+    if q.device != cache.device:
+        raise ValueError(f"q must be on {cache.device}, got {q.device}")
+    N, Hq, D = q.shape
+    st = q.stride()
+    if st[2] != 1 or (Hq > 1 and st[1] != D):
+        raise ValueError("q: a token's heads must be dense")
+    return N, Hq, st[0] if N > 1 else Hq * D
+
+
 def kv_append_mxfp4(cache: KvCacheMxfp4, k, v, slots, stream=None) -> None:
     """Quantise ``k``, ``v`` [N, kv heads, head_dim] (bf16 or float32; token rows may be strided, as slices of a
     fused projection) and write them to ``slots`` int32 [N] (-1: not written)."""
@@ -210,18 +227,8 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     and to learn of waits that ran out (``attention_read_status``): those of a
     workspace made here go unseen."""
     dev = cache.device
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q must be torch.bfloat16, got {q.dtype}")
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError(f"q must have shape [N, Hq, {cache.head_dim}], got {tuple(q.shape)}")
-    if q.device != dev:
-        raise ValueError(f"q must be on {dev}, got {q.device}")
-    N, Hq, D = q.shape
-    st = q.stride()
-    if st[2] != 1 or (Hq > 1 and st[1] != D):
-        raise ValueError("q: a token's heads must be dense")
+    N, Hq, q_stride = _queries(q, cache, torch.bfloat16)
+    D = cache.head_dim
     R = seq_lens.shape[0]
     if block_table.dim() != 2:
         raise ValueError("block_table must be [R, max_blocks]")
@@ -236,7 +243,7 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
     # (a window past the C ABI's int hides nothing: no request has that many keys)
-    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, min(window, 2 ** 31 - 1), st[0] if N > 1 else Hq * D,
+    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, min(window, 2 ** 31 - 1), q_stride,
                      D ** -0.5 if scale is None else scale)
     lib = _native.load()
     ref = ctypes.byref(a)

@@ -126,3 +126,61 @@ def test_rope_overlap(native, other):
     for p in (at[other], last):
         assert rope(native, {"q_out": p}) == OVERLAP
         assert rope(native, data=p) == OVERLAP
+
+
+# ------------------------------------------------------------------ shared prefix
+
+SHARED_NAMES = ("q", "shared", "len", "table", "lens", "start", "out", "lse", "ws")
+
+
+def shared(native, at=None, cache=(8, 16, 2, 64), data=64 << 20, size=None, blocks=3, **kw):
+    a = native.KvAttnStruct(**{**dict(R=2, N=4, Hq=8, max_blocks=5, max_q_len=2, causal=1, window=0, q_stride=512, scale=0.1), **kw})
+    c = native.KvCacheStruct(data, *cache)
+    p = {k: (i + 1) << 20 for i, k in enumerate(SHARED_NAMES)}
+    p.update(at or {})
+    if size is None:
+        size = 1 << 40
+    return native.load().kv_mxfp4_attention_shared(ctypes.byref(c), ctypes.byref(a), blocks, *(p[k] for k in SHARED_NAMES), size, None)
+
+
+def shared_workspace(native, blocks=3, **kw):
+    a = native.KvAttnStruct(**{**dict(R=2, N=4, Hq=8, max_blocks=5, max_q_len=2, causal=1, window=0, q_stride=512, scale=0.1), **kw})
+    c = native.KvCacheStruct(None, 8, 16, 2, 64)
+    return native.load().kv_mxfp4_attention_shared_workspace_bytes(ctypes.byref(c), ctypes.byref(a), blocks)
+
+
+def test_shared_refusals(native):
+    for kw in (dict(R=-1), dict(N=-1), dict(Hq=7), dict(max_blocks=0), dict(max_q_len=-1), dict(causal=2), dict(window=4), dict(blocks=0),
+               dict(blocks=1 << 27), dict(q_stride=504), dict(scale=float("inf"))):
+        assert shared(native, **kw) == DIMS, kw
+        assert shared_workspace(native, **kw) == 0, kw
+    assert shared(native, cache=(8, 20, 2, 64)) == DIMS
+    for k in SHARED_NAMES:
+        if k != "lse":
+            assert shared(native, {k: None}) == NULL, k
+    for k, off in (("q", 8), ("shared", 2), ("len", 2), ("table", 2), ("lens", 2), ("start", 2), ("out", 8), ("lse", 2), ("ws", 128)):
+        assert shared(native, {k: (32 << 20) + off}) == ALIGN, k
+    need = shared_workspace(native)
+    assert need > 0 and shared(native, size=need - 1) == WORKSPACE
+    for kw in (dict(R=0), dict(N=0), dict(max_q_len=0)):
+        assert shared(native, {k: None for k in SHARED_NAMES}, **kw) == 0
+
+
+def test_shared_overlap(native):
+    size = dict(q=2 * 4 * 512, shared=12, len=4, table=40, lens=8, start=12, data=8 * 2 * 17 * 64, out=2 * 4 * 512, lse=4 * 32,
+                ws=shared_workspace(native))
+    at = {k: (i + 1) << 24 for i, k in enumerate(size)}
+    for out in ("out", "lse", "ws"):
+        for other in size:
+            if out == other:
+                continue
+            for p in (at[other], at[other] + (size[other] - 1) // 256 * 256):
+                x = {**at, out: p}
+                data = x.pop("data")
+                assert shared(native, x, data=data, size=size["ws"]) == OVERLAP, (out, other)
+
+
+def test_shared_workspace_grows_with_rows_and_slices(native):
+    few, many = shared_workspace(native, N=2), shared_workspace(native, N=64, R=64)
+    assert many - few >= (64 - 2) * 8 * 64 * 4 * 2
+    assert shared_workspace(native, N=64, R=64, blocks=4000) > many
