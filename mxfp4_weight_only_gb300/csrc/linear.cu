@@ -175,6 +175,8 @@ cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
   return launch_stream<4, 2>(a, s);
 }
 
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) { return launch_linear_stream(a, s); }
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  return a.T <= 32 ? launch_linear_stream(a, s) : launch_linear_tc(a, s);
+}
 
 }  // namespace moe

@@ -26,6 +26,9 @@ struct LinearArgs {
 // Few rows: the weight is streamed once (linear.cu).
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s);
 
+// Many rows: tensor cores (linear_tc.cu).
+cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s);
+
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -60,9 +60,8 @@
 //               global stores
 // Tensor memory per CTA (256 columns): two (gate_up) or four (down) 32-column
 // weight stages, then one accumulator of 192 (gate_up) or 128 (down) columns.
-#include <cuda.h>
-
 #include "common.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 
@@ -196,14 +195,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&c)[4]) {
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
 
 __device__ __forceinline__ void red_add(float* addr, float v) {
   asm volatile("red.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
@@ -858,39 +849,6 @@ __global__ void __launch_bounds__(256) cast_out_kernel(const float* __restrict__
 
 // ------------------------------------------------------------------ host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t get_encoder(EncodeTiledFn* fn) {
-  static EncodeTiledFn cached = nullptr;
-  if (!cached) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr) return e != cudaSuccess ? e : cudaErrorNotSupported;
-    cached = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  *fn = cached;
-  return cudaSuccess;
-}
-
-// 16-bit [rows][K] row-major (bf16 or f16), box_rows x 64 boxes with 128-byte swizzle.
-cudaError_t make_act_map(CUtensorMap* m, const void* base, long long rows, int K, int box_rows, bool f16) {
-  EncodeTiledFn enc;
-  cudaError_t e = get_encoder(&enc);
-  if (e != cudaSuccess) return e;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kTcK, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                         const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <WeightKind KIND, bool GATE_UP>
 cudaError_t launch_tc(const CUtensorMap& map, const TcParams& p, int grid, cudaStream_t s) {
   const size_t smem = (size_t)TcLayout<GATE_UP>::kSmemBytes;
@@ -906,9 +864,9 @@ cudaError_t launch_tc(const CUtensorMap& map, const TcParams& p, int grid, cudaS
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s) {
   const long long P = (long long)a.T * a.topk;
   CUtensorMap map_x, map_a;
-  cudaError_t e = make_act_map(&map_x, a.xs, P, a.H, kTcRowsUp, false);
+  cudaError_t e = make_rows_map(&map_x, a.xs, P, a.H, a.H, kTcRowsUp, false);
   if (e != cudaSuccess) return e;
-  e = make_act_map(&map_a, a.a16, P, a.I, kTcRowsDown, true);
+  e = make_rows_map(&map_a, a.a16, P, a.I, a.I, kTcRowsDown, true);
   if (e != cudaSuccess) return e;
 
   timing_mark(1, false, s);
