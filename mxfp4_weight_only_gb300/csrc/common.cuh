@@ -251,41 +251,6 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two exact E2M1 values as f16 (one packed byte) -> the same values times
-// 2^-112 as bf16: the f16 exponent field and mantissa bit move down 3 bits
-// into the bf16 layout, sign kept, zero stays zero.
-__device__ __forceinline__ uint32_t f16pair_to_bf16_rebias(uint32_t h) {
-  return ((h >> 3) & 0x0FFF0FFFu) | (h & 0x80008000u);
-}
-
-// 32 E2M1 values (16 packed bytes) of one block with E8M0 scale s -> 16 words
-// of two bf16 (K order, lower element in the low half), exact.
-__device__ __forceinline__ void dequant_block(const uint4& q, uint32_t s, uint4 (&out)[4]) {
-  // value * 2^-112 * 2^(s-15) = value * 2^(s-127); 2^(s-15) is a normal bf16 for s <= 142
-  const bool big = s > 142u;
-  const uint32_t e1 = big ? 127u + 127u : s - 15u + 127u;
-  const uint32_t f1 = (e1 << 7) | (e1 << 23);
-  const uint32_t e2 = big ? s - 142u + 127u : 127u;
-  const uint32_t f2 = (e2 << 7) | (e2 << 23);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h0, h1, h2, h3;
-    e2m1x8_to_f16x8(w[i], h0, h1, h2, h3);
-    uint32_t b0 = bf16x2_mul(f16pair_to_bf16_rebias(h0), f1);
-    uint32_t b1 = bf16x2_mul(f16pair_to_bf16_rebias(h1), f1);
-    uint32_t b2 = bf16x2_mul(f16pair_to_bf16_rebias(h2), f1);
-    uint32_t b3 = bf16x2_mul(f16pair_to_bf16_rebias(h3), f1);
-    if (big) {
-      b0 = bf16x2_mul(b0, f2);
-      b1 = bf16x2_mul(b1, f2);
-      b2 = bf16x2_mul(b2, f2);
-      b3 = bf16x2_mul(b3, f2);
-    }
-    out[i] = make_uint4(b0, b1, b2, b3);
-  }
-}
-
 // Pack two floats into f16x2 (lo in the low half), round to nearest even.
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
   uint32_t r;

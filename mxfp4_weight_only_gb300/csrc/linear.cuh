@@ -33,12 +33,22 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
 
-// 32 weights of a block as 16 words of two bf16, NaN for scale byte 255.
+// 32 weights of a block as 16 words of two bf16, exact: codes to f16 pairs, each
+// value to float32 (on the multiply-add pipe), whose upper halves are the bf16 values,
+// put together by a byte permute, times 2^(s-127) (s = 0: subnormal; 255: NaN).  The
+// ALU pipe, which the conversions and permutes share, bounds the tensor-core kernel's
+// converters.
 __device__ __forceinline__ void linear_block(const uint4& q, uint32_t s, uint4 (&out)[4]) {
-  dequant_block(q, s, out);
-  if (s == 255u) {
+  const uint32_t f = s == 0u ? 0x00400040u : s == 255u ? 0x7FFF7FFFu : s * 0x00800080u;
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[4], o[4];
+    e2m1x8_to_f16x8(w[i], h[0], h[1], h[2], h[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = bf16x2_mul(prmt(__float_as_uint(f16_lo(h[k])), __float_as_uint(f16_hi(h[k])), 0x7632u), f);
+    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -59,6 +69,32 @@ __device__ __forceinline__ void linear_store(const LinearArgs& a, int token, int
   const size_t at = (size_t)token * a.out_stride + col;
   if (a.f32) reinterpret_cast<float*>(a.out)[at] = v;
   else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16_bits(v);
+}
+
+// Residual and store of N activated values of column ``col``, of tokens tok, tok + STEP, ..
+template <int N, int STEP>
+__device__ __forceinline__ void linear_store_column(const LinearArgs& a, int tok, int col, float (&h)[N]) {
+  const int left = (a.T - tok + STEP - 1) / STEP;  // tokens that exist
+  if (a.res) {
+    const uint16_t* src = a.res + (size_t)tok * a.res_stride + col;
+    uint16_t r[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = k < left ? src[(size_t)(k * STEP) * a.res_stride] : (uint16_t)0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) h[k] += __uint_as_float((uint32_t)r[k] << 16);
+  }
+  const size_t at = (size_t)tok * a.out_stride + col;
+  if (a.f32) {
+    float* dst = reinterpret_cast<float*>(a.out) + at;
+#pragma unroll
+    for (int k = 0; k < N; ++k, dst += STEP * a.out_stride)
+      if (k < left) *dst = h[k];
+  } else {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+    for (int k = 0; k < N; ++k, dst += STEP * a.out_stride)
+      if (k < left) *dst = f32_to_bf16_bits(h[k]);
+  }
 }
 
 #endif

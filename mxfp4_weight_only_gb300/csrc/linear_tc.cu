@@ -15,11 +15,16 @@
 // columns, so that one warp holds both.
 //
 // Warps of a CTA:
-//   0 - 3   epilogue: a thread a row of D; bias, activation, residual, store
-//   4 - 11  converters, in two groups of four warps that take turns: a thread a row of
-//           the weight, both blocks of 32 of a step, loaded kAhead of its turns ahead
-//   12      TMA of the x tiles
-//   13      MMAs (first CTA); in the second it tells the first that a stage is full
+//   0 - 7   epilogue: a thread a row of D, two warps sharing its tokens; bias, activation,
+//           residual, store
+//   8 - 23  converters, in four groups of four warps that take turns: a thread a row of
+//           the weight, both blocks of 32 of a step
+//   24      TMA of the x tiles
+//   25      MMAs (first CTA)
+//   26      TMA of the packed weight, four steps (256 of K) at a time
+// Packed weights come by TMA because loads into registers ahead of their use do not
+// outlive the proxy fence that a converter needs each step, and because rows
+// 1,792 bytes apart cost a wavefront of the load unit each.
 // Two accumulators of 256 columns: the epilogue of one tile runs beside the MMAs of
 // the next.  Clusters walk over the tiles, weight tiles innermost.
 #include <algorithm>
@@ -37,28 +42,33 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEpiWarps = 4, kConvWarp = 4, kTmaWarp = 12, kMmaWarp = 13;
-constexpr int kTcThreads = 32 * 14;
+constexpr int kGroups = 4;              // of converter warps
+constexpr int kEpiWarps = 8, kConvWarp = kEpiWarps, kConvWarps = 4 * kGroups;
+constexpr int kTmaWarp = kConvWarp + kConvWarps, kMmaWarp = kTmaWarp + 1, kRawWarp = kTmaWarp + 2;
+constexpr int kTcThreads = 32 * (kRawWarp + 1);
 constexpr int kRows = 128;              // rows of the weight a CTA
 constexpr int kABytes = kRows * 128;    // one step of them in bf16
-constexpr int kAhead = 3;               // converter turns whose packed weights are on their way
+constexpr int kQuad = 4;                // steps of a load of packed weights
+constexpr int kRawStages = 3, kRawBytes = kRows * 128, kRawRows = 16;
 constexpr uint32_t kAccCols = 256, kCols = 512;
 
 template <int BN>
 struct TcCfg {
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 7 : 8;
   static constexpr int kBBytes = BN / 2 * 128;
   static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kBarOff = kStages * kStage;
+  static constexpr int kRawOff = kStages * kStage;
+  static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
   static constexpr int kSmem = 1024 + kBarOff + 512;
   static_assert(kBBytes % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
 };
 
 template <int S>
 struct TcShared {
-  uint64_t a_full[S], b_full[S];  // this CTA's weights, x tile of a stage
-  uint64_t peer_full[S];          // first CTA: both of the second
-  uint64_t empty[S];              // the stage's MMAs are done
+  uint64_t b_full[S];  // this CTA's x tile of a stage
+  uint64_t full[S];    // first CTA: weights and x tiles of both
+  uint64_t empty[S];   // the stage's MMAs are done
+  uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // packed weights of four steps
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_slot;
@@ -77,11 +87,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Arrives on the barrier at the same place in CTA ``rank`` of the cluster.
+// Arrives on the barrier at the same place in CTA ``rank`` of the cluster.  What an
+// arrival stands for here is shared memory that the MMAs read, or tensor memory: writes
+// that a proxy fence or a tcgen05 fence before it has ordered.  It publishes no other writes, so
+// it has no release at cluster scope (one such a step, 1 us, is what a step took).
 __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
   asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar)),
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(
+          smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
@@ -177,7 +190,8 @@ __device__ __forceinline__ int weight_row(const LinearArgs& a, int mt, int rank,
 }
 
 template <int BN>
-__global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map, const LinearTc p) {
+__global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map,
+                                                                  const __grid_constant__ CUtensorMap wmap, const LinearTc p) {
   using C = TcCfg<BN>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -187,15 +201,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
   const LinearArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = cluster_rank(), cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const int KB = a.K >> 5, KS = (KB + 1) >> 1;  // blocks of 32, steps of 64
+  const int KB = a.K >> 5, KS = (KB + 1) >> 1, KQ = (KS + kQuad - 1) / kQuad;  // blocks of 32, steps of 64, quads of steps
   const uint64_t limit = a.wait.limit_ns;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&sh.a_full[s], 4);
-      mbar_init(&sh.b_full[s], 1 + a.wait.extra_waiters);
-      mbar_init(&sh.peer_full[s], 1);
+      mbar_init(&sh.b_full[s], 1);
+      mbar_init(&sh.full[s], 2 * 4 + a.wait.extra_waiters);  // a group's warps in both CTAs
       mbar_init(&sh.empty[s], 1);
+    }
+    for (int s = 0; s < kRawStages; ++s) {
+      mbar_init(&sh.raw_full[s], 1);
+      mbar_init(&sh.raw_empty[s], kConvWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.acc_full[b], 1);
@@ -220,114 +237,116 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
 
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue: thread = row of D
+    const int quad = warp & 3, half = warp >> 2;
+    const bool gated = a.act == LINEAR_ACT_SWIGLU;
     int it = 0;
     for (int tile = cluster; tile < p.tiles; tile += clusters, ++it) {
       const int buf = it & 1, mt = tile % p.m_tiles;
       int t0;
       const int n = tokens(tile, t0);
-      const int row = weight_row(a, mt, rank, tid);
-      const bool gated = a.act == LINEAR_ACT_SWIGLU;
+      const int row = weight_row(a, mt, rank, 32 * quad + lane);
       const float bias = row >= 0 ? linear_bias(a, row) : 0.f;
-      if (!wait_cluster(&sh.acc_full[buf], (it >> 1) & 1, a.status, limit, &sh.abort_flag)) {
+      if (!mbar_wait_warp(&sh.acc_full[buf], (it >> 1) & 1, a.status, limit, &sh.abort_flag)) {
         sh.abort_flag = 1;
         break;
       }
       tc_after();
-      const uint32_t src = tmem + ((uint32_t)(32 * warp) << 16) + kAccCols * buf;
-      for (int c = 0; c < n; c += 32) {
+      const uint32_t src = tmem + ((uint32_t)(32 * quad) << 16) + kAccCols * buf;
+      auto release = [&]() {  // this warp has read its part of the accumulator
+        tc_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(&sh.acc_empty[buf], 0);
+      };
+      if (32 * half >= n) release();
+      for (int c = 32 * half; c < n; c += 64) {
         uint32_t v[32];
         tmem_ld32(src + c, v);
-        if (c + 32 >= n) {  // the accumulator has been read
-          tc_before();
-          __syncwarp();
-          if (lane == 0) arrive_at(&sh.acc_empty[buf], 0);
-        }
-        const int tok = t0 + c;
+        if (c + 64 >= n) release();
         if (gated) {
+          // lanes of gate rows take the even tokens, those of up rows the odd ones
           const bool up = lane & 16;
-          const int col = row < 0 ? -1 : up ? row - a.cols : row;
+          float h[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float x0 = __uint_as_float(v[k]) + bias, x1 = __uint_as_float(v[k + 1]) + bias;
+          for (int k = 0; k < 16; ++k) {
+            const float x0 = __uint_as_float(v[2 * k]) + bias, x1 = __uint_as_float(v[2 * k + 1]) + bias;
             const float theirs = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 16);
-            const float h = up ? silu(theirs) * x1 : silu(x0) * theirs;
-            const int t = tok + k + (up ? 1 : 0);
-            if (col >= 0 && t < a.T) linear_store(a, t, col, h);
+            h[k] = silu(up ? theirs : x0) * (up ? x1 : theirs);
           }
+          if (row >= 0) linear_store_column<16, 2>(a, t0 + c + (up ? 1 : 0), up ? row - a.cols : row, h);
         } else if (row >= 0) {
+          float h[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (tok + k < a.T) linear_store(a, tok + k, row, linear_act(a.act, __uint_as_float(v[k]) + bias));
+          for (int k = 0; k < 32; ++k) h[k] = __uint_as_float(v[k]) + bias;
+          if (a.act == LINEAR_ACT_SILU) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) h[k] = silu(h[k]);
+          } else if (a.act == LINEAR_ACT_GELU) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) h[k] = linear_act(LINEAR_ACT_GELU, h[k]);
+          }
+          linear_store_column<32, 1>(a, t0 + c, row, h);
         }
       }
     }
   } else if (warp < kTmaWarp) {
     // ---------------------------------------------------------------- converters: thread = row of the weight
     const int group = (warp - kConvWarp) >> 2, i = (tid - 32 * kConvWarp) & 127;
-    // a place in the walk over (tile, step), steps counted over all tiles; this group takes every second one
-    struct Place {
-      int tile, step;
+    auto row_scales = [&](int tile) -> const uint8_t* {
+      const int row = tile < p.tiles ? weight_row(a, tile % p.m_tiles, rank, i) : -1;
+      return row < 0 ? nullptr : a.ws + (size_t)row * KB;
     };
-    auto next = [&](Place& q) {
-      q.step += 2;
-      while (q.step >= KS) {
-        q.step -= KS;
-        q.tile += clusters;
-      }
+    const bool wide = (((uintptr_t)a.ws | (uintptr_t)KB) & 1) == 0;
+    // The scale bytes of this thread's two blocks of a quad.
+    auto scales = [&](const uint8_t* src, int quad) -> uint32_t {
+      const int b = 8 * quad + 2 * group;
+      if (!src || b >= KB) return 0x7F7Fu;
+      src += b;
+      if (wide) return __ldg(reinterpret_cast<const uint16_t*>(src));
+      return (uint32_t)__ldg(src) | (b + 1 < KB ? (uint32_t)__ldg(src + 1) << 8 : 0x7F00u);
     };
-    Place load{cluster, group}, at{cluster, group};
-    while (load.step >= KS) {
-      load.step -= KS;
-      load.tile += clusters;
-    }
-    at = load;
-    uint4 q[kAhead][2];
-    uint32_t sc[kAhead][2];
-    auto fetch = [&](int u) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        q[u][b] = make_uint4(0u, 0u, 0u, 0u);
-        sc[u][b] = 127u;
-      }
-      if (load.tile < p.tiles) {
-        const int row = weight_row(a, load.tile % p.m_tiles, rank, i);
-        if (row >= 0) {
-          const size_t first = (size_t)row * KB + 2 * load.step;
+    const uint8_t* here = row_scales(cluster);
+    uint32_t sc = scales(here, 0);
+    bool ok = true;
+    int gs0 = 0, gq = 0;  // steps before this quad, quads
+    for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
+      const uint8_t* after = row_scales(tile + clusters);
+      for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
+        const int r = gq % kRawStages, steps = min(kQuad, KS - kQuad * quad);
+        const int gs = gs0 + group, s = gs % S;
+        const bool mine = group < steps;
+        // (probes now, waits where they failed: the round trips pass beside the conversion)
+        const bool free_now = !mine || gs < S || mbar_try_wait(&sh.empty[s], ((gs / S) - 1) & 1);
+        const bool x_there = !mine || (warp & 3) != 0 || mbar_try_wait(&sh.b_full[s], (gs / S) & 1);
+        ok = mbar_wait_warp(&sh.raw_full[r], (gq / kRawStages) & 1, a.status, limit, &sh.abort_flag);
+        uint4 w[2][4];
+        if (mine) {
+          const uint8_t* raw = smem + C::kRawOff + r * kRawBytes + i * 128;
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            if (2 * load.step + b < KB) {
-              q[u][b] = __ldg(reinterpret_cast<const uint4*>(a.w) + first + b);
-              sc[u][b] = __ldg(a.ws + first + b);
-            }
+            linear_block(*reinterpret_cast<const uint4*>(raw + (((2 * group + b) ^ (i & 7)) << 4)), (sc >> (8 * b)) & 255u, w[b]);
         }
-      }
-      next(load);
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) fetch(u);
-    bool ok = true;
-    for (int gs = group; at.tile < p.tiles && ok;) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (at.tile >= p.tiles || !ok) break;
-        uint4 w[2][4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) linear_block(q[u][b], sc[u][b], w[b]);
-        fetch(u);
-        const int s = gs % S;
-        if (gs >= S) ok = wait_cluster(&sh.empty[s], ((gs / S) - 1) & 1, a.status, limit, &sh.abort_flag);
-        if (!ok) break;
-        uint8_t* dst = smem + s * C::kStage + i * 128;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(dst + (((4 * b + k) ^ (i & 7)) << 4)) = w[b][k];
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.a_full[s]);
-        gs += 2;
-        next(at);
+        if (lane == 0) mbar_arrive(&sh.raw_empty[r]);
+        if (mine) {
+          if (ok && !__all_sync(0xffffffffu, free_now))
+            ok = mbar_wait_warp(&sh.empty[s], ((gs / S) - 1) & 1, a.status, limit, &sh.abort_flag);
+          if (!ok) break;
+          uint8_t* dst = smem + s * C::kStage + i * 128;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(dst + (((4 * b + k) ^ (i & 7)) << 4)) = w[b][k];
+          fence_proxy_async_smem();
+          // one warp of the group answers for the x tile as well
+          if ((warp & 3) == 0 && !__all_sync(0xffffffffu, x_there))
+            ok = mbar_wait_warp(&sh.b_full[s], (gs / S) & 1, a.status, limit, &sh.abort_flag);
+          __syncwarp();
+          if (ok && lane == 0) arrive_at(&sh.full[s], 0);
+        }
+        sc = quad + 1 < KQ ? scales(here, quad + 1) : scales(after, 0);
+        gs0 += steps;
       }
+      here = after;
     }
     if (!ok) sh.abort_flag = 1;
   } else if (warp == kTmaWarp) {
@@ -353,24 +372,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       }
     }
     __syncwarp();
+  } else if (warp == kRawWarp) {
+    // ---------------------------------------------------------------- packed weights, 16 rows a copy
+    if (lane == 0) {
+      int gq = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
+        const int mt = tile % p.m_tiles;
+        for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
+          const int r = gq % kRawStages;
+          if (gq >= kRawStages) ok = sh.abort_flag == 0 && mbar_wait(&sh.raw_empty[r], ((gq / kRawStages) - 1) & 1, a.status, limit);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&sh.raw_full[r], kRawBytes);
+#pragma unroll
+          for (int k = 0; k < kRows / kRawRows; ++k) {
+            const int row = a.act == LINEAR_ACT_SWIGLU ? mt * 128 + rank * 64 + (k >> 1) * 16 + (k & 1) * a.cols
+                                                       : mt * 256 + rank * 128 + k * 16;
+            tma_load_2d(smem + C::kRawOff + r * kRawBytes + k * kRawRows * 128, &wmap, 128 * quad, row, &sh.raw_full[r]);
+          }
+        }
+      }
+      if (!ok) {
+        sh.abort_flag = 1;
+        for (int k = max(0, gq - kRawStages); k < gq; ++k) mbar_wait(&sh.raw_full[k % kRawStages], (k / kRawStages) & 1, a.status, limit);
+      }
+    }
+    __syncwarp();
   } else if (rank == 0) {
     // ---------------------------------------------------------------- MMAs
     // (the whole warp runs the loop on uniform values, one lane issues)
     const uint64_t da = sw128(smem_u32(smem));
     const uint32_t a_lo = (uint32_t)da, hi = (uint32_t)(da >> 32);
-    int gs = 0, it = 0;
-    bool ok = true;
+    int s = 0, it = 0;
+    uint32_t par = 0;
+    bool ok = true, there = false;
     for (int tile = cluster; tile < p.tiles && ok; tile += clusters, ++it) {
       const int buf = it & 1;
       int t0;
       const uint32_t id = idesc(tokens(tile, t0)), d = tmem + kAccCols * buf;
       if (it >= 2) ok = wait_cluster(&sh.acc_empty[buf], ((it >> 1) - 1) & 1, a.status, limit, &sh.abort_flag);
-      for (int step = 0; step < KS && ok; ++step, ++gs) {
-        const int s = gs % S;
-        const uint32_t par = (gs / S) & 1;
-        ok = wait_cluster(&sh.b_full[s], par, a.status, limit, &sh.abort_flag) &&
-             wait_cluster(&sh.a_full[s], par, a.status, limit, &sh.abort_flag) &&
-             wait_cluster(&sh.peer_full[s], par, a.status, limit, &sh.abort_flag);
+      for (int step = 0; step < KS && ok; ++step) {
+        if (!there) ok = wait_cluster(&sh.full[s], par, a.status, limit, &sh.abort_flag);
         if (!ok) break;
         tc_after();
         const uint32_t lo = a_lo + s * (C::kStage >> 4);
@@ -382,6 +424,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           if (step == KS - 1) pair_commit(&sh.acc_full[buf]);
         }
         __syncwarp();
+        if (++s == S) {
+          s = 0;
+          par ^= 1;
+        }
+        there = __all_sync(0xffffffffu, try_wait_cluster(&sh.full[s], par));
       }
     }
     if (!ok) sh.abort_flag = 1;
@@ -390,20 +437,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     __syncwarp();
     mbar_wait_warp(&sh.drain, 0, a.status, limit);
   } else {
-    // ---------------------------------------------------------------- second CTA: full stages told to the first
-    int gs = 0;
-    bool ok = true;
-    for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
-      for (int step = 0; step < KS && ok; ++step, ++gs) {
-        const int s = gs % S;
-        const uint32_t par = (gs / S) & 1;
-        ok = wait_cluster(&sh.b_full[s], par, a.status, limit, &sh.abort_flag) &&
-             wait_cluster(&sh.a_full[s], par, a.status, limit, &sh.abort_flag);
-        if (ok && lane == 0) arrive_at(&sh.peer_full[s], 0);
-        __syncwarp();
-      }
-    }
-    if (!ok) sh.abort_flag = 1;
     mbar_wait_warp(&sh.drain, 0, a.status, limit);
   }
   tc_before();
@@ -424,6 +457,9 @@ cudaError_t launch_tc(const LinearArgs& a, int m_tiles, cudaStream_t s) {
   CUtensorMap map;
   e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, BN / 2, false);
   if (e != cudaSuccess) return e;
+  CUtensorMap wmap;
+  e = make_bytes_map(&wmap, a.w, a.N, a.K / 2, kRawRows);
+  if (e != cudaSuccess) return e;
   LinearTc p{a, m_tiles, m_tiles * ((a.T + BN - 1) / BN)};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)std::min(p.tiles, a.num_sms / 2));
@@ -437,7 +473,7 @@ cudaError_t launch_tc(const LinearArgs& a, int m_tiles, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN>, map, p);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN>, map, wmap, p);
 }
 
 }  // namespace
