@@ -176,7 +176,8 @@ cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  return a.T <= 32 ? launch_linear_stream(a, s) : launch_linear_tc(a, s);
+  if (a.T <= 32) return launch_linear_stream(a, s);
+  return launch_linear_tc(a, s);
 }
 
 }  // namespace moe

@@ -19,14 +19,21 @@
 //           residual, store
 //   8 - 23  converters, in four groups of four warps that take turns: a thread a row of
 //           the weight, both blocks of 32 of a step
-//   24      TMA of the x tiles
-//   25      MMAs (first CTA)
-//   26      TMA of the packed weight, four steps (256 of K) at a time
-// Packed weights come by TMA because loads into registers ahead of their use do not
-// outlive the proxy fence that a converter needs each step, and because rows
-// 1,792 bytes apart cost a wavefront of the load unit each.
+//   24      MMAs (first CTA)
+//   25      TMA of the x tiles
+//   26      TMA of the packed weight, four steps (256 of K, a quad) at a time
+//   27      scale bytes of a quad, kScalesAhead quads ahead, to shared memory
+// Packed weights and scales do not come by loads of the converters: these would have to
+// land before the proxy fence that a converter needs each step (a quad took the
+// latency of its scale bytes, 1 us), and rows 1,792 bytes apart cost a wavefront of the load unit
+// each.
 // Two accumulators of 256 columns: the epilogue of one tile runs beside the MMAs of
 // the next.  Clusters walk over the tiles, weight tiles innermost.
+//
+// Where there are fewer tiles than pairs of SMs, K is split (SPLIT): a cluster of 2, 3 or 4
+// pairs takes one tile, each pair a run of K; then every CTA hands the other pairs' CTAs
+// of the same rows its sums of the tokens (in chunks of 32) that are theirs, in their
+// shared memory, and finishes its own.
 #include <algorithm>
 #include <atomic>
 
@@ -44,26 +51,23 @@ namespace cg = cooperative_groups;
 
 constexpr int kGroups = 4;              // of converter warps
 constexpr int kEpiWarps = 8, kConvWarp = kEpiWarps, kConvWarps = 4 * kGroups;
-constexpr int kTmaWarp = kConvWarp + kConvWarps, kMmaWarp = kTmaWarp + 1, kRawWarp = kTmaWarp + 2;
-constexpr int kTcThreads = 32 * (kRawWarp + 1);
+constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1, kRawWarp = kTmaWarp + 1, kScaleWarp = kRawWarp + 1;
+constexpr int kTcThreads = 32 * (kScaleWarp + 1);
 constexpr int kRows = 128;              // rows of the weight a CTA
 constexpr int kABytes = kRows * 128;    // one step of them in bf16
 constexpr int kQuad = 4;                // steps of a load of packed weights
 constexpr int kRawStages = 3, kRawBytes = kRows * 128, kRawRows = 16;
+constexpr int kScaleBytes = kRows * 8, kScalesAhead = 3;
+constexpr int kChunk = 16;              // tokens that the epilogue takes at a time
 constexpr uint32_t kAccCols = 256, kCols = 512;
 
-template <int BN>
-struct TcCfg {
-  static constexpr int kStages = BN == 256 ? 5 : BN == 128 ? 7 : 8;
-  static constexpr int kBBytes = BN / 2 * 128;
-  static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kRawOff = kStages * kStage;
-  static constexpr int kBarOff = kRawOff + kRawStages * kRawBytes;
-  static constexpr int kSmem = 1024 + kBarOff + 512;
-  static_assert(kBBytes % 1024 == 0 && kSmem <= 227 * 1024, "shared memory");
-};
+constexpr int BN = 256;                 // tokens of a tile
+constexpr int S = 5;                    // stages of a step
+constexpr int kBBytes = BN / 2 * 128, kStage = kABytes + kBBytes;
+constexpr int kRawOff = S * kStage, kScaleOff = kRawOff + kRawStages * kRawBytes, kBarOff = kScaleOff + kRawStages * kScaleBytes;
+constexpr int kTcSmem = 1024 + kBarOff + 512;
+static_assert(kTcSmem <= 227 * 1024, "shared memory");
 
-template <int S>
 struct TcShared {
   uint64_t b_full[S];  // this CTA's x tile of a stage
   uint64_t full[S];    // first CTA: weights and x tiles of both
@@ -78,6 +82,7 @@ struct TcShared {
 struct LinearTc {
   LinearArgs a;
   int m_tiles, tiles;
+  int splits;  // of K, 1 without SPLIT
 };
 
 // ------------------------------------------------------------------ pairs of CTAs
@@ -109,7 +114,26 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-// The same by a whole warp, with a limit, one result (see mbar_wait_warp).
+// Is it complete now?  (try_wait may suspend the thread while it is not.)
+__device__ __forceinline__ bool test_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool test_here(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// try_wait_cluster by a whole warp, with a limit, one result (see mbar_wait_warp).
 __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint32_t* status, uint64_t limit_ns,
                                              const volatile int* abort) {
   if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
@@ -139,11 +163,19 @@ __device__ __forceinline__ void pair_dealloc(uint32_t taddr) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// Arrives on the barriers at this place in both CTAs of the pair once all MMAs issued so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+// Arrives on the barriers at this place in both CTAs of the pair (bits of ``mask``) once all MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"(mask)
+               : "memory");
+}
+// Four floats to CTA ``rank``'s shared memory.
+__device__ __forceinline__ void store_at(float* p, uint32_t rank, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile(
-      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
-      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(smem_u32(bar))
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.v4.b32 [a], {%2, %3, %4, %5};\n}" ::"r"(
+          smem_u32(p)),
+      "r"(rank), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
@@ -167,17 +199,17 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t hi, uint32_t b
 __device__ __forceinline__ uint32_t idesc(int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((256u >> 4) << 24);
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// The cluster's barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The weight row of row i (0 .. 127) of CTA ``rank`` in tile mt; -1 outside the weight.
 __device__ __forceinline__ int weight_row(const LinearArgs& a, int mt, int rank, int i) {
@@ -189,19 +221,56 @@ __device__ __forceinline__ int weight_row(const LinearArgs& a, int mt, int rank,
   return row < a.N ? row : -1;
 }
 
-template <int BN>
+// Bias, activation, residual and store of a weight row's sums for a chunk of tokens from ``tok`` on (the whole warp calls it).
+__device__ __forceinline__ void finish(const LinearArgs& a, int row, float bias, int tok, const uint32_t (&v)[kChunk]) {
+  const int lane = threadIdx.x & 31;
+  if (a.act == LINEAR_ACT_SWIGLU) {
+    // lanes of gate rows take the even tokens, those of up rows the odd ones
+    const bool up = lane & 16;
+    float h[kChunk / 2];
+#pragma unroll
+    for (int k = 0; k < kChunk / 2; ++k) {
+      const float x0 = __uint_as_float(v[2 * k]) + bias, x1 = __uint_as_float(v[2 * k + 1]) + bias;
+      const float theirs = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 16);
+      h[k] = silu(up ? theirs : x0) * (up ? x1 : theirs);
+    }
+    if (row >= 0) linear_store_column<kChunk / 2, 2>(a, tok + (up ? 1 : 0), up ? row - a.cols : row, h);
+  } else if (row >= 0) {
+    float h[kChunk];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) h[k] = __uint_as_float(v[k]) + bias;
+    if (a.act == LINEAR_ACT_SILU) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) h[k] = silu(h[k]);
+    } else if (a.act == LINEAR_ACT_GELU) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) h[k] = linear_act(LINEAR_ACT_GELU, h[k]);
+    }
+    linear_store_column<kChunk, 1>(a, tok, row, h);
+  }
+}
+
+template <bool SPLIT>
 __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_constant__ CUtensorMap map,
                                                                   const __grid_constant__ CUtensorMap wmap, const LinearTc p) {
-  using C = TcCfg<BN>;
-  constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   // (both CTAs' tiles lie at the same addresses: the launch gives every CTA the same base)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TcShared<S>& sh = *reinterpret_cast<TcShared<S>*>(smem + C::kBarOff);
+  TcShared& sh = *reinterpret_cast<TcShared*>(smem + kBarOff);
   const LinearArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int rank = cluster_rank(), cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const int KB = a.K >> 5, KS = (KB + 1) >> 1, KQ = (KS + kQuad - 1) / kQuad;  // blocks of 32, steps of 64, quads of steps
+  // rank within the pair, the pair's first CTA, its run of K
+  const int crank = cluster_rank(), rank = crank & 1, first = crank & ~1, z = crank >> 1;
+  const int ctas = SPLIT ? 2 * p.splits : 2, cluster = blockIdx.x / ctas, clusters = gridDim.x / ctas;
+  const uint16_t both = (uint16_t)(3u << first);
+  const int KB = a.K >> 5;  // blocks of 32
+  int q_lo = 0, KS = (KB + 1) >> 1, KQ = (KS + kQuad - 1) / kQuad;  // first quad, steps of 64, quads of steps
+  if (SPLIT) {
+    const int all = KQ, steps = KS;
+    q_lo = all * z / p.splits;
+    KQ = all * (z + 1) / p.splits - q_lo;
+    KS = min(steps - kQuad * q_lo, kQuad * KQ);
+  }
   const uint64_t limit = a.wait.limit_ns;
 
   if (tid == 0) {
@@ -211,7 +280,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       mbar_init(&sh.empty[s], 1);
     }
     for (int s = 0; s < kRawStages; ++s) {
-      mbar_init(&sh.raw_full[s], 1);
+      mbar_init(&sh.raw_full[s], 2);  // packed weights, scales
       mbar_init(&sh.raw_empty[s], kConvWarps);
     }
     for (int b = 0; b < 2; ++b) {
@@ -223,12 +292,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     fence_barrier_init();
   }
   __syncthreads();
-  cg::this_cluster().sync();  // the other CTA's barriers are there
-  if (warp == kMmaWarp) pair_alloc(&sh.tmem_slot);
-  tc_before();
-  __syncthreads();
-  tc_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_slot, 0);
+  cluster_arrive();  // warps that touch the other CTA wait for it; copies begin at once
+  uint32_t tmem = 0;
+  if (warp <= kMmaWarp) {
+    if (warp == kMmaWarp) pair_alloc(&sh.tmem_slot);
+    tc_before();
+    named_bar_sync(1, 32 * (kMmaWarp + 1));
+    tc_after();
+    tmem = __shfl_sync(0xffffffffu, sh.tmem_slot, 0);
+    cluster_wait();  // the other CTA's barriers are there
+  }
   // tokens of a tile, and of it what the MMAs take (a multiple of 16)
   auto tokens = [&](int tile, int& t0) -> int {
     t0 = tile / p.m_tiles * BN;
@@ -238,9 +311,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
   if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue: thread = row of D
     const int quad = warp & 3, half = warp >> 2;
-    const bool gated = a.act == LINEAR_ACT_SWIGLU;
     int it = 0;
-    for (int tile = cluster; tile < p.tiles; tile += clusters, ++it) {
+    for (int tile = cluster; !SPLIT && tile < p.tiles; tile += clusters, ++it) {
       const int buf = it & 1, mt = tile % p.m_tiles;
       int t0;
       const int n = tokens(tile, t0);
@@ -255,72 +327,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       auto release = [&]() {  // this warp has read its part of the accumulator
         tc_before();
         __syncwarp();
-        if (lane == 0) arrive_at(&sh.acc_empty[buf], 0);
+        if (lane == 0) arrive_at(&sh.acc_empty[buf], first);
       };
-      if (32 * half >= n) release();
-      for (int c = 32 * half; c < n; c += 64) {
-        uint32_t v[32];
-        tmem_ld32(src + c, v);
-        if (c + 64 >= n) release();
-        if (gated) {
-          // lanes of gate rows take the even tokens, those of up rows the odd ones
-          const bool up = lane & 16;
-          float h[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float x0 = __uint_as_float(v[2 * k]) + bias, x1 = __uint_as_float(v[2 * k + 1]) + bias;
-            const float theirs = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 16);
-            h[k] = silu(up ? theirs : x0) * (up ? x1 : theirs);
-          }
-          if (row >= 0) linear_store_column<16, 2>(a, t0 + c + (up ? 1 : 0), up ? row - a.cols : row, h);
-        } else if (row >= 0) {
-          float h[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) h[k] = __uint_as_float(v[k]) + bias;
-          if (a.act == LINEAR_ACT_SILU) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) h[k] = silu(h[k]);
-          } else if (a.act == LINEAR_ACT_GELU) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) h[k] = linear_act(LINEAR_ACT_GELU, h[k]);
-          }
-          linear_store_column<32, 1>(a, t0 + c, row, h);
-        }
+      if (kChunk * half >= n) release();
+      for (int c = kChunk * half; c < n; c += 2 * kChunk) {
+        uint32_t v[kChunk];
+        tmem_ld16(src + c, v);
+        if (c + 2 * kChunk >= n) release();
+        finish(a, row, bias, t0 + c, v);
       }
     }
-  } else if (warp < kTmaWarp) {
+  } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- converters: thread = row of the weight
     const int group = (warp - kConvWarp) >> 2, i = (tid - 32 * kConvWarp) & 127;
-    auto row_scales = [&](int tile) -> const uint8_t* {
-      const int row = tile < p.tiles ? weight_row(a, tile % p.m_tiles, rank, i) : -1;
-      return row < 0 ? nullptr : a.ws + (size_t)row * KB;
-    };
-    const bool wide = (((uintptr_t)a.ws | (uintptr_t)KB) & 1) == 0;
-    // The scale bytes of this thread's two blocks of a quad.
-    auto scales = [&](const uint8_t* src, int quad) -> uint32_t {
-      const int b = 8 * quad + 2 * group;
-      if (!src || b >= KB) return 0x7F7Fu;
-      src += b;
-      if (wide) return __ldg(reinterpret_cast<const uint16_t*>(src));
-      return (uint32_t)__ldg(src) | (b + 1 < KB ? (uint32_t)__ldg(src + 1) << 8 : 0x7F00u);
-    };
-    const uint8_t* here = row_scales(cluster);
-    uint32_t sc = scales(here, 0);
     bool ok = true;
     int gs0 = 0, gq = 0;  // steps before this quad, quads
     for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
-      const uint8_t* after = row_scales(tile + clusters);
       for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
         const int r = gq % kRawStages, steps = min(kQuad, KS - kQuad * quad);
         const int gs = gs0 + group, s = gs % S;
         const bool mine = group < steps;
         // (probes now, waits where they failed: the round trips pass beside the conversion)
-        const bool free_now = !mine || gs < S || mbar_try_wait(&sh.empty[s], ((gs / S) - 1) & 1);
-        const bool x_there = !mine || (warp & 3) != 0 || mbar_try_wait(&sh.b_full[s], (gs / S) & 1);
+        const bool free_now = !mine || gs < S || test_here(&sh.empty[s], ((gs / S) - 1) & 1);
+        const bool x_there = !mine || (warp & 3) != 0 || test_here(&sh.b_full[s], (gs / S) & 1);
         ok = mbar_wait_warp(&sh.raw_full[r], (gq / kRawStages) & 1, a.status, limit, &sh.abort_flag);
         uint4 w[2][4];
         if (mine) {
-          const uint8_t* raw = smem + C::kRawOff + r * kRawBytes + i * 128;
+          const uint8_t* raw = smem + kRawOff + r * kRawBytes + i * 128;
+          const uint32_t sc = *reinterpret_cast<const uint16_t*>(smem + kScaleOff + r * kScaleBytes + i * 8 + 2 * group);
 #pragma unroll
           for (int b = 0; b < 2; ++b)
             linear_block(*reinterpret_cast<const uint4*>(raw + (((2 * group + b) ^ (i & 7)) << 4)), (sc >> (8 * b)) & 255u, w[b]);
@@ -331,7 +365,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           if (ok && !__all_sync(0xffffffffu, free_now))
             ok = mbar_wait_warp(&sh.empty[s], ((gs / S) - 1) & 1, a.status, limit, &sh.abort_flag);
           if (!ok) break;
-          uint8_t* dst = smem + s * C::kStage + i * 128;
+          uint8_t* dst = smem + s * kStage + i * 128;
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -341,12 +375,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           if ((warp & 3) == 0 && !__all_sync(0xffffffffu, x_there))
             ok = mbar_wait_warp(&sh.b_full[s], (gs / S) & 1, a.status, limit, &sh.abort_flag);
           __syncwarp();
-          if (ok && lane == 0) arrive_at(&sh.full[s], 0);
+          if (ok && lane == 0) arrive_at(&sh.full[s], first);
         }
-        sc = quad + 1 < KQ ? scales(here, quad + 1) : scales(after, 0);
         gs0 += steps;
       }
-      here = after;
     }
     if (!ok) sh.abort_flag = 1;
   } else if (warp == kTmaWarp) {
@@ -361,8 +393,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           const int s = gs % S;
           if (gs >= S) ok = sh.abort_flag == 0 && mbar_wait(&sh.empty[s], ((gs / S) - 1) & 1, a.status, limit);
           if (!ok) break;
-          mbar_arrive_expect_tx(&sh.b_full[s], C::kBBytes);
-          tma_load_2d(smem + s * C::kStage + kABytes, &map, 64 * step, t0 + rank * (n >> 1), &sh.b_full[s]);
+          mbar_arrive_expect_tx(&sh.b_full[s], kBBytes);
+          tma_load_2d(smem + s * kStage + kABytes, &map, 64 * (kQuad * q_lo + step), t0 + rank * (n >> 1), &sh.b_full[s]);
         }
       }
       if (!ok) {
@@ -388,7 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           for (int k = 0; k < kRows / kRawRows; ++k) {
             const int row = a.act == LINEAR_ACT_SWIGLU ? mt * 128 + rank * 64 + (k >> 1) * 16 + (k & 1) * a.cols
                                                        : mt * 256 + rank * 128 + k * 16;
-            tma_load_2d(smem + C::kRawOff + r * kRawBytes + k * kRawRows * 128, &wmap, 128 * quad, row, &sh.raw_full[r]);
+            tma_load_2d(smem + kRawOff + r * kRawBytes + k * kRawRows * 128, &wmap, 128 * (q_lo + quad), row, &sh.raw_full[r]);
           }
         }
       }
@@ -398,6 +430,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       }
     }
     __syncwarp();
+  } else if (warp == kScaleWarp) {
+    // ---------------------------------------------------------------- scale bytes: four rows a lane
+    const bool wide = (((uintptr_t)a.ws | (uintptr_t)KB) & 7) == 0;  // eight bytes lie on such a boundary in every row
+    int row[4];
+    auto rows_of = [&](int tile) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) row[k] = tile < p.tiles ? weight_row(a, tile % p.m_tiles, rank, 32 * k + lane) : -1;
+    };
+    int ltile = cluster, lquad = 0;
+    rows_of(ltile);
+    uint2 v[kScalesAhead][4];
+    auto fetch = [&](uint2 (&to)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        to[k] = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (row[k] < 0) continue;
+        const int b0 = 8 * (q_lo + lquad);
+        const uint8_t* src = a.ws + (size_t)row[k] * KB + b0;
+        if (wide) {
+          to[k] = __ldg(reinterpret_cast<const uint2*>(src));
+          continue;
+        }
+        // three words around the eight bytes, or byte by byte at the ends of the array
+        const uintptr_t word = (uintptr_t)src & ~(uintptr_t)3;
+        const int n = KB - b0;  // bytes that exist; the others stay 127 (their weights are 0)
+        if (word >= (uintptr_t)a.ws && word + 12 <= (uintptr_t)a.ws + (size_t)a.N * KB) {
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(word);
+          const uint32_t sh = 8u * (uint32_t)((uintptr_t)src & 3), x = __ldg(q), y = __ldg(q + 1), z2 = __ldg(q + 2);
+          to[k] = make_uint2(__funnelshift_r(x, y, sh), __funnelshift_r(y, z2, sh));
+        } else {
+          to[k] = make_uint2(0u, 0u);
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (b < n) (b < 4 ? to[k].x : to[k].y) |= (uint32_t)__ldg(src + b) << (8 * (b & 3));
+        }
+        if (n < 8) {
+          const uint64_t keep = (1ull << (8 * n)) - 1;
+          to[k].x = (to[k].x & (uint32_t)keep) | (0x7F7F7F7Fu & ~(uint32_t)keep);
+          to[k].y = (to[k].y & (uint32_t)(keep >> 32)) | (0x7F7F7F7Fu & ~(uint32_t)(keep >> 32));
+        }
+      }
+      if (++lquad == KQ) {
+        lquad = 0;
+        ltile += clusters;
+        rows_of(ltile);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kScalesAhead; ++u) fetch(v[u]);
+    int gq = 0, u = 0;
+    bool ok = true;
+    for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
+      for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
+        const int r = gq % kRawStages;
+        if (gq >= kRawStages) ok = mbar_wait_warp(&sh.raw_empty[r], ((gq / kRawStages) - 1) & 1, a.status, limit, &sh.abort_flag);
+        if (!ok) break;
+#pragma unroll
+        for (int w = 0; w < kScalesAhead; ++w)
+          if (u == w) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint2*>(smem + kScaleOff + r * kScaleBytes + (32 * k + lane) * 8) = v[w][k];
+            fetch(v[w]);
+          }
+        u = u + 1 == kScalesAhead ? 0 : u + 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.raw_full[r]);
+      }
+    }
+    if (!ok) sh.abort_flag = 1;
   } else if (rank == 0) {
     // ---------------------------------------------------------------- MMAs
     // (the whole warp runs the loop on uniform values, one lane issues)
@@ -414,78 +516,158 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       for (int step = 0; step < KS && ok; ++step) {
         if (!there) ok = wait_cluster(&sh.full[s], par, a.status, limit, &sh.abort_flag);
         if (!ok) break;
+        // (the next stage is looked at before this one's MMAs go out: the probe's round trip passes beside them)
+        const int s1 = s + 1 == S ? 0 : s + 1;
+        const uint32_t par1 = s + 1 == S ? par ^ 1 : par;
+        const bool next = test_cluster(&sh.full[s1], par1);
         tc_after();
-        const uint32_t lo = a_lo + s * (C::kStage >> 4);
+        const uint32_t lo = a_lo + s * (kStage >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             pair_mma(d, desc_at(lo, hi, 32 * k), desc_at(lo, hi, kABytes + 32 * k), id, step > 0 || k > 0);
-          pair_commit(&sh.empty[s]);
-          if (step == KS - 1) pair_commit(&sh.acc_full[buf]);
+          pair_commit(&sh.empty[s], both);
+          if (step == KS - 1) pair_commit(&sh.acc_full[buf], both);
         }
         __syncwarp();
-        if (++s == S) {
-          s = 0;
-          par ^= 1;
-        }
-        there = __all_sync(0xffffffffu, try_wait_cluster(&sh.full[s], par));
+        s = s1;
+        par = par1;
+        there = __all_sync(0xffffffffu, next);
       }
     }
     if (!ok) sh.abort_flag = 1;
     // all issued MMAs are done before shared and tensor memory go away
-    if (elect_one()) pair_commit(&sh.drain);
+    if (elect_one()) pair_commit(&sh.drain, both);
     __syncwarp();
     mbar_wait_warp(&sh.drain, 0, a.status, limit);
   } else {
     mbar_wait_warp(&sh.drain, 0, a.status, limit);
   }
+  if (warp > kMmaWarp) cluster_wait();
   tc_before();
   __syncthreads();
-  cg::this_cluster().sync();  // no MMA, arrival or read of the other CTA's is left
+  cg::this_cluster().sync();  // no MMA, copy, arrival or read of any CTA's is left
+  if constexpr (SPLIT) {
+    // chunk c of the tokens is finished by the pair c % splits; kTeams warps take a quarter of the rows
+    constexpr int kTeams = (kMmaWarp) / 4;
+    const int quad = warp & 3, team = warp >> 2, mt = cluster % p.m_tiles;
+    int t0;
+    const int chunks = tokens(cluster, t0) / kChunk, most = (chunks + p.splits - 1) / p.splits;
+    const uint32_t src = tmem + ((uint32_t)(32 * quad) << 16);
+    // sums handed over: [other pair][own chunk][tokens / 4][row 128][token 4]
+    float* mine = reinterpret_cast<float*>(smem) + 4 * (32 * quad + lane);
+    tc_after();
+    if (team < kTeams) {
+      for (int c = team; c < chunks; c += kTeams) {
+        const int to = c % p.splits;
+        if (to == z) continue;
+        uint32_t v[kChunk];
+        tmem_ld16(src + kChunk * c, v);
+        float* dst = mine + (size_t)((z < to ? z : z - 1) * most + c / p.splits) * (kChunk * kRows);
+#pragma unroll
+        for (int k = 0; k < kChunk; k += 4) store_at(dst + k * kRows, 2 * to + rank, v[k], v[k + 1], v[k + 2], v[k + 3]);
+      }
+    }
+    cg::this_cluster().sync();  // the sums are where they belong
+    if (team < kTeams) {
+      const int row = weight_row(a, mt, rank, 32 * quad + lane);
+      const float bias = row >= 0 ? linear_bias(a, row) : 0.f;
+      for (int c = z + p.splits * team; c < chunks; c += p.splits * kTeams) {
+        uint32_t v[kChunk];
+        tmem_ld16(src + kChunk * c, v);
+        for (int o = 0; o < p.splits - 1; ++o) {
+          const float* add = mine + (size_t)(o * most + c / p.splits) * (kChunk * kRows);
+#pragma unroll
+          for (int k = 0; k < kChunk; k += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(add + k * kRows);
+            v[k] = __float_as_uint(__uint_as_float(v[k]) + x.x);
+            v[k + 1] = __float_as_uint(__uint_as_float(v[k + 1]) + x.y);
+            v[k + 2] = __float_as_uint(__uint_as_float(v[k + 2]) + x.z);
+            v[k + 3] = __float_as_uint(__uint_as_float(v[k + 3]) + x.w);
+          }
+        }
+        finish(a, row, bias, t0 + kChunk * c, v);
+      }
+    }
+    tc_before();
+    cg::this_cluster().sync();
+  }
   if (warp == kMmaWarp) {
     tc_after();
     pair_dealloc(tmem);
   }
 }
 
-template <int BN>
-cudaError_t launch_tc(const LinearArgs& a, int m_tiles, cudaStream_t s) {
-  using C = TcCfg<BN>;
-  static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_shared(linear_tc_kernel<BN>, C::kSmem, done);
-  if (e != cudaSuccess) return e;
-  CUtensorMap map;
-  e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, BN / 2, false);
-  if (e != cudaSuccess) return e;
-  CUtensorMap wmap;
-  e = make_bytes_map(&wmap, a.w, a.N, a.K / 2, kRawRows);
-  if (e != cudaSuccess) return e;
-  LinearTc p{a, m_tiles, m_tiles * ((a.T + BN - 1) / BN)};
+cudaLaunchConfig_t tc_config(int splits, unsigned clusters, cudaLaunchAttribute* attr, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)std::min(p.tiles, a.num_sms / 2));
+  cfg.gridDim = dim3(2 * splits * clusters);
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = kTcSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<BN>, map, wmap, p);
+  return cfg;
+}
+
+template <bool SPLIT>
+cudaError_t allow_tc() {
+  static std::atomic<unsigned long long> done{0};
+  return allow_shared(linear_tc_kernel<SPLIT>, kTcSmem, done);
+}
+
+// Clusters of ``splits`` pairs that fit on the current device at once (asked of the runtime once per device).
+cudaError_t resident_clusters(int splits, int* n) {
+  static std::atomic<int> known[64][5];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* at = dev < 64 ? &known[dev][splits] : nullptr;
+  *n = at ? at->load(std::memory_order_relaxed) : 0;
+  if (*n > 0) return cudaSuccess;
+  if ((e = allow_tc<true>()) != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = tc_config(splits, 1, attr, nullptr);
+  if ((e = cudaOccupancyMaxActiveClusters(n, linear_tc_kernel<true>, &cfg)) != cudaSuccess) return e;
+  if (at) at->store(*n, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+template <bool SPLIT>
+cudaError_t launch_tc(const LinearArgs& a, int m_tiles, int splits, cudaStream_t s) {
+  cudaError_t e = allow_tc<SPLIT>();
+  if (e != cudaSuccess) return e;
+  CUtensorMap map, wmap;
+  if ((e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, BN / 2, false)) != cudaSuccess) return e;
+  if ((e = make_bytes_map(&wmap, a.w, a.N, a.K / 2, kRawRows)) != cudaSuccess) return e;
+  const LinearTc p{a, m_tiles, m_tiles * ((a.T + BN - 1) / BN), splits};
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = tc_config(splits, (unsigned)(SPLIT ? p.tiles : std::min(p.tiles, a.num_sms / 2)), attr, s);
+  return cudaLaunchKernelEx(&cfg, linear_tc_kernel<SPLIT>, map, wmap, p);
 }
 
 }  // namespace
 
+// Splits of K: as many as leave all clusters resident at once with three quads of K or more
+// each (one tile a pair: 250 rows x 3584 -> 8192, 32 tiles, 28.6 us unsplit, 22.3 in 2;
+// 64 x 3584 -> 3584, 14 tiles, 24.0 / 17.2 / 15.0 / 14.5 in 1 / 2 / 3 / 4, and
+// 128 x 3584 -> 4608, 18 tiles, whose 18 clusters of 8 do not fit at once, 24.9 / 18.3 /
+// 17.1 / 29.2; 64 x 512 -> 1024, two quads, 8.8 unsplit and 10.0 in 2).
 cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s) {
   const int per = a.act == LINEAR_ACT_SWIGLU ? 128 : 256;
-  const int m_tiles = (a.cols + per - 1) / per, pairs = a.num_sms / 2;
-  // tiles of fewer tokens where wide ones would leave SMs without any
-  auto tiles = [&](int n) { return (long long)m_tiles * ((a.T + n - 1) / n); };
-  if (tiles(256) >= pairs) return launch_tc<256>(a, m_tiles, s);
-  if (tiles(128) >= pairs) return launch_tc<128>(a, m_tiles, s);
-  return launch_tc<64>(a, m_tiles, s);
+  const int m_tiles = (a.cols + per - 1) / per, quads = (a.K + 255) / 256;
+  const long long tiles = (long long)m_tiles * ((a.T + BN - 1) / BN);
+  for (int n = 4; n > 1; --n) {
+    if (quads < 3 * n || 2 * n * tiles > a.num_sms) continue;
+    int fit = 0;
+    const cudaError_t e = resident_clusters(n, &fit);
+    if (e != cudaSuccess) return e;
+    if (tiles <= fit) return launch_tc<true>(a, m_tiles, n, s);
+  }
+  return launch_tc<false>(a, m_tiles, 1, s);
 }
 
 }  // namespace moe
