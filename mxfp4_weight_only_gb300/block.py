@@ -19,9 +19,11 @@ import torch
 
 from . import _native
 from ._native import KvAttnStruct, KvRopeStruct, LinearStruct
-from .kv_cache import KvCacheMxfp4, _empty, _i32, _need, _queries, _rows, _stream
+from .kv_cache import KvCacheMxfp4, _empty, _flat, _i32, _need, _queries, _rows, _stream
 
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
+_T, _bf16, _u8 = torch.Tensor, torch.bfloat16, torch.uint8
+_BF16, _OUT = (torch.bfloat16,), (torch.bfloat16, torch.float32)
 
 
 def linear_workspace_bytes(T: int, N: int, K: int) -> int:
@@ -30,20 +32,20 @@ def linear_workspace_bytes(T: int, N: int, K: int) -> int:
     return int(_native.load().linear_mxfp4_workspace_bytes(ctypes.byref(d)))
 
 
-def _matrix(t, name, dtypes, shape, device):
-    """Checks a matrix of dense rows; returns the rows' stride in elements."""
+def _matrix(t, name, dtypes, rows, cols, device):
+    """Checks a matrix [rows, cols] of dense rows; returns the rows' stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     st = t.stride()
-    if shape[1] > 1 and st[1] != 1:
+    if cols > 1 and st[1] != 1:
         raise ValueError(f"{name}: rows must be dense")
-    return st[0] if shape[0] > 1 else shape[1]
+    return st[0] if rows > 1 else cols
 
 
 def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=None, out_dtype=torch.bfloat16,
@@ -58,43 +60,56 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
     rows may be strided; a bf16 ``out`` may be ``residual`` itself).  Pass ``workspace``
     (uint8, ``linear_workspace_bytes``, first 4 bytes zeroed once) to allocate nothing
     but a missing ``out``, and to learn of waits that ran out (``linear_read_status``)."""
-    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
-        raise TypeError("x and w must be torch.Tensors")
+    if not isinstance(x, _T) or not isinstance(w, _T) or not isinstance(w_scale, _T):
+        raise TypeError("x, w and w_scale must be torch.Tensors")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [T, K] and w [N, K / 2]")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
-    (T, K), N, dev, code = x.shape, w.shape[0], x.device, _ACTS[act]
-    if code == 3 and N % 2:
-        raise ValueError(f"swiglu needs an even number of weight rows, got {N}")
-    cols = N // 2 if code == 3 else N
-    xs = _matrix(x, "x", (torch.bfloat16,), (T, K), dev)
-    if T <= 1:
-        xs = -(-K // 8) * 8
-    _need(w, "w", torch.uint8, (N, K // 2), dev)
-    _need(w_scale, "w_scale", torch.uint8, (N, K // 32), dev)
+    (T, K), N, dev = x.shape, w.shape[0], x.device
+    cols = N
+    if code == 3:
+        if N % 2:
+            raise ValueError(f"swiglu needs an even number of weight rows, got {N}")
+        cols = N // 2
+    # (conditions written out: a call of a few microseconds feels a function a tensor)
+    xs = x.stride()
+    if x.dtype is not _bf16 or (K > 1 and xs[1] != 1):
+        _matrix(x, "x", _BF16, T, K, dev)
+    xs = xs[0] if T > 1 else -(-K // 8) * 8
+    if w.dtype is not _u8 or w.shape[1] != K // 2 or not w.is_contiguous() or w.device != dev:
+        _need(w, "w", _u8, (N, K // 2), dev)
+    if w_scale.dtype is not _u8 or w_scale.shape != (N, K // 32) or not w_scale.is_contiguous() or w_scale.device != dev:
+        _need(w_scale, "w_scale", _u8, (N, K // 32), dev)
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (N,), dev)
-    rs = cols if residual is None else _matrix(residual, "residual", (torch.bfloat16,), (T, cols), dev)
+        if not isinstance(bias, _T) or bias.dtype is not _bf16 or bias.shape != (N,) or not bias.is_contiguous() or bias.device != dev:
+            _need(bias, "bias", _bf16, (N,), dev)
+        bias = bias.data_ptr()
+    rs = cols
+    if residual is not None:
+        rs = _matrix(residual, "residual", _BF16, T, cols, dev)
+        residual = residual.data_ptr()
     if out is None:
-        if out_dtype not in (torch.bfloat16, torch.float32):
+        if out_dtype not in _OUT:
             raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
         out = _empty((T, cols), out_dtype, dev, stream)
-    os = _matrix(out, "out", (torch.bfloat16, torch.float32), (T, cols), dev)
+        os = cols
+    else:
+        os = _matrix(out, "out", _OUT, T, cols, dev)
     lib = _native.load()
-    d = LinearStruct(T, K, N, code, 1 if out.dtype == torch.float32 else 0, xs, rs, os)
+    d = LinearStruct(T, K, N, code, 1 if out.dtype is torch.float32 else 0, xs, rs, os)
     ref = ctypes.byref(d)
     if workspace is None:
         workspace = _empty(max(256, lib.linear_mxfp4_workspace_bytes(ref)), torch.uint8, dev, stream)
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+    elif workspace.dtype is not _u8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                                None if bias is None else bias.data_ptr(),
-                                None if residual is None else residual.data_ptr(), out.data_ptr(),
+    rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias, residual, out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel(), _stream(stream, x))
-    _native.check("linear_a16w4_mxfp4", rc)
+    if rc:
+        _native.check("linear_a16w4_mxfp4", rc)
     return out
 
 
@@ -118,15 +133,18 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
     then its sines; rotary_dim, a multiple of 16, leading elements of a head are rotated, in pairs
     (i, i + rotary_dim / 2) or, with ``interleaved``, (2i, 2i + 1).  A position past the table
     makes its token NaN."""
-    if not isinstance(positions, torch.Tensor) or not isinstance(cos_sin, torch.Tensor):
-        raise TypeError("positions and cos_sin must be torch.Tensors")
+    if not isinstance(positions, _T) or not isinstance(slots, _T) or not isinstance(cos_sin, _T):
+        raise TypeError("positions, slots and cos_sin must be torch.Tensors")
     dev = cache.device
     N = positions.shape[0]
-    _need(positions, "positions", torch.int32, (N,), dev)
-    _need(slots, "slots", torch.int32, (N,), dev)
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [positions, rotary_dim]")
-    _need(cos_sin, "cos_sin", torch.float32, cos_sin.shape, dev)
+    if positions.dtype is not _i32 or positions.dim() != 1 or not positions.is_contiguous() or positions.device != dev:
+        _need(positions, "positions", _i32, (N,), dev)
+    if slots.dtype is not _i32 or slots.shape != (N,) or not slots.is_contiguous() or slots.device != dev:
+        _need(slots, "slots", _i32, (N,), dev)
+    if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or cos_sin.device != dev:
+        _need(cos_sin, "cos_sin", torch.float32, cos_sin.shape, dev)
     ks = _rows(k, "k", cache, N, (torch.bfloat16, torch.float32))
     vs = _rows(v, "v", cache, N, (k.dtype,))
     Hq, qs, D = 0, 0, cache.head_dim
@@ -136,7 +154,8 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
             raise ValueError(f"q must have shape [{N}, Hq, {D}], got {tuple(q.shape)}")
         if q_out is None:
             q_out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
-        _need(q_out, "q_out", torch.bfloat16, (N, Hq, D), dev)
+        elif not isinstance(q_out, _T) or not _flat(q_out, _bf16, (N, Hq, D), dev):
+            _need(q_out, "q_out", _bf16, (N, Hq, D), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     r = KvRopeStruct(N, Hq, 1 if k.dtype == torch.float32 else 0, cos_sin.shape[1], 1 if interleaved else 0,
@@ -145,7 +164,8 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
         cache._ref, ctypes.byref(r), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
         positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), None if q_out is None else q_out.data_ptr(),
         _stream(stream, positions))
-    _native.check("kv_mxfp4_append_rope", rc)
+    if rc:
+        _native.check("kv_mxfp4_append_rope", rc)
     return q_out
 
 
@@ -180,10 +200,12 @@ def attention_kv_mxfp4_shared(q, cache: KvCacheMxfp4, shared_table, shared_len, 
     for t, name, shape in ((shared_table, "shared_table", (sb,)), (shared_len, "shared_len", (1,)),
                            (block_table, "block_table", (R, mb)), (seq_lens, "seq_lens", (R,)),
                            (query_start, "query_start", (R + 1,))):
-        _need(t, name, _i32, shape, dev)
+        if not isinstance(t, torch.Tensor) or not _flat(t, _i32, shape, dev):
+            _need(t, name, _i32, shape, dev)
     if out is None:
         out = _empty((N, Hq, D), torch.bfloat16, dev, stream)
-    _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
+    if not isinstance(out, torch.Tensor) or not _flat(out, torch.bfloat16, (N, Hq, D), dev):
+        _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
     a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, 0, qs, D ** -0.5 if scale is None else scale)

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
 
 // NT: token tiles of 8.  AHEAD: chunks of a warp whose weights are on their way.
 template <int NT, int AHEAD>
-__global__ void __launch_bounds__(32 * kStreamWarps) linear_stream_kernel(const LinearArgs a, int row_tiles) {
+__global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(const LinearArgs a, int row_tiles) {
   constexpr int COLS = 8 * NT;
   __shared__ float part[kStreamWarps][COLS * 16];
   __shared__ float sum[COLS * 16];
@@ -163,7 +163,7 @@ cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = splits;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = splits > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT, AHEAD>, a, row_tiles);
 }
 
@@ -172,7 +172,7 @@ cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
   if (a.T <= 8) return launch_stream<1, 4>(a, s);
   if (a.T <= 16) return launch_stream<2, 2>(a, s);
-  return launch_stream<4, 2>(a, s);
+  return launch_stream<4, 1>(a, s);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {

@@ -66,6 +66,11 @@ def _cuda(t, name):
     return t.device
 
 
+def _flat(t, dtype, shape, device) -> bool:
+    """Whether ``_need`` would pass (a call of a few microseconds asks this first and names what is wrong after)."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device
+
+
 class KvCacheMxfp4:
     """One layer's paged key/value cache in MXFP4.
 
@@ -190,15 +195,19 @@ def kv_append_mxfp4(cache: KvCacheMxfp4, k, v, slots, stream=None) -> None:
 def kv_gather_mxfp4(cache: KvCacheMxfp4, slots, k_out=None, v_out=None, stream=None):
     """The keys and values that ``slots`` int32 [N] hold: two bf16 [N, kv heads, head_dim] (exact; zeros for -1)."""
     _cuda(slots, "slots")
+    dev = cache.device
     N = slots.shape[0]
-    _need(slots, "slots", _i32, (N,), cache.device)
+    if slots.dtype is not _i32 or slots.dim() != 1 or not slots.is_contiguous() or slots.device != dev:
+        _need(slots, "slots", _i32, (N,), dev)
     shape = (N, cache.num_kv_heads, cache.head_dim)
     if k_out is None:
-        k_out = _empty(shape, torch.bfloat16, cache.device, stream)
+        k_out = _empty(shape, torch.bfloat16, dev, stream)
+    elif not isinstance(k_out, torch.Tensor) or not _flat(k_out, torch.bfloat16, shape, dev):
+        _need(k_out, "k_out", torch.bfloat16, shape, dev)
     if v_out is None:
-        v_out = _empty(shape, torch.bfloat16, cache.device, stream)
-    _need(k_out, "k_out", torch.bfloat16, shape, cache.device)
-    _need(v_out, "v_out", torch.bfloat16, shape, cache.device)
+        v_out = _empty(shape, torch.bfloat16, dev, stream)
+    elif not isinstance(v_out, torch.Tensor) or not _flat(v_out, torch.bfloat16, shape, dev):
+        _need(v_out, "v_out", torch.bfloat16, shape, dev)
     rc = _native.load().kv_mxfp4_gather(cache._ref, slots.data_ptr(), N, k_out.data_ptr(), v_out.data_ptr(),
                                         _stream(stream, slots))
     _native.check("kv_mxfp4_gather", rc)
