@@ -500,8 +500,9 @@ __device__ __forceinline__ void turn8(const Turn& r, const Raw8<F32>& raw, float
 // one head.  Warps up to ``q_warps`` of the grid take queries, the others keys and
 // values (the loop bounds are uniform per warp).
 constexpr int kQueryRows = 4;
+constexpr int rope_ctas(bool f32) { return f32 ? 2 : 3; }  // an SM: what its registers hold
 template <int D, bool F32, bool PAIRS>
-__global__ void __launch_bounds__(256) kv_append_rope_kernel(const KvView c, const RopeArgs a, int q_warps) {
+__global__ void __launch_bounds__(256, rope_ctas(F32)) kv_append_rope_kernel(const KvView c, const RopeArgs a, int q_warps) {
   constexpr int L = D / 8, W = 32 / L;  // lanes a unit, units a warp
   const int lane = threadIdx.x & 31, sub = lane % L;
   const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
@@ -644,8 +645,9 @@ cudaError_t launch_kv_append(const KvView& c, const void* k, const void* v, bool
 cudaError_t launch_kv_append_rope(const KvView& c, const RopeArgs& a, bool f32, bool pairs, int num_sms, cudaStream_t s) {
   const int W = 256 / c.D;  // units a warp
   const long long q_units = (long long)a.N * ((a.Hq + kQueryRows - 1) / kQueryRows), kv_units = (long long)a.N * c.heads;
-  // the grid's warps dealt to both kinds by their number of units
-  const long long most = (long long)num_sms * kRowCtas * 8;
+  // one wave of resident warps, dealt to both kinds by their number of units (written and read
+  // back, 16,384 tokens of 28 / 4 heads of 128: 3 CTAs an SM 57.7 us, 8, not all resident, 63.8)
+  const long long most = (long long)num_sms * rope_ctas(f32) * 8;
   long long qw = (q_units + W - 1) / W, kw = (kv_units + W - 1) / W;
   if (qw + kw > most) {
     const long long share = std::max<long long>(1, most * qw / (qw + kw));
