@@ -77,6 +77,7 @@ struct PromptCfg {
 struct PromptParams {
   KvAttnArgs a;
   int G, row_limit;
+  int slice_tiles;  // shared prefix: row tiles of a slice at most, 0: its slices are streamed
   int32_t* odd;  // [R] set for requests with scales outside the exact range
 };
 
@@ -281,7 +282,8 @@ struct PromptShared {
 // One item: the rows of request r from row0 on, of kv head kvh.  FEW: see kFewKeys.
 // SHARED: the call's requests share a prefix (KvShared); results are sums.
 template <int D, bool FEW, bool SHARED = false>
-__device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem, uint32_t tmem, int r, int kvh, int row0) {
+__device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem, uint32_t tmem, int r, int kvh, int row0,
+                                            const KvRequest* known = nullptr) {
   using C = PromptCfg<D>;
   constexpr int NB = D / 32, S = C::kStages;
   PromptShared<S>& sh = *reinterpret_cast<PromptShared<S>*>(smem + C::kBarOff);
@@ -290,7 +292,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   volatile int* abort_flag = &sh.abort_flag;
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const KvRequest rq = kv_request<SHARED>(a, r);
+  const KvRequest rq = SHARED ? *known : kv_request<SHARED>(a, r);
   const int qb = rq.qb, ql = rq.ql, n = rq.n;
   const int rows = min(ql * p.G - row0, 256);  // rows of this CTA
   const int first_pos = rq.first + row0 / p.G, last_pos = rq.first + (row0 + rows - 1) / p.G;
@@ -515,9 +517,13 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
               tc_ld_wait32(v);
             }
             if (real && nt > 0) {
-              uint4* dst = reinterpret_cast<uint4*>(a.sh.o + to * D + 32 * c);
+              // (32 bytes a store: whole sectors of the row)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 32; k += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a.sh.o + to * D + 32 * c + k),
+                             "r"(v[k]), "r"(v[k + 1]), "r"(v[k + 2]), "r"(v[k + 3]), "r"(v[k + 4]), "r"(v[k + 5]),
+                             "r"(v[k + 6]), "r"(v[k + 7])
+                             : "memory");
             }
           }
         } else {
@@ -747,6 +753,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PromptShared<S>& sh = *reinterpret_cast<PromptShared<S>*>(smem + C::kBarOff);
   __shared__ int item[4];  // request, kv head, first row, few keys?
+  __shared__ KvRequest request;  // (shared prefix)
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int H = a.cache.heads;
@@ -774,26 +781,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   if (warp == 0) {
     // this CTA's item: the last row tiles of a request first (they see the most keys), heads innermost
     __syncwarp();
+    // slices of a shared prefix come first, found without a look at the requests
+    const int slices = SHARED ? a.sh.splits * p.slice_tiles * H : 0;
+    if (SHARED && (int)blockIdx.x < slices) {
+      const int of = blockIdx.x / (p.slice_tiles * H), in = blockIdx.x % (p.slice_tiles * H);
+      const KvRequest rq = kv_request<SHARED>(a, a.R + of);
+      const long long rows = (long long)rq.ql * p.G;
+      if (lane == 0 && rows > a.sh.row_limit && rows > (long long)(in / H) * 256) {
+        item[0] = a.R + of;
+        item[1] = in % H;
+        item[2] = in / H * 256;
+        item[3] = rq.n <= kFewKeys;
+        request = rq;
+      }
+    }
+    const long long block = SHARED && (int)blockIdx.x < slices ? -1 : (long long)blockIdx.x - slices;
     long long before = 0;
-    const int R = SHARED ? a.R + a.sh.splits : a.R;
-    for (int r0 = 0; r0 < R; r0 += 32) {
+    for (int r0 = 0; r0 < a.R; r0 += 32) {
       const int r = r0 + lane;
       long long rows = 0;
-      if (SHARED && r >= a.R && r < R) {
-        rows = (long long)kv_request<SHARED>(a, r).ql * p.G;
-      } else if (r < R) {
+      if (r < a.R) {
         const int qb = min(max(a.query_start[r], 0), a.N);
         rows = (long long)max(min(min(max(a.query_start[r + 1], 0), a.N) - qb, a.max_q_len), 0) * p.G;
       }
-      const int limit = SHARED && r >= a.R ? a.sh.row_limit : p.row_limit;
-      const int tiles = rows > limit ? (int)((rows + 255) / 256) : 0;
+      const int tiles = rows > p.row_limit ? (int)((rows + 255) / 256) : 0;
       long long incl = (long long)tiles * H;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
       }
-      const long long off = (long long)blockIdx.x - before - (incl - (long long)tiles * H);
+      const long long off = block - before - (incl - (long long)tiles * H);
       if (off >= 0 && off < (long long)tiles * H) {
         const int qt = tiles - 1 - (int)(off / H);
         item[0] = r;
@@ -802,9 +820,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
         const KvRequest rq = kv_request<SHARED>(a, r);
         const int seen = rq.causal ? min(rq.n, rq.first + item[2] / p.G + 1) : rq.n;
         item[3] = min(seen, a.window ? a.window : seen) <= kFewKeys;
+        if (SHARED) request = rq;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
-      if (before > (long long)blockIdx.x) break;
+      if (before > block) break;
     }
   }
   tc_before();
@@ -814,8 +833,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
   const int r = item[0];
   if (r >= 0) {
     if constexpr (SHARED) {
-      if (item[3]) prompt_item<D, true, true>(p, smem, tmem, r, item[1], item[2]);
-      else prompt_item<D, false, true>(p, smem, tmem, r, item[1], item[2]);
+      if (item[3]) prompt_item<D, true, true>(p, smem, tmem, r, item[1], item[2], &request);
+      else prompt_item<D, false, true>(p, smem, tmem, r, item[1], item[2], &request);
     } else {
       if (item[3]) prompt_item<D, true>(p, smem, tmem, r, item[1], item[2]);
       else prompt_item<D, false>(p, smem, tmem, r, item[1], item[2]);
@@ -863,8 +882,9 @@ cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, c
   const long long most = rows / (row_limit + 1) < a.R ? rows / (row_limit + 1) : a.R;
   long long grid = (rows / 256 + most) * a.cache.heads;
   if (a.sh.splits > 0) {
-    // a slice of a shared prefix has all rows
-    if (rows > a.sh.row_limit) grid += (rows + 255) / 256 * a.sh.splits * a.cache.heads;
+    // a slice of a shared prefix has all rows (fewer than the limit are streamed)
+    p.slice_tiles = rows > a.sh.row_limit ? (int)((rows + 255) / 256) : 0;
+    grid += (long long)p.slice_tiles * a.sh.splits * a.cache.heads;
     if (grid == 0) return cudaSuccess;
     return a.cache.D == 128 ? launch_prompt<128, true>(p, (unsigned)grid, s) : launch_prompt<64, true>(p, (unsigned)grid, s);
   }

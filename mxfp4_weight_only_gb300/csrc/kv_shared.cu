@@ -25,61 +25,84 @@ constexpr int kSharedStreamRows = 32;
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// One warp a row (token x query head).
-template <int D>
+// One warp a row (token x query head).  Latency-bound: the row's sums are all on their
+// way while its request is looked up, kAhead parts at a time.
+template <int D, int kAhead>
 __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
   constexpr int V = D / 32;  // dims of a lane
   grid_dep_wait();
-  const int r = blockIdx.x, lane = threadIdx.x & 31;
-  const KvRequest q = kv_request<true>(a, r);
-  const bool gone = a.seq_lens[r] < 0;  // an empty place in the batch
-  const int parts = 1 + a.sh.splits;
-  const long long rows = (long long)max(q.ql, 0) * a.Hq, all = (long long)a.N * a.Hq;
-  for (long long i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
-    const long long row = (long long)q.qb * a.Hq + i;
-    // lane p: part p
-    float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    if (lane < parts && !gone) ml = a.sh.ml[lane * all + row];
-    const bool some = ml.y != 0.f;  // (NaN too)
-    const int E0 = some ? __float_as_int(ml.z) : -100000;
-    const int E = __reduce_max_sync(0xffffffffu, E0);
-    float M = some ? ml.x : -INFINITY;
+  const int lane = threadIdx.x & 31, parts = 1 + a.sh.splits;
+  const long long all = (long long)a.N * a.Hq, row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= all) return;
+  const float* src = a.sh.o + (size_t)row * D + V * lane;
+  float v[kAhead][V];
+  auto load = [&](int p0) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float w = some ? exp2f(4.f * (ml.x - (M == -INFINITY ? 0.f : M))) : 0.f;
-    float l = some ? w * ml.y : 0.f;
+    for (int u = 0; u < kAhead; ++u)
+      if (p0 + u < parts) {
+        const float* q = src + (size_t)(p0 + u) * all * D;
+        if constexpr (V == 4) *reinterpret_cast<float4*>(v[u]) = __ldcs(reinterpret_cast<const float4*>(q));
+        else *reinterpret_cast<float2*>(v[u]) = __ldcs(reinterpret_cast<const float2*>(q));
+      }
+  };
+  load(0);
+  // lane p: part p
+  float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (lane < parts) ml = a.sh.ml[lane * all + row];
+  // the token's request: the last that begins at or before it, 32 candidates at a time
+  const int tok = (int)(row / a.Hq);
+  int lo = 0, n = a.R;  // it is one of lo .. lo + n - 1, or the token is none's
+  while (n > 1) {
+    const int step = (n + 31) / 32, k = lane * step;
+    const bool begun = k < n && a.query_start[lo + k] <= tok;
+    const int c = __popc(__ballot_sync(0xffffffffu, begun));
+    if (c == 0) return;
+    lo += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
+  }
+  const KvRequest q = kv_request<true>(a, lo);
+  if (tok < q.qb || tok - q.qb >= q.ql) return;  // (none's, or past max_q_len)
+  const bool some = ml.y != 0.f && a.seq_lens[lo] >= 0;  // (NaN too; a negative length: an empty place in the batch)
+  const int E0 = some ? __float_as_int(ml.z) : -100000;
+  const int E = __reduce_max_sync(0xffffffffu, E0);
+  float M = some ? ml.x : -INFINITY;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (some && E0 != E) w *= exp2f((float)max(E0 - E, -300));
-    uint32_t there = __ballot_sync(0xffffffffu, some);
-    float o[V];
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float w = some ? exp2f(4.f * (ml.x - (M == -INFINITY ? 0.f : M))) : 0.f;
+  float l = some ? w * ml.y : 0.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] = 0.f;
-    for (; there; there &= there - 1) {
-      const int p = __ffs(there) - 1;
-      const float wp = __shfl_sync(0xffffffffu, w, p);
-      const float* src = a.sh.o + ((size_t)p * all + row) * D + V * lane;
-      float v[V];
-      if constexpr (V == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (some && E0 != E) w *= exp2f((float)max(E0 - E, -300));
+  const uint32_t there = __ballot_sync(0xffffffffu, some);
+  float o[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) o[k] = fmaf(v[k], wp, o[k]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int k = 0; k < V; ++k) o[k] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += kAhead) {
+    if (p0 > 0) load(p0);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      o[k] *= inv;
-      if (l != 0.f && E != 127) {  // two factors: either alone may leave the range
-        const int e = min(max(E - 127, -252), 252), h = e >> 1;
-        o[k] = o[k] * exp2_int(h) * exp2_int(e - h);
+    for (int u = 0; u < kAhead; ++u) {
+      const int p = p0 + u;
+      const float wp = __shfl_sync(0xffffffffu, w, p & 31);
+      if (p < parts && (there >> p & 1u)) {  // (the sums of others may be anything)
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = fmaf(v[u][k], wp, o[k]);
       }
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + V * lane);
-    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
-    else *dst = f32x2_to_bf16x2(o[0], o[1]);
-    if (lane == 0 && a.lse)
-      a.lse[row] = l == 0.f ? -INFINITY : M == -INFINITY ? l : fmaf(M, 2.772588722239781f, logf(l));
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    o[k] *= inv;
+    if (l != 0.f && E != 127) {  // two factors: either alone may leave the range
+      const int e = min(max(E - 127, -252), 252), h = e >> 1;
+      o[k] = o[k] * exp2_int(h) * exp2_int(e - h);
+    }
+  }
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + V * lane);
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(f32x2_to_bf16x2(o[0], o[1]), f32x2_to_bf16x2(o[2], o[3]));
+  else *dst = f32x2_to_bf16x2(o[0], o[1]);
+  if (lane == 0 && a.lse)
+    a.lse[row] = l == 0.f ? -INFINITY : M == -INFINITY ? l : fmaf(M, 2.772588722239781f, logf(l));
 }
 
 struct SharedLayout {
@@ -140,9 +163,12 @@ cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s) {
   // (row tiles as without a prefix; a streamed prefix has most of the keys)
   const long long streamed = all <= kSharedStreamRows ? all : own <= limit ? own : G;
   if ((e = launch_kv_stream(a, limit, odd, streamed <= 8 ? 1 : 2, ws, s)) != cudaSuccess) return e;
-  const long long want = (std::min<long long>(a.max_q_len, a.N) * a.Hq + 7) / 8;
-  const dim3 grid((unsigned)a.R, (unsigned)std::min<long long>(std::max<long long>(want, 1), 65535));
-  auto kern = a.cache.D == 128 ? kv_join_kernel<128> : kv_join_kernel<64>;
+  const dim3 grid((unsigned)(((long long)a.N * a.Hq + 7) / 8));
+  // (8 parts at a time leave room for twice the rows on an SM: 256 requests of 6 parts 86 us
+  // in all, 89 with 16 at a time; 64 of 20 parts 76, with 8 79)
+  const bool few = 1 + a.sh.splits <= 8;
+  auto kern = a.cache.D == 128 ? (few ? kv_join_kernel<128, 8> : kv_join_kernel<128, 16>)
+                               : (few ? kv_join_kernel<64, 8> : kv_join_kernel<64, 16>);
   return launch_kernel(kern, grid, dim3(256), 0, s, true, false, a);
 }
 
