@@ -37,7 +37,7 @@ extern "C" {
  *   act          LINEAR_ACT_*
  *   out_is_f32   0: bf16 results, 1: float32
  *   x_stride, res_stride, out_stride  elements between rows: x_stride a multiple
- *                of 8 and >= K, the others >= the columns of the result
+ *                of 8 and >= K, the others >= the columns of the result, all at most 2^38
  */
 typedef struct linear_mxfp4 {
   int32_t T, K, N, act, out_is_f32;

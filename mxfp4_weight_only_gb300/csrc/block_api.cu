@@ -13,7 +13,7 @@ bool linear_valid(const linear_mxfp4_t* d) {
   if (d->act < LINEAR_ACT_NONE || d->act > LINEAR_ACT_SWIGLU || (d->out_is_f32 != 0 && d->out_is_f32 != 1)) return false;
   if (d->act == LINEAR_ACT_SWIGLU && d->N % 2) return false;
   if ((long long)d->T * d->N > 1ll << 36) return false;
-  const int64_t cols = d->act == LINEAR_ACT_SWIGLU ? d->N / 2 : d->N, most = 1ll << 40;
+  const int64_t cols = d->act == LINEAR_ACT_SWIGLU ? d->N / 2 : d->N, most = 1ll << 38;  // (tensor maps: strides below 2^40 bytes)
   return d->x_stride % 8 == 0 && d->x_stride >= d->K && d->x_stride <= most && d->res_stride >= cols &&
          d->res_stride <= most && d->out_stride >= cols && d->out_stride <= most;
 }

@@ -884,6 +884,7 @@ cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, c
   if (a.sh.splits > 0) {
     // a slice of a shared prefix has all rows (fewer than the limit are streamed)
     p.slice_tiles = rows > a.sh.row_limit ? (int)((rows + 255) / 256) : 0;
+    if ((long long)a.max_q_len * p.G <= row_limit) grid = 0;  // no request of its own has enough rows
     grid += (long long)p.slice_tiles * a.sh.splits * a.cache.heads;
     if (grid == 0) return cudaSuccess;
     return a.cache.D == 128 ? launch_prompt<128, true>(p, (unsigned)grid, s) : launch_prompt<64, true>(p, (unsigned)grid, s);

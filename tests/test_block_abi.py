@@ -48,7 +48,7 @@ def test_linear_refusals(native):
     for kw in (dict(T=-1), dict(T=(1 << 24) + 1), dict(K=0), dict(K=48), dict(K=65568, x_stride=65568), dict(N=0), dict(N=(1 << 20) + 1),
                dict(act=-1), dict(act=4), dict(act=3, N=47), dict(out_is_f32=2), dict(x_stride=56), dict(x_stride=68),
                dict(res_stride=47), dict(out_stride=47), dict(T=1 << 24, N=1 << 13, res_stride=1 << 13, out_stride=1 << 13),
-               dict(out_stride=(1 << 40) + 1)):
+               dict(out_stride=(1 << 38) + 1), dict(x_stride=(1 << 38) + 8)):
         assert linear(native, **kw) == DIMS, kw
         d = native.LinearStruct(**{**LINEAR, **kw})
         assert native.load().linear_mxfp4_workspace_bytes(ctypes.byref(d)) == 0
