@@ -22,7 +22,7 @@
 //   24      MMAs (first CTA)
 //   25      TMA of the x tiles
 //   26      TMA of the packed weight, four steps (256 of K, a quad) at a time
-//   27      scale bytes of a quad, kScalesAhead quads ahead, to shared memory
+//   27      scale bytes of a quad to shared memory, loaded a quad ahead of the ring
 // Packed weights and scales do not come by loads of the converters: these would have to
 // land before the proxy fence that a converter needs each step (a quad took the
 // latency of its scale bytes, 1 us), and rows 1,792 bytes apart cost a wavefront of the load unit
@@ -56,8 +56,8 @@ constexpr int kTcThreads = 32 * (kScaleWarp + 1);
 constexpr int kRows = 128;              // rows of the weight a CTA
 constexpr int kABytes = kRows * 128;    // one step of them in bf16
 constexpr int kQuad = 4;                // steps of a load of packed weights
-constexpr int kRawStages = 3, kRawBytes = kRows * 128, kRawRows = 16;
-constexpr int kScaleBytes = kRows * 8, kScalesAhead = 3;
+constexpr int kRawStages = 3, kRawBytes = kRows * 128;
+constexpr int kScaleBytes = kRows * 8;
 constexpr int kChunk = 16;              // tokens that the epilogue takes at a time
 constexpr uint32_t kAccCols = 256, kCols = 512;
 
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == kRawWarp) {
-    // ---------------------------------------------------------------- packed weights, 16 rows a copy
+    // ---------------------------------------------------------------- packed weights
     if (lane == 0) {
       int gq = 0;
       bool ok = true;
@@ -416,11 +416,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
           if (gq >= kRawStages) ok = sh.abort_flag == 0 && mbar_wait(&sh.raw_empty[r], ((gq / kRawStages) - 1) & 1, a.status, limit);
           if (!ok) break;
           mbar_arrive_expect_tx(&sh.raw_full[r], kRawBytes);
-#pragma unroll
-          for (int k = 0; k < kRows / kRawRows; ++k) {
-            const int row = a.act == LINEAR_ACT_SWIGLU ? mt * 128 + rank * 64 + (k >> 1) * 16 + (k & 1) * a.cols
-                                                       : mt * 256 + rank * 128 + k * 16;
-            tma_load_2d(smem + kRawOff + r * kRawBytes + k * kRawRows * 128, &wmap, 128 * (q_lo + quad), row, &sh.raw_full[r]);
+          uint8_t* dst = smem + kRawOff + r * kRawBytes;
+          const int at = 128 * (q_lo + quad);
+          if (a.act == LINEAR_ACT_SWIGLU) {  // 16 gate rows and the 16 up rows of the same columns a copy
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k)
+              tma_load_3d(dst + k * (32 * 128), &wmap, at, mt * 128 + rank * 64 + 16 * k, 0, &sh.raw_full[r]);
+          } else {
+            tma_load_3d(dst, &wmap, at, mt * 256 + rank * 128, 0, &sh.raw_full[r]);
           }
         }
       }
@@ -439,8 +442,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
       for (int k = 0; k < 4; ++k) row[k] = tile < p.tiles ? weight_row(a, tile % p.m_tiles, rank, 32 * k + lane) : -1;
     };
     int ltile = cluster, lquad = 0;
+    const int tiles_mine = (p.tiles - cluster + clusters - 1) / clusters;
     rows_of(ltile);
-    uint2 v[kScalesAhead][4];
     auto fetch = [&](uint2 (&to)[4]) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -477,27 +480,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         rows_of(ltile);
       }
     };
-#pragma unroll
-    for (int u = 0; u < kScalesAhead; ++u) fetch(v[u]);
-    int gq = 0, u = 0;
+    // quad i's loads go out, then quad i - 1's arrive (two copies of this code: registers of a load
+    // on its way cannot be moved)
+    const int mine = tiles_mine * KQ;
     bool ok = true;
-    for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
-      for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
-        const int r = gq % kRawStages;
-        if (gq >= kRawStages) ok = mbar_wait_warp(&sh.raw_empty[r], ((gq / kRawStages) - 1) & 1, a.status, limit, &sh.abort_flag);
-        if (!ok) break;
+    auto turn = [&](int i, uint2 (&out)[4], uint2 (&in)[4]) {
+      if (i < mine) fetch(out);
+      if (i == 0 || i > mine || !ok) return;
+      const int gq = i - 1, r = gq % kRawStages;
+      if (gq >= kRawStages) ok = mbar_wait_warp(&sh.raw_empty[r], ((gq / kRawStages) - 1) & 1, a.status, limit, &sh.abort_flag);
+      if (!ok) return;
 #pragma unroll
-        for (int w = 0; w < kScalesAhead; ++w)
-          if (u == w) {
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint2*>(smem + kScaleOff + r * kScaleBytes + (32 * k + lane) * 8) = in[k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.raw_full[r]);
+    };
+    uint2 u[4], v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint2*>(smem + kScaleOff + r * kScaleBytes + (32 * k + lane) * 8) = v[w][k];
-            fetch(v[w]);
-          }
-        u = u + 1 == kScalesAhead ? 0 : u + 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.raw_full[r]);
-      }
+    for (int k = 0; k < 4; ++k) u[k] = v[k] = make_uint2(0u, 0u);
+    for (int i = 0; i <= mine && ok; i += 2) {
+      turn(i, u, v);
+      turn(i + 1, v, u);
     }
     if (!ok) sh.abort_flag = 1;
   } else if (rank == 0) {
@@ -642,7 +645,8 @@ cudaError_t launch_tc(const LinearArgs& a, int m_tiles, int splits, cudaStream_t
   if (e != cudaSuccess) return e;
   CUtensorMap map, wmap;
   if ((e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, BN / 2, false)) != cudaSuccess) return e;
-  if ((e = make_bytes_map(&wmap, a.w, a.N, a.K / 2, kRawRows)) != cudaSuccess) return e;
+  const bool gated = a.act == LINEAR_ACT_SWIGLU;
+  if ((e = make_bytes_map(&wmap, a.w, gated ? 2 : 1, a.cols, a.K / 2, gated ? 16 : kRows)) != cudaSuccess) return e;
   const LinearTc p{a, m_tiles, m_tiles * ((a.T + BN - 1) / BN), splits};
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = tc_config(splits, (unsigned)(SPLIT ? p.tiles : std::min(p.tiles, a.num_sms / 2)), attr, s);

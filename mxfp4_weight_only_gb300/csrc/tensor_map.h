@@ -45,17 +45,17 @@ inline cudaError_t make_rows_map(CUtensorMap* m, const void* base, long long row
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Bytes [rows][bytes] (rows a multiple of 16 bytes long): boxes of box_rows x 128 with the
-// 128-byte swizzle, zeros outside.
-inline cudaError_t make_bytes_map(CUtensorMap* m, const void* base, long long rows, long long bytes, int box_rows) {
+// Bytes [halves][rows][bytes] (a multiple of 16 bytes a row), dense: boxes of halves x box_rows x 128
+// with the 128-byte swizzle, zeros outside.
+inline cudaError_t make_bytes_map(CUtensorMap* m, const void* base, int halves, long long rows, long long bytes, int box_rows) {
   EncodeTiledFn enc;
   cudaError_t e = get_encoder(&enc);
   if (e != cudaSuccess) return e;
-  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)bytes};
-  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint64_t dims[3] = {(cuuint64_t)bytes, (cuuint64_t)rows, (cuuint64_t)halves};
+  const cuuint64_t strides[2] = {(cuuint64_t)bytes, (cuuint64_t)(bytes * rows)};
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)halves};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -67,6 +67,13 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_u32(smem_dst)),
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
 #endif
