@@ -162,6 +162,44 @@ def test_not_finite(m, T):
         assert np.isfinite(got[fine]).all()
 
 
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16, 20, 40])
+@pytest.mark.parametrize("K", [96, 128, 1056, 4096])
+def test_unlike_sizes(m, T, K):
+    """Values and scale bytes of very unlike size side by side, in some chunks of K only: what a kernel may hold in
+    fewer exponent bits has to be noticed."""
+    g = np.random.default_rng(T + K)
+    p = problem(T, K, 70, f32=True, seed=17)
+    x = p["x"].double().numpy().copy()
+    for k in range(0, K, 64):
+        kind = (k // 64) % 6
+        part = x[:, k: k + 32]
+        if kind == 0:
+            part *= 2.0 ** g.integers(-60, 1, part.shape)  # values far below the largest
+        elif kind == 1:
+            part[:] = 0.0
+        elif kind == 2:
+            part *= 2.0 ** -115  # close to the smallest normal number
+        elif kind == 3:
+            part *= 2.0 ** g.integers(-20, 20, (T, 1))  # tokens of unlike size
+        elif kind == 4:
+            part[:, ::2] = 0.0
+            part[:, 1::2] *= 2.0 ** -40
+    p["x"] = torch.from_numpy(x).bfloat16()
+    s = p["s"]
+    s[::3, ::2] = g.integers(60, 160, s[::3, ::2].shape)  # scales far apart in a row
+    s[1::7] = 0  # rows of the smallest scale
+    s[2::9, 0] = 0
+    p["w"][2::9, :16] = 0  # a block of zeros, as the conversion writes it
+    check(p, call(m, p))
+
+
+@pytest.mark.parametrize("T", [1, 7, 16])
+@pytest.mark.parametrize("K,N", [(128, 20000), (4096, 5500), (32768, 33), (8192, 700), (32, 16)])
+def test_many_tiles_and_deep_rows(m, T, K, N):
+    p = problem(T, K, N, bias=True, residual=True, seed=18)
+    check(p, call(m, p))
+
+
 def test_huge_activations(m):
     # products of 2^120, sums within float32
     for T in (1, 40, 300):
