@@ -495,7 +495,8 @@ __device__ __forceinline__ void turn8(const Turn& r, const Raw8<F32>& raw, float
 
 // Rotated queries and the quantising write of rotated keys and of values
 // (kv_mxfp4_append_rope).  HBM-bound: 2 or 4 bytes read a value, 2 bytes written of
-// a query and 17/32 of a key or value.  D / 8 lanes take a unit: up to kQueryRows
+// a query and 17/32 of a key or value (16,384 tokens of 28 / 4 heads of 128: bf16 50.1 us, 5.7
+// TB/s, float32 72.3, 6.0; 32 tokens 2.8 us, one launch).  D / 8 lanes take a unit: up to kQueryRows
 // query heads of one token, which share its cosines and sines, or the K and V row of
 // one head.  Warps up to ``q_warps`` of the grid take queries, the others keys and
 // values (the loop bounds are uniform per warp).

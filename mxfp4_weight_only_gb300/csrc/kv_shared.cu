@@ -9,6 +9,11 @@
 // attention kernels take as they take any other request (few rows: streamed;
 // many: tensor cores, one CTA per 256 rows, kv head and slice).  The requests' own
 // keys are parts too.  kv_join_kernel joins a row's parts.
+//
+// Measured, 28 / 4 heads of 128: 64 requests behind 32,768 tokens, up to 2048 own, 76 us: prefix 40
+// (14 tiles of 128 keys a CTA at 2.1 us, 7 us until the first scores, 4 after the last), own keys 20,
+// items cut between CTAs 4, parts joined 6.  4 requests behind 100,003: 54 us, the streaming
+// kernel's issue.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -20,7 +25,9 @@ namespace {
 constexpr size_t kStatusBytes = 256;
 // The plan is made for a GB300's SMs, so that a workspace's size depends on the sizes alone.
 constexpr int kPlanSms = 152;
-// Rows (tokens x query heads per kv head) up to which the prefix is streamed.
+// Rows (tokens x query heads per kv head) up to which the prefix is streamed (28 rows, 4 kv
+// heads, 100,003 keys: 54 us streamed, 86 on the tensor cores, where a tile of keys takes
+// 2.6 us however few its rows).
 constexpr int kSharedStreamRows = 32;
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }

@@ -1,6 +1,11 @@
 // The linear layer on MXFP4 weights (linear_a16w4_mxfp4) for few rows: the weight
 // is streamed from memory once, straight into the operands of m16n8k16 MMAs.
 //
+// Measured (device time in a CUDA graph, weights from memory): 3584 -> 4608, one row
+// 5.8 us, 8 rows 6.2, 16 7.8, 32 12.4; 4096 -> 14336, one row 15.2 us (1.9 TB/s).  Small
+// weights: latency of a launch, a load and a reduction; large ones: the issue of the
+// exact conversions, five instructions on two weights.
+//
 //   h[n][token] = sum_k W[n][k] x[token][k]
 //
 // A CTA takes 16 rows of the weight (SwiGLU: 8 gate rows and the 8 up rows of the
@@ -170,12 +175,17 @@ cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
+  // (chunks ahead: what two CTAs an SM have registers for; 32 rows with one CTA an SM and
+  // two chunks ahead 15.8 us instead of 13.7, 8 rows with three CTAs and three chunks 9.5
+  // instead of 6.2)
   if (a.T <= 8) return launch_stream<1, 4>(a, s);
   if (a.T <= 16) return launch_stream<2, 2>(a, s);
   return launch_stream<4, 1>(a, s);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  // 3584 -> 3584: 32 rows streamed 12.1 us, on the tensor cores 13.6; 33 rows and more take two
+  // passes over the weight if streamed
   if (a.T <= 32) return launch_linear_stream(a, s);
   return launch_linear_tc(a, s);
 }
