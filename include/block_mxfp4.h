@@ -115,7 +115,8 @@ int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, co
 
 /* Bytes of workspace that kv_mxfp4_attention_shared needs (256-byte aligned; 0 for
  * invalid sizes): as kv_mxfp4_attention's, but it grows with N * Hq * head_dim (a
- * float32 sum of each row, for its own keys and for every slice of the prefix). */
+ * float32 sum of each row, for its own keys and for every slice of the prefix).  The
+ * workspace of a call with more requests, rows or heads does for a smaller one too. */
 size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks);
 
 /*

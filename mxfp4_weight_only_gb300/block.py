@@ -171,7 +171,7 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
 
 def attention_shared_workspace_bytes(cache: KvCacheMxfp4, R: int, N: int, Hq: int, max_blocks: int, max_q_len: int,
                                      shared_blocks: int) -> int:
-    """Bytes of workspace for ``attention_kv_mxfp4_shared`` calls of these sizes."""
+    """Bytes of workspace for ``attention_kv_mxfp4_shared`` calls of these sizes, or of fewer requests and rows."""
     D = cache.head_dim
     a = KvAttnStruct(R, N, Hq, max_blocks, max_q_len, 1, 0, Hq * D, 1.0)
     return int(_native.load().kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ctypes.byref(a), shared_blocks))

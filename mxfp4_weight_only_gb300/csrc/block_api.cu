@@ -105,7 +105,9 @@ int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, co
 }
 
 size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks) {
-  return shared_valid(c, a, shared_blocks) ? kv_shared_workspace(view_of(c), a, shared_blocks) : 0;
+  if (!shared_valid(c, a, shared_blocks)) return 0;
+  const KvView view = view_of(c);
+  return kv_shared_workspace(view, a, kv_shared_splits(view, a, shared_blocks));
 }
 
 int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks, const void* q,
@@ -123,7 +125,10 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
       !aligned(query_start, 4) || !aligned(lse, 4))
     return MOE_ERR_ALIGN;
   const KvView view = view_of(c);
-  const size_t need = kv_shared_workspace(view, a, shared_blocks);
+  // fewer rows may be cut into more slices: a workspace for more rows does, with fewer of them
+  int splits = kv_shared_splits(view, a, shared_blocks);
+  while (splits > 1 && kv_shared_workspace(view, a, splits) > workspace_bytes) --splits;
+  const size_t need = kv_shared_workspace(view, a, splits);
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   const uint64_t heads = (uint64_t)a->N * (uint64_t)a->Hq, D = (uint64_t)c->head_dim, R = (uint64_t)a->R;
   const Span span[] = {{q, 2 * ((uint64_t)(a->N - 1) * (uint64_t)a->q_stride + (uint64_t)a->Hq * D)},
@@ -135,7 +140,7 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
   KvAttnArgs g = attn_args(view, a, q, block_table, seq_lens, query_start, out, lse, workspace, sms, wait);
-  g.sh.splits = kv_shared_splits(view, a, shared_blocks);
+  g.sh.splits = splits;
   g.sh.blocks = shared_blocks;
   g.sh.table = shared_table;
   g.sh.len = shared_len;

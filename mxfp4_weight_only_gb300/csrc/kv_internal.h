@@ -231,7 +231,7 @@ int kv_stream_rows(const KvAttnArgs& a);
 
 // Attention with a shared prefix: how it is cut, its workspace, the call.
 int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
-size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
+size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int splits);
 cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s);
 
 size_t kv_attention_workspace(const KvView& c, const kv_mxfp4_attn_t* a);

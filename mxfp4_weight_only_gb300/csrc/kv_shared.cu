@@ -148,8 +148,8 @@ int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
   return best;
 }
 
-size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
-  return shared_layout(c.D, a->R, a->N, a->Hq, kv_shared_splits(c, a, blocks)).total;
+size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int splits) {
+  return shared_layout(c.D, a->R, a->N, a->Hq, splits).total;
 }
 
 cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s) {

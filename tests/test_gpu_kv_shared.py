@@ -145,6 +145,40 @@ def test_several_query_rows(m, G, D, q, causal):
     both(m, problem(700, lens, [q, q, q, q, 3, max(1, q // 2)], 2, G, D, 32, seed=q, gaps=3), causal=causal)
 
 
+@pytest.mark.parametrize("G,D,lens,qlens", [
+    (7, 128, [300, 1, 200], [300, 1, 123]), (1, 64, [257, 1500], [257, 1300]), (16, 64, [130, 64, -1, 90], [130, 64, 2, 1]),
+    (5, 128, [500, 0, 129], [370, 30, 128]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_behind_a_prefix(m, G, D, lens, qlens, causal):
+    """Enough rows a request for the tensor-core kernel on its own keys too."""
+    both(m, problem(333, lens, qlens, 2, G, D, 64, seed=len(lens) + G), causal=causal, scale=0.1)
+
+
+def test_many_requests(m):
+    g = np.random.default_rng(2)
+    both(m, problem(200, g.integers(-1, 30, 700).tolist(), [1] * 700, 1, 2, 64, 16))
+
+
+def test_workspace_of_a_larger_batch(m):
+    """Fewer rows can be cut into more slices: a workspace for more of them has to do."""
+    H, G, D = 4, 7, 128
+    c = m.KvCacheMxfp4(4, 16, H, D)
+    size = [m.attention_shared_workspace_bytes(c, R, R, H * G, 1, 1, 128) for R in range(1, 80)]
+    R = next(i for i, (a, b) in enumerate(zip(size, size[1:]), 1) if a > b)
+    p = problem(128 * 16 - 3, [10] * R, [1] * R, H, G, D, 16, seed=3, extra=0)
+    assert len(p["shared"]) == 128 and p["table"].shape[1] == 1
+    c = m.KvCacheMxfp4(p["pages"], 16, H, D, data=torch.from_numpy(p["data"]).cuda())
+    q = p["q"].cuda()
+    out, lse = torch.empty_like(q), torch.empty(R, H * G, device="cuda")
+    args = (q, c, i32(p["shared"]), i32([p["P"]]), i32(p["table"]), i32(p["lens"]), i32(p["start"]), 1)
+    ws = torch.zeros(m.attention_shared_workspace_bytes(c, R + 1, R + 1, H * G, 1, 1, 128), dtype=torch.uint8, device="cuda")
+    m.attention_kv_mxfp4_shared(*args, scale=0.2, out=out, lse=lse, workspace=ws)
+    check(p, out, lse)
+    with pytest.raises(m.MoeError, match="WORKSPACE"):
+        m.attention_kv_mxfp4_shared(*args, scale=0.2, out=out, lse=lse, workspace=ws[: ws.numel() // 32])
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 def test_page_sizes(m, page):
     both(m, problem(777, [5, 257, 40] * 4, [1] * 12, 2, 4, 128, page, seed=page))

@@ -103,6 +103,25 @@ def test_columns(m, N, T):
     both(m, T, 192, N, seed=3, bias=True, residual=True)
 
 
+@pytest.mark.parametrize("T", [1, 33, 300])
+def test_small_gated_and_deepest(m, T):
+    for N in (2, 4, 30, 34, 258):
+        both(m, T, 96, N, act="swiglu", bias=True, residual=True, seed=19)
+    both(m, T, 65536, 5, bias=True, seed=20)
+
+
+@pytest.mark.parametrize("T", [2, 50, 300])
+@pytest.mark.parametrize("K", [32, 96, 160, 2080])
+@pytest.mark.parametrize("skip", [1, 2, 3])
+def test_scales_at_any_address(m, T, K, skip):
+    """Scale rows of an odd length that begin anywhere: slices of a taller array, whose other rows are NaN."""
+    p = problem(T, K, 50, seed=21)
+    tall = torch.full((50 + 2 * skip, K // 32), 255, dtype=torch.uint8, device="cuda")
+    s = tall[skip: skip + 50]
+    s.copy_(torch.from_numpy(p["s"]))
+    check(p, m.linear_a16w4_mxfp4(on_gpu(p["x"]), torch.from_numpy(p["w"]).cuda(), s))
+
+
 @pytest.mark.parametrize("act", [None, "silu", "gelu", "swiglu"])
 @pytest.mark.parametrize("bias,residual,f32", [(False, False, False), (True, False, True), (False, True, True), (True, True, False)])
 @pytest.mark.parametrize("T", [3, 50, 140, 600])
