@@ -2,7 +2,7 @@
 // is streamed from memory once, straight into the operands of m16n8k16 MMAs.
 //
 // Measured (device time in a CUDA graph, weights from memory): 3584 -> 4608, one row
-// 5.8 us, 8 rows 6.2, 16 7.8, 32 12.4; 4096 -> 14336, one row 15.2 us (1.9 TB/s).  Small
+// 5.8 us, 8 rows 6.2, 16 7.8, 24 8.4, 32 9.5; 4096 -> 14336, one row 15.2 us (1.9 TB/s).  Small
 // weights: latency of a launch, a load and a reduction; large ones: the issue of the
 // exact conversions, five instructions on two weights.
 //
@@ -22,7 +22,9 @@
 
 #include <cooperative_groups.h>
 
+#include "kv_internal.h"
 #include "linear.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 
@@ -49,13 +51,12 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
 
 // NT: token tiles of 8.  AHEAD: chunks of a warp whose weights are on their way.
 template <int NT, int AHEAD>
-__global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(const LinearArgs a, int row_tiles) {
+__global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(const LinearArgs a) {
   constexpr int COLS = 8 * NT;
   __shared__ float part[kStreamWarps][COLS * 16];
   __shared__ float sum[COLS * 16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int tile = blockIdx.x % row_tiles, tok0 = blockIdx.x / row_tiles * COLS;
-  const int splits = gridDim.y, step = kStreamWarps * splits;
+  const int tile = blockIdx.x, splits = gridDim.y, step = kStreamWarps * splits;
   const int KB = a.K >> 5, chunks = (KB + 3) >> 2;
   const bool gated = a.act == LINEAR_ACT_SWIGLU;
   // rows g and g + 8 of the tile
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
       uint4 x[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int tok = tok0 + 8 * n + g;
+        const int tok = 8 * n + g;
         const bool there = tok < a.T && b < KB;
         const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)tok * a.x_stride + 32 * b);
 #pragma unroll
@@ -141,51 +142,233 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
   __syncthreads();
   const int per = gated ? 8 : 16;  // columns of the result a tile
   for (int e = threadIdx.x; e < COLS * per; e += 32 * kStreamWarps) {
-    const int n = e / per, r = e % per, col = tile * per + r, tok = tok0 + n;
-    if (col >= a.cols || tok >= a.T) continue;
+    const int n = e / per, r = e % per, col = tile * per + r;
+    if (col >= a.cols || n >= a.T) continue;
     float h = sum[n * 16 + r] + linear_bias(a, col);
     if (gated) h = silu(h) * (sum[n * 16 + 8 + r] + linear_bias(a, a.cols + col));
     else h = linear_act(a.act, h);
-    linear_store(a, tok, col, h);
+    linear_store(a, n, col, h);
   }
 }
 
-template <int NT, int AHEAD>
-cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
-  const int per = a.act == LINEAR_ACT_SWIGLU ? 8 : 16;
-  const int row_tiles = (a.cols + per - 1) / per;
-  const long long tiles = (long long)row_tiles * ((a.T + 8 * NT - 1) / (8 * NT));
-  // K shared between CTAs where there are too few tiles for the SMs, down to one chunk a warp
-  int splits = 1;
-  while (splits < 8 && tiles * splits < a.num_sms && kStreamWarps * splits * 128 < a.K) splits *= 2;
+// ------------------------------------------------------------------ 17 to 32 rows
+//
+// The same products, 32 rows of the weight a CTA, x by TMA: each warp has a ring of its
+// own that x of its next kXStages chunks is on its way into, 64 columns a box, zeros
+// outside.  (Loads of the lanes, as above, would be 64-byte pieces of eight rows, without
+// registers to have the next chunk's under way: 3584 -> 3584, 32 rows 12.1 us instead of
+// 9.2, 8192 -> 28672 132 instead of 88.)
+constexpr int kXStages = 3;
+template <int NT>
+constexpr int kXBytes = 8 * NT * 256;  // of a chunk: tokens x 128
+template <int NT>
+constexpr int kWideSmem = 1024 + kStreamWarps * kXStages * kXBytes<NT>;
+
+template <int NT>
+__global__ void __launch_bounds__(32 * kStreamWarps, 1) linear_wide_kernel(const __grid_constant__ CUtensorMap map,
+                                                                          const LinearArgs a) {
+  constexpr int MT = 2, ROWS = 16 * MT, COLS = 8 * NT, AHEAD = 2, kBytes = kXBytes<NT>;
+  static_assert((kStreamWarps + 1) * COLS * ROWS * 4 <= kStreamWarps * kXStages * kBytes, "sums fit into the rings");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t bars[kStreamWarps][kXStages];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
+  const int tile = blockIdx.x, splits = gridDim.y, step = kStreamWarps * splits, first = warp * splits + blockIdx.y;
+  const int KB = a.K >> 5, chunks = (KB + 3) >> 2, cnt = first < chunks ? (chunks - first + step - 1) / step : 0;
+  const bool gated = a.act == LINEAR_ACT_SWIGLU;
+  const int per = gated ? ROWS / 2 : ROWS;  // columns of the result a tile
+  uint8_t* ring = smem + warp * (kXStages * kBytes);
+
+  auto issue = [&](int i) {  // x of this warp's chunk i: two boxes of 64 columns
+    if (lane == 0 && i < cnt) {
+      const int s = i % kXStages, k = 128 * (first + i * step);
+      mbar_arrive_expect_tx(&bars[warp][s], kBytes);
+      tma_load_2d(ring + s * kBytes, &map, k, 0, &bars[warp][s]);
+      tma_load_2d(ring + s * kBytes + kBytes / 2, &map, k + 64, 0, &bars[warp][s]);
+    }
+  };
+  // weight rows: of row tile m, g and g + 8
+  long long row[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = tile * per + (gated ? 8 * m + g : 16 * m + 8 * h + g);
+      row[m][h] = col < a.cols ? (long long)(gated && h ? col + a.cols : col) * KB : -1;
+    }
+  uint4 wq[AHEAD][MT][2];
+  uint32_t sc[AHEAD][MT][2];
+  auto load = [&](int p, int i) {
+    const int b = 4 * (first + i * step) + t;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wq[p][m][h] = make_uint4(0u, 0u, 0u, 0u);
+        sc[p][m][h] = 127u;
+        if (row[m][h] >= 0 && i < cnt && b < KB) {
+          wq[p][m][h] = load_once(a.w + (row[m][h] + b) * 16);
+          sc[p][m][h] = __ldg(a.ws + row[m][h] + b);
+        }
+      }
+  };
+#pragma unroll
+  for (int p = 0; p < AHEAD; ++p) load(p, p);
+  if (lane == 0) {
+    for (int s = 0; s < kXStages; ++s) mbar_init(&bars[warp][s], 1 + a.wait.extra_waiters);
+    fence_barrier_init();
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kXStages; ++i) issue(i);
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+
+  bool ok = true;
+  int i = 0;
+  while (i < cnt && ok) {
+#pragma unroll
+    for (int p = 0; p < AHEAD; ++p) {
+      if (i >= cnt || !ok) break;
+      uint4 w[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (lanes of the second box take the block's halves the other way round: the
+          // eight reads of x of a quarter warp then fall into different banks)
+          const uint4 q = wq[p][m][h];
+          linear_block(t & 2 ? make_uint4(q.z, q.w, q.x, q.y) : q, sc[p][m][h], w[m][h]);
+        }
+      load(p, i + AHEAD);
+      const int s = i % kXStages;
+      ok = mbar_wait_warp(&bars[warp][s], (i / kXStages) & 1, a.status, a.wait.limit_ns);
+      if (!ok) break;
+      // block t of the chunk: 16-byte pieces 4 (t & 1) .. of a token's row in box t / 2
+      const uint8_t* box = ring + s * kBytes + (t >> 1) * (kBytes / 2);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = *reinterpret_cast<const uint4*>(box + (8 * n + g) * 128 + (((4 * (t & 1) + (k ^ (t & 2))) ^ g) << 4));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            mma_bf16(acc[m][n], w[m][0][k].x, w[m][1][k].x, w[m][0][k].y, w[m][1][k].y, x[k].x, x[k].y);
+            mma_bf16(acc[m][n], w[m][0][k].z, w[m][1][k].z, w[m][0][k].w, w[m][1][k].w, x[k].z, x[k].w);
+          }
+      }
+      __syncwarp();  // the stage has been read
+      issue(i + kXStages);
+      ++i;
+    }
+  }
+  if (!ok)  // copies in flight land before the ring is used again
+    for (int k = i; k < min(i + kXStages, cnt); ++k)
+      mbar_wait_warp(&bars[warp][k % kXStages], (k / kXStages) & 1, a.status, a.wait.limit_ns);
+  __syncthreads();
+  // the warps' sums, in the rings: [warp][token][row]
+  float(*part)[COLS * ROWS] = reinterpret_cast<float(*)[COLS * ROWS]>(smem);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) part[warp][(8 * n + 2 * t + (k & 1)) * ROWS + 16 * m + g + 8 * (k >> 1)] = acc[m][n][k];
+  __syncthreads();
+  float* sum = part[kStreamWarps];
+  for (int e = threadIdx.x; e < COLS * ROWS; e += 32 * kStreamWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kStreamWarps; ++w) v += part[w][e];
+    sum[e] = v;
+  }
+  if (splits > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (blockIdx.y == 0)
+      for (int e = threadIdx.x; e < COLS * ROWS; e += 32 * kStreamWarps)
+        for (int z = 1; z < splits; ++z) sum[e] += *cluster.map_shared_rank(&sum[e], z);
+    cluster.sync();
+    if (blockIdx.y) return;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < COLS * per; e += 32 * kStreamWarps) {
+    const int n = e / per, r = e % per, col = tile * per + r;
+    if (col >= a.cols || n >= a.T) continue;
+    // (gated: of every 16 rows, 8 gates and their ups)
+    const int at = n * ROWS + (gated ? 16 * (r >> 3) + (r & 7) : r);
+    float h = sum[at] + linear_bias(a, col);
+    if (gated) h = silu(h) * (sum[at + 8] + linear_bias(a, a.cols + col));
+    else h = linear_act(a.act, h);
+    linear_store(a, n, col, h);
+  }
+}
+
+// A launch whose CTAs of one tile (gridDim.y of them) form a cluster.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, size_t smem, cudaStream_t s, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)tiles, splits);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kStreamWarps);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = splits;
+  attr[0].val.clusterDim.y = grid.y;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT, AHEAD>, a, row_tiles);
+  cfg.numAttrs = grid.y > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+// K shared between CTAs where there are too few tiles for the SMs, down to one chunk a warp.
+// Up to ``limit`` CTAs before the last doubling.
+int stream_splits(const LinearArgs& a, int tiles, int limit) {
+  int splits = 1;
+  while (splits < 8 && tiles * splits < limit && kStreamWarps * splits * 128 < a.K) splits *= 2;
+  return splits;
+}
+
+template <int NT>
+cudaError_t launch_wide(const LinearArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = allow_shared(linear_wide_kernel<NT>, kWideSmem<NT>, done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if ((e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, 8 * NT, false)) != cudaSuccess) return e;
+  const int per = a.act == LINEAR_ACT_SWIGLU ? 16 : 32, tiles = (a.cols + per - 1) / per;
+  // (one CTA an SM: no split into a second wave.  112 tiles in two halves 16 us instead of 10)
+  return launch_clusters(linear_wide_kernel<NT>, dim3(tiles, stream_splits(a, tiles, a.num_sms / 2 + 1)), kWideSmem<NT>, s, map, a);
+}
+
+template <int NT, int AHEAD>
+cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
+  const int per = a.act == LINEAR_ACT_SWIGLU ? 8 : 16, tiles = (a.cols + per - 1) / per;
+  return launch_clusters(linear_stream_kernel<NT, AHEAD>, dim3(tiles, stream_splits(a, tiles, a.num_sms)), 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
-  // (chunks ahead: what two CTAs an SM have registers for; 32 rows with one CTA an SM and
-  // two chunks ahead 15.8 us instead of 13.7, 8 rows with three CTAs and three chunks 9.5
-  // instead of 6.2)
+  // (chunks ahead: what two CTAs an SM have registers for; 8 rows with three CTAs and three
+  // chunks 9.5 us instead of 6.2)
   if (a.T <= 8) return launch_stream<1, 4>(a, s);
   if (a.T <= 16) return launch_stream<2, 2>(a, s);
-  return launch_stream<4, 1>(a, s);
+  // 3584 -> 3584: 24 rows 8.2 us, streamed 10.9 (512 -> 512: 3.8 and 2.8); 16 rows 7.5 and 7.6
+  // (512 -> 512: 3.4 and 2.4)
+  if (a.T <= 24) return launch_wide<3>(a, s);
+  return launch_wide<4>(a, s);
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  // 3584 -> 3584: 32 rows streamed 12.1 us, on the tensor cores 13.6; 33 rows and more take two
-  // passes over the weight if streamed
+  // 3584 -> 3584: 32 rows 9.2 us, on the tensor cores 13.3; 33 rows and more would take two
+  // passes over the weight
   if (a.T <= 32) return launch_linear_stream(a, s);
   return launch_linear_tc(a, s);
 }

@@ -1,7 +1,7 @@
 """The give-up path of the linear layer's and the shared prefix's bounded waits, run on the GPU without a fault.
 
 The wait hook (moe_set_wait_limit) gives the next call a 1 ms limit and makes one of its waits expect an arrival more than
-will come (a full stage of the linear layer's tensor-core kernel, a tile's weights or a record of the attention's), so the
+will come (a full stage of the linear layer's tensor-core kernel, a chunk of x of its kernel for few rows, a tile's weights or a record of the attention's), so the
 real wait code runs out: the kernels must record MOE_STATUS_WAIT_TIMEOUT, stop and return, and the next calls on the
 workspace are right."""
 
@@ -31,16 +31,20 @@ def give_up(m, call, status, good):  # noqa: F811
         assert status() == 0
 
 
-# one tile, several tiles a pair, K split in two, in three and in four
+# tensor cores: one tile, several tiles a pair, K split in two, in three and in four
 @pytest.mark.parametrize("T,K,N", [(64, 256, 100), (700, 512, 7000), (300, 1600, 6200), (300, 2400, 4000), (40, 3200, 600)])
 def test_linear(m, T, K, N):  # noqa: F811
-    p = linear.problem(T, K, N, bias=True, seed=1)
+    check_linear(m, T, K, N, None)
+
+
+def check_linear(m, T, K, N, act):  # noqa: F811
+    p = linear.problem(T, K, N, act=act, bias=True, seed=1)
     x, w, s, b = linear.on_gpu(p["x"]), torch.from_numpy(p["w"]).cuda(), torch.from_numpy(p["s"]).cuda(), p["b"].cuda()
     ws = torch.zeros(m.linear_workspace_bytes(T, N, K), dtype=torch.uint8, device="cuda")
     want = []
 
     def call():
-        out = m.linear_a16w4_mxfp4(x, w, s, bias=b, workspace=ws)
+        out = m.linear_a16w4_mxfp4(x, w, s, bias=b, act=act, workspace=ws)
         torch.cuda.synchronize()
         return out
 
@@ -51,6 +55,12 @@ def test_linear(m, T, K, N):  # noqa: F811
         assert torch.equal(out, want[0])
 
     give_up(m, call, lambda: m.linear_read_status(ws), good)
+
+
+# a cluster, one chunk, more chunks than a warp's ring, partial ones
+@pytest.mark.parametrize("T,K,N,act", [(32, 1600, 600, None), (20, 96, 4000, None), (17, 5152, 9000, "silu"), (25, 4096, 700, "swiglu")])
+def test_linear_few_rows(m, T, K, N, act):  # noqa: F811
+    check_linear(m, T, K, N, act)
 
 
 @pytest.mark.parametrize("P,R,H,G,D", [(700, 40, 2, 4, 64), (500, 3, 2, 4, 128), (300, 60, 4, 7, 128)])

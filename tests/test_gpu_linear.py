@@ -103,6 +103,13 @@ def test_columns(m, N, T):
     both(m, T, 192, N, seed=3, bias=True, residual=True)
 
 
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("T,N", [(17, 2), (18, 34), (24, 1110), (25, 62), (32, 5000)])
+@pytest.mark.parametrize("K", [32, 96, 1056, 3200, 8224])  # a part of a chunk .. more chunks than a warp has on the way
+def test_up_to_32_rows(m, T, N, K, act):
+    both(m, T, K, N, act=act, bias=True, residual=True, seed=22)
+
+
 @pytest.mark.parametrize("T", [1, 33, 300])
 def test_small_gated_and_deepest(m, T):
     for N in (2, 4, 30, 34, 258):
