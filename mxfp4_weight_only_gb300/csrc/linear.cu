@@ -1,5 +1,5 @@
-// The linear layer on MXFP4 weights (linear_a16w4_mxfp4) for few rows: the weight
-// is streamed from memory once, straight into the operands of m16n8k16 MMAs.
+// The linear layer on MXFP4 weights (linear_a16w4_mxfp4) for few rows, or few tiles: the
+// weight is streamed from memory, straight into the operands of m16n8k16 MMAs.
 //
 // Measured (device time in a CUDA graph, weights from memory): 3584 -> 4608, one row
 // 5.8 us, 8 rows 6.2, 16 7.8, 24 8.4, 32 9.5; 4096 -> 14336, one row 15.2 us (1.9 TB/s).  Small
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
   }
 }
 
-// ------------------------------------------------------------------ 17 to 32 rows
+// ------------------------------------------------------------------ more than 16 rows
 //
-// The same products, 32 rows of the weight a CTA, x by TMA: each warp has a ring of its
+// The same products, 32 rows of the weight and up to 32 tokens a CTA, x by TMA: each warp has a ring of its
 // own that x of its next kXStages chunks is on its way into, 64 columns a box, zeros
 // outside.  (Loads of the lanes, as above, would be 64-byte pieces of eight rows, without
 // registers to have the next chunk's under way: 3584 -> 3584, 32 rows 12.1 us instead of
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) linear_wide_kernel(const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t bars[kStreamWarps][kXStages];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
-  const int tile = blockIdx.x, splits = gridDim.y, step = kStreamWarps * splits, first = warp * splits + blockIdx.y;
+  const int tile = blockIdx.x, tok0 = blockIdx.z * COLS, splits = gridDim.y, step = kStreamWarps * splits, first = warp * splits + blockIdx.y;
   const int KB = a.K >> 5, chunks = (KB + 3) >> 2, cnt = first < chunks ? (chunks - first + step - 1) / step : 0;
   const bool gated = a.act == LINEAR_ACT_SWIGLU;
   const int per = gated ? ROWS / 2 : ROWS;  // columns of the result a tile
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) linear_wide_kernel(const
     if (lane == 0 && i < cnt) {
       const int s = i % kXStages, k = 128 * (first + i * step);
       mbar_arrive_expect_tx(&bars[warp][s], kBytes);
-      tma_load_2d(ring + s * kBytes, &map, k, 0, &bars[warp][s]);
-      tma_load_2d(ring + s * kBytes + kBytes / 2, &map, k + 64, 0, &bars[warp][s]);
+      tma_load_2d(ring + s * kBytes, &map, k, tok0, &bars[warp][s]);
+      tma_load_2d(ring + s * kBytes + kBytes / 2, &map, k + 64, tok0, &bars[warp][s]);
     }
   };
   // weight rows: of row tile m, g and g + 8
@@ -299,14 +299,14 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) linear_wide_kernel(const
   }
   __syncthreads();
   for (int e = threadIdx.x; e < COLS * per; e += 32 * kStreamWarps) {
-    const int n = e / per, r = e % per, col = tile * per + r;
-    if (col >= a.cols || n >= a.T) continue;
+    const int n = e / per, r = e % per, col = tile * per + r, tok = tok0 + n;
+    if (col >= a.cols || tok >= a.T) continue;
     // (gated: of every 16 rows, 8 gates and their ups)
     const int at = n * ROWS + (gated ? 16 * (r >> 3) + (r & 7) : r);
     float h = sum[at] + linear_bias(a, col);
     if (gated) h = silu(h) * (sum[at + 8] + linear_bias(a, a.cols + col));
     else h = linear_act(a.act, h);
-    linear_store(a, n, col, h);
+    linear_store(a, tok, col, h);
   }
 }
 
@@ -335,6 +335,10 @@ int stream_splits(const LinearArgs& a, int tiles, int limit) {
   return splits;
 }
 
+int wide_tiles(const LinearArgs& a) {
+  const int per = a.act == LINEAR_ACT_SWIGLU ? 16 : 32;
+  return (a.cols + per - 1) / per;
+}
 template <int NT>
 cudaError_t launch_wide(const LinearArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
@@ -342,9 +346,10 @@ cudaError_t launch_wide(const LinearArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   if ((e = make_rows_map(&map, a.x, a.T, a.K, a.x_stride, 8 * NT, false)) != cudaSuccess) return e;
-  const int per = a.act == LINEAR_ACT_SWIGLU ? 16 : 32, tiles = (a.cols + per - 1) / per;
+  const int tiles = wide_tiles(a), tok_tiles = (a.T + 8 * NT - 1) / (8 * NT);
   // (one CTA an SM: no split into a second wave.  112 tiles in two halves 16 us instead of 10)
-  return launch_clusters(linear_wide_kernel<NT>, dim3(tiles, stream_splits(a, tiles, a.num_sms / 2 + 1)), kWideSmem<NT>, s, map, a);
+  const dim3 grid(tiles, stream_splits(a, tiles * tok_tiles, a.num_sms / 2 + 1), tok_tiles);
+  return launch_clusters(linear_wide_kernel<NT>, grid, kWideSmem<NT>, s, map, a);
 }
 
 template <int NT, int AHEAD>
@@ -367,9 +372,10 @@ cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  // 3584 -> 3584: 32 rows 9.2 us, on the tensor cores 13.3; 33 rows and more would take two
-  // passes over the weight
-  if (a.T <= 32) return launch_linear_stream(a, s);
+  // 3584 -> 3584: 32 rows 9.2 us, with tcgen05 13.3; more rows take more passes over the weight
+  // (in one wave of CTAs: 64 x 3584 -> 2048 9.1 and 13.1, 128 x 8192 -> 1024 15.4 and 19.1, 256 x 512 -> 512
+  // 4.4 and 10.2; in two: 96 x 3584 -> 2048 16.6 and 13.6, 256 x 8192 -> 1024 29.3 and 20.9)
+  if (a.T <= 32 || (long long)wide_tiles(a) * ((a.T + 31) / 32) <= a.num_sms) return launch_linear_stream(a, s);
   return launch_linear_tc(a, s);
 }
 

@@ -31,7 +31,7 @@ def give_up(m, call, status, good):  # noqa: F811
         assert status() == 0
 
 
-# tensor cores: one tile, several tiles a pair, K split in two, in three and in four
+# few tiles (the first and the last), many: several tiles a pair of CTAs, K split in two and in three
 @pytest.mark.parametrize("T,K,N", [(64, 256, 100), (700, 512, 7000), (300, 1600, 6200), (300, 2400, 4000), (40, 3200, 600)])
 def test_linear(m, T, K, N):  # noqa: F811
     check_linear(m, T, K, N, None)
@@ -57,8 +57,15 @@ def check_linear(m, T, K, N, act):  # noqa: F811
     give_up(m, call, lambda: m.linear_read_status(ws), good)
 
 
-# a cluster, one chunk, more chunks than a warp's ring, partial ones
-@pytest.mark.parametrize("T,K,N,act", [(32, 1600, 600, None), (20, 96, 4000, None), (17, 5152, 9000, "silu"), (25, 4096, 700, "swiglu")])
+# tensor cores: more than one wave of small tiles, K split in four and in two, not split
+@pytest.mark.parametrize("T,K,N", [(40, 3200, 4860), (64, 512, 9000), (700, 256, 300)])
+def test_linear_tiles(m, T, K, N):  # noqa: F811
+    check_linear(m, T, K, N, "silu")
+
+
+# streamed: a cluster, one chunk, more chunks than a warp's ring, partial ones, tiles of tokens
+@pytest.mark.parametrize("T,K,N,act", [(32, 1600, 600, None), (20, 96, 4000, None), (17, 5152, 9000, "silu"), (25, 4096, 700, "swiglu"),
+                                       (100, 4000, 290, "gelu")])
 def test_linear_few_rows(m, T, K, N, act):  # noqa: F811
     check_linear(m, T, K, N, act)
 
