@@ -2,7 +2,7 @@
 // weight is streamed from memory, straight into the operands of m16n8k16 MMAs.
 //
 // Measured (device time in a CUDA graph, weights from memory): 3584 -> 4608, one row
-// 5.8 us, 8 rows 6.2, 16 7.8, 24 8.4, 32 9.5; 4096 -> 14336, one row 15.2 us (1.9 TB/s).  Small
+// 5.5 us, 8 rows 5.8, 16 7.5, 24 8.4, 32 9.4; 4096 -> 14336, one row 14.7 us (2.1 TB/s).  Small
 // weights: latency of a launch, a load and a reduction; large ones: the issue of the
 // exact conversions, five instructions on two weights.
 //

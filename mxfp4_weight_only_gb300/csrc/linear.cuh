@@ -34,13 +34,33 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 #ifdef __CUDACC__
 
 // 32 weights of a block as 16 words of two bf16, exact: codes to f16 pairs, each
-// value to float32 (on the multiply-add pipe), whose upper halves are the bf16 values,
-// put together by a byte permute, times 2^(s-127) (s = 0: subnormal; 255: NaN).  The
-// ALU pipe, which the conversions and permutes share, bounds the tensor-core kernel's
-// converters.
+// value to float32 times 2^(s-127) (a mixed multiply-add), whose upper halves are the bf16
+// values, put together by a byte permute.  Scales that f16 does not hold (s = 0: subnormal;
+// 255: NaN) are multiplied in bf16 (all so: one row x 3584 -> 4608 5.8 us instead of 5.5, 8192
+// rows gated 240 instead of 234).  The ALU pipe, which the conversions and permutes share,
+// bounds the tensor-core kernel's converters.
 __device__ __forceinline__ void linear_block(const uint4& q, uint32_t s, uint4 (&out)[4]) {
-  const uint32_t f = s == 0u ? 0x00400040u : s == 255u ? 0x7FFF7FFFu : s * 0x00800080u;
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (s - 103u < 40u) {
+    const uint16_t f = s >= 113u ? (s - 112u) << 10 : 1u << (s - 103u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4], o[4];
+      e2m1x8_to_f16x8(w[i], h[0], h[1], h[2], h[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n fma.rn.f32.f16 %0, l, %3, 0f00000000;\n"
+            " fma.rn.f32.f16 %1, h, %3, 0f00000000;\n}"
+            : "=f"(lo), "=f"(hi)
+            : "r"(h[k]), "h"(f));
+        o[k] = prmt(__float_as_uint(lo), __float_as_uint(hi), 0x7632u);
+      }
+      out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    return;
+  }
+  const uint32_t f = s == 0u ? 0x00400040u : s == 255u ? 0x7FFF7FFFu : s * 0x00800080u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t h[4], o[4];

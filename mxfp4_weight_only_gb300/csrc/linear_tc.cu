@@ -1,7 +1,7 @@
 // The linear layer on MXFP4 weights (linear_a16w4_mxfp4) for many rows: tcgen05 MMAs
 // of CTA pairs, weights converted on the way into shared memory.
 //
-// Measured: 8192 rows x 3584 -> 2 x 3584 gated 239 us, 1,760 TFLOP/s (92 % of the library's
+// Measured: 8192 rows x 3584 -> 2 x 3584 gated 234 us, 1,800 TFLOP/s (92 % of the library's
 // bf16 matrix product; 265 us on data that draws more power), tensor pipe 76 % active: a
 // step's conversions (580 to 690 cycles) are a little longer than its MMAs (512).  250 x 3584 ->
 // 8192 21.2 us: 28 steps of 0.3 us, 6 us to the first MMA and after the last, 4 us of sums handed over.
