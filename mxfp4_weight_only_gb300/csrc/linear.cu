@@ -2,7 +2,7 @@
 // weight is streamed from memory, straight into the operands of m16n8k16 MMAs.
 //
 // Measured (device time in a CUDA graph, weights from memory): 3584 -> 4608, one row
-// 5.5 us, 8 rows 5.8, 16 7.5, 24 8.4, 32 9.4; 4096 -> 14336, one row 14.7 us (2.1 TB/s).  Small
+// 5.5 us, 8 rows 5.8, 16 7.5, 24 8.4, 32 9.4; 4096 -> 14336, one row 12.6 us (2.5 TB/s).  Small
 // weights: latency of a launch, a load and a reduction; large ones: the issue of the
 // exact conversions, five instructions on two weights.
 //
@@ -41,12 +41,55 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 16 bytes to shared memory, of which ``bytes`` are read (the rest zeros).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+// Values of x of block b (32 of K) of tokens g, g + 8 ..; zeros past the end of either.
+template <int NT>
+__device__ __forceinline__ void load_x(const LinearArgs& a, int g, int b, uint4 (&x)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int tok = 8 * n + g;
+    const bool there = tok < a.T && 32 * b < a.K;
+    const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)tok * a.x_stride + 32 * b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[n][i] = there ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+// The products of a chunk: w0, w1 of rows g and g + 8.
+template <int NT>
+__device__ __forceinline__ void mma_chunk(float (&acc)[NT][4], const uint4 (&w0)[4], const uint4 (&w1)[4], const uint4 (&x)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mma_bf16(acc[n], w0[i].x, w1[i].x, w0[i].y, w1[i].y, x[n][i].x, x[n][i].y);
+      mma_bf16(acc[n], w0[i].z, w1[i].z, w0[i].w, w1[i].w, x[n][i].z, x[n][i].w);
+    }
+}
+// A warp's sums of a tile to [token][row].
+template <int NT>
+__device__ __forceinline__ void store_part(float* part, int g, int t, const float (&acc)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part[(8 * n + 2 * t + (k & 1)) * 16 + g + 8 * (k >> 1)] = acc[n][k];
 }
 
 // NT: token tiles of 8.  AHEAD: chunks of a warp whose weights are on their way.
@@ -91,34 +134,18 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
   for (int c0 = first; c0 < chunks; c0 += AHEAD * step) {
 #pragma unroll
     for (int p = 0; p < AHEAD; ++p) {
-      const int c = c0 + p * step, b = 4 * c + t;
+      const int c = c0 + p * step;
       if (c >= chunks) break;
       uint4 x[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int tok = 8 * n + g;
-        const bool there = tok < a.T && b < KB;
-        const uint4* src = reinterpret_cast<const uint4*>(a.x + (size_t)tok * a.x_stride + 32 * b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[n][i] = there ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-      }
+      load_x(a, g, 4 * c + t, x);
       uint4 w0[4], w1[4];
       linear_block(wq[p][0], sc[p][0], w0);
       linear_block(wq[p][1], sc[p][1], w1);
       load(p, c + AHEAD * step);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mma_bf16(acc[n], w0[i].x, w1[i].x, w0[i].y, w1[i].y, x[n][i].x, x[n][i].y);
-          mma_bf16(acc[n], w0[i].z, w1[i].z, w0[i].w, w1[i].w, x[n][i].z, x[n][i].w);
-        }
+      mma_chunk(acc, w0, w1, x);
     }
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) part[warp][(8 * n + 2 * t + (k & 1)) * 16 + g + 8 * (k >> 1)] = acc[n][k];
+  store_part(part[warp], g, t, acc);
   __syncthreads();
   for (int e = threadIdx.x; e < COLS * 16; e += 32 * kStreamWarps) {
     float v = 0.f;
@@ -149,6 +176,105 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
     else h = linear_act(a.act, h);
     linear_store(a, n, col, h);
   }
+}
+
+// ------------------------------------------------------------------ many tiles
+//
+// The same for more tiles than two CTAs an SM hold: resident CTAs walk over them, and a
+// warp's next weights are on their way across the end of a tile.  They wait in shared memory,
+// each lane's own (cp.async: no registers, so that three CTAs an SM fit), a tile's chunks of a warp filled
+// up to a multiple of kWalkAhead.  Measured, one row: 512 -> 28672 7.0 us, with a CTA a tile
+// 11.2; 3584 -> 7168 7.3 and 9.2; 4096 -> 14336 12.6 and 14.7; 8192 -> 28672 39.8 and 46.0 (3584 -> 4608,
+// two CTAs an SM hold all tiles, 5.7 and 5.5).  16 rows: 8192 -> 28672 70.7 and 75.2.  What bounds it: 4
+// instructions a weight, two thirds of the issue slots, ALU pipe 60 %; four chunks ahead are slower.
+constexpr int kWalkAhead = 2, kWalkSmem = kStreamWarps * kWalkAhead * 1024;
+template <int NT>
+constexpr int kWalkCtas = NT == 1 ? 3 : 2;
+
+template <int NT>
+__global__ void __launch_bounds__(32 * kStreamWarps, kWalkCtas<NT>) linear_walk_kernel(const LinearArgs a, int tiles) {
+  constexpr int COLS = 8 * NT, AHEAD = kWalkAhead;
+  __shared__ float part[2][kStreamWarps][COLS * 16];
+  extern __shared__ uint4 walk_ring[];
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
+  const int KB = a.K >> 5, chunks = (KB + 3) >> 2;
+  const bool gated = a.act == LINEAR_ACT_SWIGLU;
+  const int per = gated ? 8 : 16;  // columns of the result a tile
+  constexpr int kRound = AHEAD * kStreamWarps;
+  const int end = (chunks + kRound - 1) / kRound * kRound + warp;  // of a warp's chunks warp, warp + 8 ..
+  uint4* ring = walk_ring + warp * (AHEAD * 64) + lane;  // [chunk][row g, g + 8][lane]
+  uint32_t sc[AHEAD][2];
+  // what is loaded next: block t of chunk lc of tile lt, rows g and g + 8 (past the last: another's, not stored)
+  int lt = blockIdx.x, lc = warp;
+  const uint8_t *wp[2], *sp[2];
+  auto point = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = min(gated ? lt * 8 + g : lt * 16 + 8 * h + g, a.cols - 1);
+      const size_t at = (size_t)(gated && h ? col + a.cols : col) * KB + 4 * warp + t;
+      wp[h] = a.w + at * 16;
+      sp[h] = a.ws + at;
+    }
+  };
+  auto load = [&](int p) {
+    const bool there = lt < tiles && 4 * lc + t < KB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      cp_async16(ring + p * 64 + 32 * h, there ? wp[h] : a.w, there ? 16 : 0);
+      sc[p][h] = there ? __ldg(sp[h]) : 127u;
+      wp[h] += 64 * kStreamWarps;
+      sp[h] += 4 * kStreamWarps;
+    }
+    cp_async_commit();
+    lc += kStreamWarps;
+    if (lc == end) {
+      lc = warp;
+      lt += gridDim.x;
+      point();
+    }
+  };
+  point();
+#pragma unroll
+  for (int p = 0; p < AHEAD; ++p) load(p);
+  int buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (int c0 = warp; c0 < end; c0 += kRound) {
+#pragma unroll
+      for (int p = 0; p < AHEAD; ++p) {
+        const int c = c0 + p * kStreamWarps;
+        if (c < chunks) {
+          uint4 x[NT][4];
+          load_x(a, g, 4 * c + t, x);
+          cp_async_wait<AHEAD - 1>();
+          uint4 w0[4], w1[4];
+          linear_block(ring[p * 64], sc[p][0], w0);
+          linear_block(ring[p * 64 + 32], sc[p][1], w1);
+          mma_chunk(acc, w0, w1, x);
+        }
+        load(p);
+      }
+    }
+    store_part(part[buf][warp], g, t, acc);
+    __syncthreads();  // (one a tile: the other buffer is written after the next, when all have read this one)
+    for (int e = threadIdx.x; e < COLS * per; e += 32 * kStreamWarps) {
+      const int n = e / per, r = e % per, col = tile * per + r;
+      if (col >= a.cols || n >= a.T) continue;
+      float h = 0.f, u = 0.f;
+#pragma unroll
+      for (int w = 0; w < kStreamWarps; ++w) {
+        h += part[buf][w][n * 16 + r];
+        if (gated) u += part[buf][w][n * 16 + 8 + r];
+      }
+      h += linear_bias(a, col);
+      if (gated) h = silu(h) * (u + linear_bias(a, a.cols + col));
+      else h = linear_act(a.act, h);
+      linear_store(a, n, col, h);
+    }
+  }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ more than 16 rows
@@ -355,6 +481,8 @@ cudaError_t launch_wide(const LinearArgs& a, cudaStream_t s) {
 template <int NT, int AHEAD>
 cudaError_t launch_stream(const LinearArgs& a, cudaStream_t s) {
   const int per = a.act == LINEAR_ACT_SWIGLU ? 8 : 16, tiles = (a.cols + per - 1) / per;
+  if (tiles > 2 * a.num_sms)
+    return launch_clusters(linear_walk_kernel<NT>, dim3(std::min(tiles, kWalkCtas<NT> * a.num_sms)), kWalkSmem, s, a, tiles);
   return launch_clusters(linear_stream_kernel<NT, AHEAD>, dim3(tiles, stream_splits(a, tiles, a.num_sms)), 0, s, a);
 }
 

@@ -219,6 +219,26 @@ def test_unlike_sizes(m, T, K):
     check(p, call(m, p))
 
 
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("T", [1, 3, 8, 9, 16])
+@pytest.mark.parametrize("K,N", [(32, 4866), (96, 12002), (1056, 7300), (2048, 7298), (3200, 9800), (8192, 5000)])
+def test_tiles_walked(m, T, K, N, act):
+    """More tiles of 16 rows than two an SM: a last round that is not full, tiles past the end, parts of chunks."""
+    both(m, T, K, N, act=act, bias=True, residual=True, f32=T == 3, seed=23)
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_tiles_walked_not_finite(m, T):
+    p = problem(T, 1056, 6000, seed=24)
+    p["s"][5999, 32] = 255  # the last block of the last row is NaN
+    p["x"][T - 1, 1055] = float("inf")  # 0 in row 17, positive in row 18
+    p["w"][17, -1] = 0
+    p["w"][18, -1] = 0x20
+    got = call(m, p).float().cpu().numpy()
+    assert np.isnan(got[:, 5999]).all() and np.isnan(got[T - 1, 17]) and got[T - 1, 18] == np.inf
+    assert np.isfinite(got[: T - 1, :5999]).all()
+
+
 @pytest.mark.parametrize("T", [1, 7, 16])
 @pytest.mark.parametrize("K,N", [(128, 20000), (4096, 5500), (32768, 33), (8192, 700), (32, 16)])
 def test_many_tiles_and_deep_rows(m, T, K, N):
