@@ -107,7 +107,7 @@ int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, co
 size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks) {
   if (!shared_valid(c, a, shared_blocks)) return 0;
   const KvView view = view_of(c);
-  return kv_shared_workspace(view, a, kv_shared_splits(view, a, shared_blocks));
+  return kv_shared_workspace(view, a, kv_shared_plan(view, a, shared_blocks).splits);
 }
 
 int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks, const void* q,
@@ -126,7 +126,8 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
     return MOE_ERR_ALIGN;
   const KvView view = view_of(c);
   // fewer rows may be cut into more slices: a workspace for more rows does, with fewer of them
-  int splits = kv_shared_splits(view, a, shared_blocks);
+  const KvSharedPlan plan = kv_shared_plan(view, a, shared_blocks);
+  int splits = plan.splits;
   while (splits > 1 && kv_shared_workspace(view, a, splits) > workspace_bytes) --splits;
   const size_t need = kv_shared_workspace(view, a, splits);
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
@@ -141,6 +142,7 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
   if (rc != MOE_OK) return rc;
   KvAttnArgs g = attn_args(view, a, q, block_table, seq_lens, query_start, out, lse, workspace, sms, wait);
   g.sh.splits = splits;
+  g.sh.row_limit = plan.stream ? INT32_MAX : 0;
   g.sh.blocks = shared_blocks;
   g.sh.table = shared_table;
   g.sh.len = shared_len;

@@ -104,7 +104,7 @@ constexpr int kSliceKeys = 128;  // slices start at multiples of this
 struct KvShared {
   int splits = 0;  // 0: no prefix, one result a row
   int blocks = 0;  // entries of table
-  int row_limit = 0;  // slices with more rows than this go to the tensor-core kernel
+  int row_limit = 0;  // slices with more rows than this go to the tensor-core kernel: all, or none
   const int32_t *table = nullptr, *len = nullptr;
   float* o = nullptr;    // [part][N * Hq][D]: weighted sums of values, in units of 2^(E - 127)
   float4* ml = nullptr;  // [part][N * Hq]: reference (units of 4 log2), sum of weights, E, unused
@@ -230,7 +230,11 @@ cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, c
 int kv_stream_rows(const KvAttnArgs& a);
 
 // Attention with a shared prefix: how it is cut, its workspace, the call.
-int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
+struct KvSharedPlan {
+  int splits;   // slices of the prefix
+  bool stream;  // they are streamed, else on the tensor cores
+};
+KvSharedPlan kv_shared_plan(const KvView& c, const kv_mxfp4_attn_t* a, int blocks);
 size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int splits);
 cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s);
 

@@ -6,8 +6,8 @@
 //   out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
 // The prefix is read once for all rows of the batch: it is cut into slices, each a
 // request of its own whose rows are all query rows of the call, which the two
-// attention kernels take as they take any other request (few rows: streamed;
-// many: tensor cores, one CTA per 256 rows, kv head and slice).  The requests' own
+// attention kernels take as they take any other request (few rows or keys:
+// streamed; many: tensor cores, one CTA per 256 rows, kv head and slice).  The requests' own
 // keys are parts too.  kv_join_kernel joins a row's parts.
 //
 // Measured, 28 / 4 heads of 128: 64 requests behind 32,768 tokens, up to 2048 own, 76 us: prefix 40
@@ -25,11 +25,6 @@ namespace {
 constexpr size_t kStatusBytes = 256;
 // The plan is made for a GB300's SMs, so that a workspace's size depends on the sizes alone.
 constexpr int kPlanSms = 152;
-// Rows (tokens x query heads per kv head) up to which the prefix is streamed (28 rows, 4 kv
-// heads, 100,003 keys: 54 us streamed, 86 on the tensor cores, where a tile of keys takes
-// 2.6 us however few its rows).
-constexpr int kSharedStreamRows = 32;
-
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // One warp a row (token x query head).  Latency-bound: the row's sums are all on their
@@ -127,12 +122,16 @@ SharedLayout shared_layout(int D, int R, int N, int Hq, int splits) {
 
 }  // namespace
 
-// Slices of a prefix of up to ``blocks`` pages: as many as shorten the tensor-core
-// kernel's waves (a CTA takes about 16 ns a key and some 5 us besides), against what
-// a slice's sums cost to write and read (about 4 bytes a picosecond).
-int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
+// How a prefix of up to ``blocks`` pages is read.  Streamed, whole, while that is thought to take
+// less than the tensor cores: a row tile of 16 and kv head takes an SM 6.5 ns a key, and some 4 us for
+// its pieces, which warps and CTAs share; all SMs work on it.  On the tensor cores, cut into slices: as many as
+// shorten that kernel's waves (a CTA of 256 rows takes about 16 ns a key and some 5 us besides),
+// against what a slice's sums cost to write and read (about 4 bytes a picosecond); 9 us for
+// the launch and its marks.  Measured, streamed and on the tensor cores: 64 requests, 4 x 7 heads of
+// 128: 16 keys 16 and 35 us, 2400 32 and 37, 5000 46 and 39; 12 requests: 10,000 keys 28 and 35;
+// 256 requests: 300 keys 44 and 39; 28 rows, 100,003 keys 54 and 86.
+KvSharedPlan kv_shared_plan(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
   const long long rows = (long long)a->N * (a->Hq / c.heads);
-  if (rows <= kSharedStreamRows) return 1;
   const long long tiles = (rows + 255) / 256 * c.heads, keys = (long long)blocks << c.page_shift;
   int best = 1;
   double least = 0;
@@ -145,7 +144,10 @@ int kv_shared_splits(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
       best = s;
     }
   }
-  return best;
+  const double items = (double)((rows + 15) / 16 * c.heads);
+  const double streamed = items * (6.5e-9 * keys + 4e-6 * std::min(keys, 256LL) / 256) / kPlanSms + 3e-6;
+  if (streamed <= least + 9e-6) return {1, true};
+  return {best, false};
 }
 
 size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int splits) {
@@ -155,7 +157,6 @@ size_t kv_shared_workspace(const KvView& c, const kv_mxfp4_attn_t* a, int splits
 cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s) {
   const int G = a.Hq / a.cache.heads;
   const SharedLayout L = shared_layout(a.cache.D, a.R, a.N, a.Hq, a.sh.splits);
-  a.sh.row_limit = kSharedStreamRows;
   a.sh.ml = reinterpret_cast<float4*>(a.workspace + L.ml);
   a.sh.o = reinterpret_cast<float*>(a.workspace + L.o);
   uint8_t* ws = a.workspace + kStatusBytes;
@@ -163,12 +164,18 @@ cudaError_t launch_kv_shared(KvAttnArgs a, cudaStream_t s) {
   const int limit = kv_stream_rows(a);
   int32_t* odd = nullptr;
   cudaError_t e;
-  if (all > kSharedStreamRows || own > limit) {
+  const bool stream = a.sh.row_limit > 0;
+  if (!stream || own > limit) {
     odd = reinterpret_cast<int32_t*>(a.workspace + L.odd);
     if ((e = launch_kv_prompt(a, limit, odd, s)) != cudaSuccess) return e;
   }
-  // (row tiles as without a prefix; a streamed prefix has most of the keys)
-  const long long streamed = all <= kSharedStreamRows ? all : own <= limit ? own : G;
+  // row tiles of 8 where the streamed rows fit (as without a prefix); a streamed prefix with more rows
+  // takes tiles of 16, unless the requests' own keys, thought to be half of their tables', weigh more: a
+  // tile of 8 takes 4.6 ns a key, one of 16 6.5
+  long long streamed = own <= limit ? own : G;
+  if (stream && all > 8) {
+    if (0.7 * a.max_blocks / 2 * a.R < (double)((all + 15) / 16) * a.sh.blocks) streamed = all;
+  }
   if ((e = launch_kv_stream(a, limit, odd, streamed <= 8 ? 1 : 2, ws, s)) != cudaSuccess) return e;
   const dim3 grid((unsigned)(((long long)a.N * a.Hq + 7) / 8));
   // (8 parts at a time leave room for twice the rows on an SM: 256 requests of 6 parts 86 us

@@ -8,6 +8,7 @@ workspace are right."""
 import ctypes
 import time
 
+import numpy as np
 import pytest
 import torch
 
@@ -70,9 +71,12 @@ def test_linear_few_rows(m, T, K, N, act):  # noqa: F811
     check_linear(m, T, K, N, act)
 
 
-@pytest.mark.parametrize("P,R,H,G,D", [(700, 40, 2, 4, 64), (500, 3, 2, 4, 128), (300, 60, 4, 7, 128)])
-def test_shared(m, P, R, H, G, D):  # noqa: F811
-    p = shared.problem(P, [30] * R, [1] * R, H, G, D, 32, seed=2)
+# (``tail``: entries of the shared table past the prefix; with many the prefix goes to the tensor cores)
+@pytest.mark.parametrize("P,R,H,G,D,tail", [(700, 40, 2, 4, 64, 0), (500, 3, 2, 4, 128, 0), (300, 60, 4, 7, 128, 0),
+                                            (700, 80, 2, 4, 64, 4000), (300, 60, 4, 7, 128, 4000)])
+def test_shared(m, P, R, H, G, D, tail):  # noqa: F811
+    p = shared.problem(P, [30] * R, [1] * R, H, G, D, 32, seed=2, extra=1)
+    p["shared"] = np.concatenate([p["shared"], np.zeros(tail, np.int32)])
     c = m.KvCacheMxfp4(p["pages"], 32, H, D, data=torch.from_numpy(p["data"]).cuda())
     i32, q = shared.i32, p["q"].cuda()
     args = (i32(p["shared"]), i32([P]), i32(p["table"]), i32(p["lens"]), i32(p["start"]), 1)

@@ -50,10 +50,13 @@ def test_streams_at_once(m):  # noqa: F811
         assert torch.equal(out, alone[0]) and torch.equal(lse, alone[1])
 
 
-def test_two_graphs_share_a_workspace(m):  # noqa: F811
-    problems = [shared.problem(P, [20] * R, [1] * R, 2, 7, 128, 64, seed=R) for P, R in ((1500, 30), (300, 12))]
-    ws = None
-    runs = []
+@pytest.mark.parametrize("sizes", [((1500, 30), (300, 12)), ((1500, 60), (300, 50)), ((700, 90), (1500, 20))])
+@pytest.mark.parametrize("tail", [0, 2000])  # (entries of the shared table past the prefix)
+def test_two_graphs_share_a_workspace(m, sizes, tail):  # noqa: F811
+    problems = [shared.problem(P, [20] * R, [1] * R, 2, 7, 128, 64, seed=R) for P, R in sizes]
+    for p in problems:
+        p["shared"] = np.concatenate([p["shared"], np.zeros(tail, np.int32)])
+    ws, runs = None, []
     for p in problems:
         c = m.KvCacheMxfp4(p["pages"], 64, 2, 128, data=torch.from_numpy(p["data"]).cuda())
         q, R = p["q"].cuda(), len(p["lens"])
@@ -71,12 +74,12 @@ def test_two_graphs_share_a_workspace(m):  # noqa: F811
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             call()
-        runs.append((g, p, out, lse))
+        runs.append((g, p, out, lse, (q, c, args)))  # (the graph's inputs live as long as it does)
     for _ in range(5):
-        for g, _, out, lse in runs:
+        for g, _, out, lse, _ in runs:
             out.zero_()
             g.replay()
-        for _, p, out, lse in runs:
+        for _, p, out, lse, _ in runs:
             shared.check(p, out, lse)
     assert m.attention_read_status(ws) == 0
 

@@ -14,6 +14,11 @@ On top comes what weights below 2^-126 of the largest add, which float32 exponen
 at most 2^-126 (keys) max |v|, max |v| being 6 2^(s - 127) for the largest value scale s.
 (Found by keys that hold a dimension's only value 2^138 below the heaviest key, with
 values of 2^16: 2.6e-37, where the float32 weight is 0.)
+Where a part has more than 256 keys, the tensor-core kernel holds its weights p 2^9 in f16, 11 bits down to
+p = 2^-23 of the part's reference and multiples of 2^-33 below, off by at most 2^-34: as in the tests
+of prompts without a prefix, 2^-34 of sum |v|, at most 2^-34 (keys) max |v|, comes on top there.  (The reference is
+a score of the part, so that its sum of weights is at least 1, and a part enters the result with a weight of at
+most 1.  Found by a dimension whose heaviest key has the value 0: 1.8e-8, 2.1e-10 off.)
 Results near or below the smallest normal number are held to 1e-37, eight times its size (as there).
 Rows outside every request are not written.
 """
@@ -75,7 +80,7 @@ def problem(P, lens, qlens, H, G, D, page, seed=0, bands=((120, 127), (120, 127)
     start = np.concatenate([[0], np.cumsum(qlens)])
     q = torch.from_numpy(g.standard_normal((start[-1] + gaps, H * G, D))).to(torch.bfloat16)
     return dict(q=q, data=data, shared=shared, P=P, table=table, lens=np.array(lens), start=start, H=H, G=G, D=D, page=page, pages=pages,
-                lost=2.0 ** -126 * (P + max(lens)) * 6 * 2.0 ** (bands[1][1] - 127))
+                lost=(2.0 ** -126 + (2.0 ** -34 if max(P, *lens) > 256 else 0)) * (P + max(lens)) * 6 * 2.0 ** (bands[1][1] - 127))
 
 
 def run(m, p, scale=0.2, causal=True, q=None, stream=None, max_q=None):
@@ -164,15 +169,15 @@ def test_workspace_of_a_larger_batch(m):
     """Fewer rows can be cut into more slices: a workspace for more of them has to do."""
     H, G, D = 4, 7, 128
     c = m.KvCacheMxfp4(4, 16, H, D)
-    size = [m.attention_shared_workspace_bytes(c, R, R, H * G, 1, 1, 128) for R in range(1, 80)]
+    size = [m.attention_shared_workspace_bytes(c, R, R, H * G, 1, 1, 512) for R in range(1, 80)]
     R = next(i for i, (a, b) in enumerate(zip(size, size[1:]), 1) if a > b)
-    p = problem(128 * 16 - 3, [10] * R, [1] * R, H, G, D, 16, seed=3, extra=0)
-    assert len(p["shared"]) == 128 and p["table"].shape[1] == 1
+    p = problem(512 * 16 - 3, [10] * R, [1] * R, H, G, D, 16, seed=3, extra=0)
+    assert len(p["shared"]) == 512 and p["table"].shape[1] == 1
     c = m.KvCacheMxfp4(p["pages"], 16, H, D, data=torch.from_numpy(p["data"]).cuda())
     q = p["q"].cuda()
     out, lse = torch.empty_like(q), torch.empty(R, H * G, device="cuda")
     args = (q, c, i32(p["shared"]), i32([p["P"]]), i32(p["table"]), i32(p["lens"]), i32(p["start"]), 1)
-    ws = torch.zeros(m.attention_shared_workspace_bytes(c, R + 1, R + 1, H * G, 1, 1, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(m.attention_shared_workspace_bytes(c, R + 1, R + 1, H * G, 1, 1, 512), dtype=torch.uint8, device="cuda")
     m.attention_kv_mxfp4_shared(*args, scale=0.2, out=out, lse=lse, workspace=ws)
     check(p, out, lse)
     with pytest.raises(m.MoeError, match="WORKSPACE"):
