@@ -76,10 +76,31 @@ __device__ __forceinline__ float linear_bias(const LinearArgs& a, int row) {
   return a.bias ? __uint_as_float((uint32_t)a.bias[row] << 16) : 0.f;
 }
 
+// h (1 + erf(h / sqrt 2)) / 2 = max(h, 0) - |h| q with the normal tail q = e^(-h^2 / 2) t P(t), t = 1 / (1 + 0.34 |h|):
+// P, of degree 8, is erfcx(|h| / sqrt 2) / (2 t) to 3.4e-8 of it for |h| <= 14.5, fitted by reweighted least squares at
+// Chebyshev nodes.  2e-7 |h| in all, 3.2e-8 of normal values' root mean square, as with the library's
+// normcdff, with which 827 x 160 -> 564 takes 19.3 us instead of 12.2, 1003 x 2080 -> 1111 22.7 instead of 20.6.
+__device__ __forceinline__ float gelu(float h) {
+  const float a = fabsf(h), t = __fdividef(1.f, fmaf(0.34f, a, 1.f));
+  float p = -0.02587643451988697f;
+  p = fmaf(p, t, 0.13835705816745758f);
+  p = fmaf(p, t, -0.27087101340293884f);
+  p = fmaf(p, t, 0.19971758127212524f);
+  p = fmaf(p, t, -0.04310628026723862f);
+  p = fmaf(p, t, 0.11471360176801682f);
+  p = fmaf(p, t, 0.11535170674324036f);
+  p = fmaf(p, t, 0.13609223067760468f);
+  p = fmaf(p, t, 0.135621577501297f);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * a * -0.72134752044448170f));  // (log2(e) / 2)
+  const float q = t * p * e;
+  return h > 8.f ? h : fmaf(-a, q, fmaxf(h, 0.f));  // (h > 8: |h| q is below half a step; infinity)
+}
+
 // The activation of one value (not the gated one).
 __device__ __forceinline__ float linear_act(int act, float h) {
   if (act == LINEAR_ACT_SILU) return silu(h);
-  if (act == LINEAR_ACT_GELU) return h * normcdff(h);
+  if (act == LINEAR_ACT_GELU) return gelu(h);
   return h;
 }
 

@@ -246,6 +246,27 @@ def test_many_tiles_and_deep_rows(m, T, K, N):
     check(p, call(m, p))
 
 
+def test_gelu_of_every_size(m):
+    """h itself by a weight of ones on the diagonal, against h Phi(h).  The kernel's max(h, 0) - |h| q, q = Phi(-|h|) as
+    t P(t) e^(-h^2/2): the fit of P 2^-24.8 of it, t off by 2^-22 at a sensitivity of at most 2.4, eight steps of P 2^-22.4,
+    the exponential 2^-22 and two roundings of its argument, h^2 2^-24, two products 2^-23: below (2^-19 + h^2 2^-24) |h| q."""
+    special = pytest.importorskip("scipy.special")
+    h = torch.cat([torch.linspace(-14, 14, 4000), torch.randn(4000), torch.randn(4000) * 0.01, torch.tensor(
+        [0.0, -0.0, 8.0, -8.0, 8.0625, 30.0, -30.0, 1e30, -1e30, float("inf"), float("nan")] + [0.0] * 21)]).bfloat16()
+    h = h[: h.numel() // 32 * 32].reshape(-1, 32)
+    w = np.zeros((32, 16), np.uint8)
+    for k in range(32):
+        w[k, k // 2] = 0x20 if k % 2 else 0x02
+    s = torch.full((32, 1), 127, dtype=torch.uint8, device="cuda")
+    h[~torch.isfinite(h)] = 0  # (an infinity would meet the weight's zeros)
+    for T in (1, 9, 20, h.shape[0]):
+        x = h[-T:].cuda()
+        out = m.linear_a16w4_mxfp4(x, torch.from_numpy(w).cuda(), s, act="gelu", out_dtype=torch.float32).double().cpu().numpy()
+        v = h[-T:].double().numpy()
+        want, q = v * special.ndtr(v), special.ndtr(-np.abs(v))
+        assert (np.abs(out - want) <= (2.0 ** -19 + v * v * 2.0 ** -24) * np.abs(v) * q + 2.0 ** -24 * np.abs(want) + 1e-37).all()
+
+
 def test_huge_activations(m):
     # products of 2^120, sums within float32
     for T in (1, 40, 300):
