@@ -55,6 +55,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kGroups = 4;              // of converter warps (2: 336 us instead of 327, before the epilogue had 8 warps)
+static_assert(kGroups == 4, "a group takes every fourth step of a quad of four");
 constexpr int kEpiWarps = 8, kConvWarp = kEpiWarps, kConvWarps = 4 * kGroups;
 constexpr int kMmaWarp = kConvWarp + kConvWarps, kTmaWarp = kMmaWarp + 1, kRawWarp = kTmaWarp + 1, kScaleWarp = kRawWarp + 1;
 constexpr int kTcThreads = 32 * (kScaleWarp + 1);
@@ -350,19 +351,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     for (int tile = cluster; tile < p.tiles && ok; tile += clusters) {
       for (int quad = 0; quad < KQ && ok; ++quad, ++gq) {
         const int r = gq % kRawStages, steps = min(kQuad, KS - kQuad * quad);
-        const int gs = gs0 + group, s = gs % S;
-        const bool mine = group < steps;
-        // (probes now, waits where they failed: the round trips pass beside the conversion)
+        // (a group takes every fourth step whatever the quads' lengths: the stage of a step of its own has
+        // then been left by the step 2 S before, so that the barriers' parities are those of the last two uses.
+        // With step ``group`` of each quad, 7 steps lie across the end of a tile whose last quad has 3.)
+        const int at = (group - gs0) & (kGroups - 1), gs = gs0 + at, s = gs % S;
+        const bool mine = at < steps;
+        // (probes now, waits where they failed: the round trips pass beside the conversion.  The x tile is
+        // looked for in a free stage only: before, the stage's last x may still be on its way, later than
+        // this group's own last one, and the barrier two phases back, where the parity is the same)
         const bool free_now = !mine || gs < S || test_here(&sh.empty[s], ((gs / S) - 1) & 1);
-        const bool x_there = !mine || (warp & 3) != 0 || test_here(&sh.b_full[s], (gs / S) & 1);
+        const bool x_there = !mine || (warp & 3) != 0 || (free_now && test_here(&sh.b_full[s], (gs / S) & 1));
         ok = mbar_wait_warp(&sh.raw_full[r], (gq / kRawStages) & 1, a.status, limit, &sh.abort_flag);
         uint4 w[2][4];
         if (mine) {
           const uint8_t* raw = smem + kRawOff + r * kRawBytes + i * 128;
-          const uint32_t sc = *reinterpret_cast<const uint16_t*>(smem + kScaleOff + r * kScaleBytes + i * 8 + 2 * group);
+          const uint32_t sc = *reinterpret_cast<const uint16_t*>(smem + kScaleOff + r * kScaleBytes + i * 8 + 2 * at);
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            linear_block(*reinterpret_cast<const uint4*>(raw + (((2 * group + b) ^ (i & 7)) << 4)), (sc >> (8 * b)) & 255u, w[b]);
+            linear_block(*reinterpret_cast<const uint4*>(raw + (((2 * at + b) ^ (i & 7)) << 4)), (sc >> (8 * b)) & 255u, w[b]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.raw_empty[r]);

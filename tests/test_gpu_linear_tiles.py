@@ -131,3 +131,28 @@ def test_captured(m, T):  # noqa: F811
     graph.replay()
     q.update(w=p["w"], s=p["s"], b=p["b"])
     check(q, out)
+
+
+@pytest.mark.parametrize("act", [None, "gelu", "swiglu"])
+@pytest.mark.parametrize("K", [64, 128, 192, 320, 352, 384, 416, 448, 480, 640, 1376, 1408, 1472, 1504, 2912, 4000])
+def test_several_tiles_a_pair(m, K, act):  # noqa: F811
+    """Steps that do not divide by four, by the stages or by the packed weights' stages, tile after tile."""
+    both(m, 2500, K, 2600, act=act, bias=True, residual=True, seed=K)
+
+
+@pytest.mark.parametrize("T,K,N", [(1208, 6080, 4096), (3020, 448, 1837), (4000, 1472, 2500), (300, 6080, 8192), (2100, 3584, 1500), (1208, 8192, 1024)])
+def test_many_calls_agree(m, T, K, N):  # noqa: F811
+    """Deep rows whose tiles of x come out of order: every call's result is the first's, and no wait runs out."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    xs = [torch.randn(T, K, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, generator=g, device="cuda")
+    s = torch.randint(115, 122, (N, K // 32), dtype=torch.uint8, generator=g, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    first = [m.linear_a16w4_mxfp4(x, w, s, workspace=ws) for x in xs]
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(240):
+        if i % 8 == 0:
+            flush.fill_(i)  # x comes from memory
+        wrong += (m.linear_a16w4_mxfp4(xs[i % 3], w, s, workspace=ws) != first[i % 3]).sum()
+    assert m.linear_read_status(ws) == 0 and wrong.item() == 0
