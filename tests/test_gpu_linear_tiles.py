@@ -1,4 +1,4 @@
-"""The linear layer on an MXFP4 weight beyond one wave of 32 x 32 tiles, where tcgen05 MMAs of CTA pairs do it: rows and
+"""The linear layer on an MXFP4 weight beyond two waves of 32 x 32 tiles, where tcgen05 MMAs of CTA pairs do it: rows and
 columns around their tiles, depths, epilogues, addresses, values of unlike size.  The same float64 oracle and derived
 bound as for smaller ones."""
 
@@ -13,9 +13,9 @@ pytestmark = pytest.mark.gpu
 
 
 def rows_for(T, more=0):
-    """Weight rows of the first size past one wave, and ``more``."""
+    """Weight rows of the first size past two waves, and ``more``."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    return 32 * (sms // -(-T // 32)) + 2 + more
+    return 32 * (2 * sms // -(-T // 32)) + 2 + more
 
 
 @pytest.mark.parametrize("T", [33, 63, 64, 65, 100, 127, 128, 129, 200, 255, 256, 257, 300, 513, 1100])
