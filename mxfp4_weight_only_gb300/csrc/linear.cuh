@@ -23,7 +23,7 @@ struct LinearArgs {
   WaitSettings wait;
 };
 
-// Few rows: the weight is streamed once (linear.cu).
+// Few rows, or few tiles: MMAs from registers (linear.cu).
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s);
 
 // Many rows: tensor cores (linear_tc.cu).
