@@ -112,18 +112,18 @@ __device__ __forceinline__ void linear_store(const LinearArgs& a, int token, int
   else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16_bits(v);
 }
 
-// Residual and store of N activated values of column ``col``, of tokens tok, tok + STEP, ..
+// Residuals of column ``col``, of tokens tok, tok + STEP, ..: zeros past the last token.
 template <int N, int STEP>
-__device__ __forceinline__ void linear_store_column(const LinearArgs& a, int tok, int col, float (&h)[N]) {
+__device__ __forceinline__ void linear_load_column(const LinearArgs& a, int tok, int col, uint16_t (&r)[N]) {
   const int left = (a.T - tok + STEP - 1) / STEP;  // tokens that exist
-  if (a.res) {
-    const uint16_t* src = a.res + (size_t)tok * a.res_stride + col;
-    uint16_t r[N];
+  const uint16_t* src = a.res + (size_t)tok * a.res_stride + col;
 #pragma unroll
-    for (int k = 0; k < N; ++k) r[k] = k < left ? src[(size_t)(k * STEP) * a.res_stride] : (uint16_t)0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) h[k] += __uint_as_float((uint32_t)r[k] << 16);
-  }
+  for (int k = 0; k < N; ++k) r[k] = k < left ? src[(size_t)(k * STEP) * a.res_stride] : (uint16_t)0;
+}
+// Store of N values of column ``col``, of tokens tok, tok + STEP, ..
+template <int N, int STEP>
+__device__ __forceinline__ void linear_store_column(const LinearArgs& a, int tok, int col, const float (&h)[N]) {
+  const int left = (a.T - tok + STEP - 1) / STEP;
   const size_t at = (size_t)tok * a.out_stride + col;
   if (a.f32) {
     float* dst = reinterpret_cast<float*>(a.out) + at;
