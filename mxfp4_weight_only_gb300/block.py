@@ -62,14 +62,16 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
     but a missing ``out``, and to learn of waits that ran out (``linear_read_status``)."""
     if not isinstance(x, _T) or not isinstance(w, _T) or not isinstance(w_scale, _T):
         raise TypeError("x, w and w_scale must be torch.Tensors")
-    if x.dim() != 2 or w.dim() != 2:
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 2:
         raise ValueError("x must be [T, K] and w [N, K / 2]")
-    if not x.is_cuda:
+    i = x.get_device()
+    if i < 0:
         raise ValueError("x must be a CUDA tensor")
     code = _ACTS.get(act)
     if code is None:
         raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
-    (T, K), N, dev = x.shape, w.shape[0], x.device
+    (T, K), N = xs, ws[0]
     cols = N
     if code == 3:
         if N % 2:
@@ -78,34 +80,36 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
     # (conditions written out: a call of a few microseconds feels a function a tensor)
     xs = x.stride()
     if x.dtype is not _bf16 or (K > 1 and xs[1] != 1):
-        _matrix(x, "x", _BF16, T, K, dev)
+        _matrix(x, "x", _BF16, T, K, x.device)
     xs = xs[0] if T > 1 else -(-K // 8) * 8
-    if w.dtype is not _u8 or w.shape[1] != K // 2 or not w.is_contiguous() or w.device != dev:
-        _need(w, "w", _u8, (N, K // 2), dev)
-    if w_scale.dtype is not _u8 or w_scale.shape != (N, K // 32) or not w_scale.is_contiguous() or w_scale.device != dev:
-        _need(w_scale, "w_scale", _u8, (N, K // 32), dev)
+    if w.dtype is not _u8 or ws[1] != K // 2 or not w.is_contiguous() or w.get_device() != i:
+        _need(w, "w", _u8, (N, K // 2), x.device)
+    if w_scale.dtype is not _u8 or w_scale.shape != (N, K // 32) or not w_scale.is_contiguous() or w_scale.get_device() != i:
+        _need(w_scale, "w_scale", _u8, (N, K // 32), x.device)
     if bias is not None:
-        if not isinstance(bias, _T) or bias.dtype is not _bf16 or bias.shape != (N,) or not bias.is_contiguous() or bias.device != dev:
-            _need(bias, "bias", _bf16, (N,), dev)
+        if not isinstance(bias, _T) or bias.dtype is not _bf16 or bias.shape != (N,) or not bias.is_contiguous() or bias.get_device() != i:
+            _need(bias, "bias", _bf16, (N,), x.device)
         bias = bias.data_ptr()
     rs = cols
     if residual is not None:
-        rs = _matrix(residual, "residual", _BF16, T, cols, dev)
+        rs = _matrix(residual, "residual", _BF16, T, cols, x.device)
         residual = residual.data_ptr()
     if out is None:
         if out_dtype not in _OUT:
             raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
-        out = _empty((T, cols), out_dtype, dev, stream)
+        out = _empty((T, cols), out_dtype, x.device, stream)
+        os = cols
+    elif isinstance(out, _T) and out.dtype is _bf16 and out.shape == (T, cols) and out.is_contiguous() and out.get_device() == i:
         os = cols
     else:
-        os = _matrix(out, "out", _OUT, T, cols, dev)
+        os = _matrix(out, "out", _OUT, T, cols, x.device)
     lib = _native.load()
     d = LinearStruct(T, K, N, code, 1 if out.dtype is torch.float32 else 0, xs, rs, os)
     ref = ctypes.byref(d)
     if workspace is None:
-        workspace = _empty(max(256, lib.linear_mxfp4_workspace_bytes(ref)), torch.uint8, dev, stream)
-    elif workspace.dtype is not _u8 or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        workspace = _empty(max(256, lib.linear_mxfp4_workspace_bytes(ref)), torch.uint8, x.device, stream)
+    elif workspace.dtype is not _u8 or workspace.get_device() != i or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
     rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias, residual, out.data_ptr(),
                                 workspace.data_ptr(), workspace.numel(), _stream(stream, x))
     if rc:
