@@ -110,6 +110,17 @@ struct KvShared {
   float4* ml = nullptr;  // [part][N * Hq]: reference (units of 4 log2), sum of weights, E, unused
 };
 
+// Keys of slice ``i`` of a prefix of P: the first and how many.
+struct KvSlice {
+  int base, n;
+};
+__host__ __device__ inline KvSlice kv_slice(int P, int splits, int i) {
+  // (64 bits: near the top of the range a slice, rounded up, passes the largest int)
+  const long long unit = (long long)splits * kSliceKeys, slice = (P + unit - 1) / unit * kSliceKeys;
+  const long long base = slice * i < P ? slice * i : P;
+  return {(int)base, (int)(P - base < slice ? P - base : slice)};
+}
+
 struct KvAttnArgs {
   KvView cache;
   int R, N, Hq, max_blocks, max_q_len;
@@ -138,15 +149,13 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   q.part = 0;
   q.causal = a.causal;
   if (SHARED && r >= a.R) {
-    const int P = kv_prefix(a);
-    const int slice = (int)(((long long)P + (long long)a.sh.splits * kSliceKeys - 1) / ((long long)a.sh.splits * kSliceKeys)) * kSliceKeys;
-    const long long base = (long long)(r - a.R) * slice;
-    q.base = (int)min(base, (long long)P);
+    const KvSlice slice = kv_slice(kv_prefix(a), a.sh.splits, r - a.R);
+    q.base = slice.base;
     q.part = 1 + r - a.R;
     q.causal = 0;
     q.qb = 0;
     q.ql = min(max(a.query_start[a.R], 0), a.N);
-    q.n = min(P - q.base, slice);
+    q.n = slice.n;
     q.first = q.n;
     return q;
   }
