@@ -224,6 +224,14 @@ __device__ __forceinline__ int kv_first_key(int pos, int window) {
   return window && pos >= window ? pos - window + 1 : 0;
 }
 
+// The tensor-core kernel's tiles of kKvTile keys (no sum leaves an int, whatever the keys): those that keys lo .. hi - 1 lie in,
+// and whether all keys of the one from j0 on are among them.
+constexpr int kKvTile = 128;
+__host__ __device__ inline int kv_tiles(int lo, int hi) {
+  return hi > lo ? hi / kKvTile + (hi % kKvTile != 0) - lo / kKvTile : 0;
+}
+__host__ __device__ inline bool kv_whole_tile(int lo, int hi, int j0) { return lo <= j0 && hi - kKvTile >= j0; }
+
 // Streaming kernels: requests of at most ``row_limit`` rows (query rows x heads
 // per kv head) or marked in ``odd`` (may be null); row tiles of 8 * tiles rows
 // (tiles 1 or 2).

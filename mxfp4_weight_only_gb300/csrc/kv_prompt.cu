@@ -44,7 +44,7 @@ constexpr int kPromptThreads = 32 * (kMmaWarp + 4);  // the last two warps only 
 // softmax groups x 128 x 160 + 2 converter groups x 128 x 56 + 128 x 40 = 60,416.
 constexpr int kLaunchRegs = 96, kSoftRegs = 160, kConvRegs = 56, kMmaRegs = 40;
 static_assert(128 * (2 * kSoftRegs + 2 * kConvRegs + kMmaRegs) <= kPromptThreads * kLaunchRegs, "register split");
-constexpr int kKeys = 128;         // keys of a tile
+constexpr int kKeys = kKvTile;     // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 // Weights are held in f16 times 2^kWeightExp; one may reach 2^kSlack before its
 // row's reference moves (at most 2^15 in f16), which rescales O.
@@ -302,7 +302,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
   const int first_pos = rq.first + row0 / p.G, last_pos = rq.first + (row0 + rows - 1) / p.G;
   const int key_hi = rq.causal ? min(n, last_pos + 1) : n;
   const int key_lo = kv_first_key(first_pos, a.window);
-  const int t0 = key_lo / kKeys, nt = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - t0 : 0;
+  const int t0 = key_lo / kKeys, nt = kv_tiles(key_lo, key_hi);
   const int nq = rows > 128 ? 2 : 1;
   const int32_t* table = SHARED && r >= a.R ? a.sh.table : a.table + (size_t)r * a.max_blocks;
 
@@ -389,7 +389,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         }
         tc_after();
         // every row of the warp sees every key of the tile?
-        const bool full = __all_sync(0xffffffffu, (lo <= j0 && hi >= j0 + kKeys) || !real) && have == 0xFFu;
+        const bool full = __all_sync(0xffffffffu, kv_whole_tile(lo, hi, j0) || !real) && have == 0xFFu;
         if (!full) {  // hidden keys: -inf, put back where the score was
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {

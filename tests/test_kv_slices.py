@@ -1,5 +1,6 @@
-"""How a shared prefix is cut into slices (kv_slice of csrc/kv_internal.h, compiled for the host): they cover its keys once, in
-order, each but the first beginning at a multiple of 128, up to the longest prefix that a call takes."""
+"""How the keys of a long request are cut (functions of csrc/kv_internal.h, compiled for the host), up to the longest that a call
+takes.  Slices of a shared prefix cover its keys once, in order, each but the first beginning at a multiple of 128; the
+tensor-core kernel's tiles are those that hold a key, and whole where every key of them is seen."""
 
 import ctypes
 import os
@@ -16,6 +17,8 @@ extern "C" void slice(int P, int splits, int i, int* base, int* n) {
   *base = s.base;
   *n = s.n;
 }
+extern "C" int tiles(int lo, int hi) { return moe::kv_tiles(lo, hi); }
+extern "C" int whole(int lo, int hi, int j0) { return moe::kv_whole_tile(lo, hi, j0); }
 extern "C" int max_splits() { return moe::kMaxSplits; }
 extern "C" int slice_keys() { return moe::kSliceKeys; }
 """
@@ -51,3 +54,13 @@ def test_slices_cover_the_prefix(lib, lengths):
                 assert n.value == 0 or at % unit == 0
                 at += n.value
             assert at == P, (P, splits, at)
+
+
+def test_tiles_of_keys(lib):
+    edges = [0, 1, 127, 128, 129, 255, 256, 1000, 2 ** 30] + [2 ** 31 - 1 - k for k in (0, 1, 15, 16, 17, 126, 127, 128, 255, 256, 300)]
+    for lo in edges:
+        for hi in edges:
+            want = (hi - 1) // 128 - lo // 128 + 1 if hi > lo else 0
+            assert lib.tiles(lo, hi) == want, (lo, hi)
+            for j0 in {lo // 128 * 128, hi // 128 * 128, max(hi - 1, 0) // 128 * 128}:
+                assert bool(lib.whole(lo, hi, j0)) == (lo <= j0 and j0 + 128 <= hi), (lo, hi, j0)
