@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 2) linear_stream_kernel(con
     const int n = e / per, r = e % per, col = tile * per + r;
     if (col >= a.cols || n >= a.T) continue;
     float h = sum[n * 16 + r] + linear_bias(a, col);
-    if (gated) h = silu(h) * (sum[n * 16 + 8 + r] + linear_bias(a, a.cols + col));
+    if (gated) h = linear_silu(h) * (sum[n * 16 + 8 + r] + linear_bias(a, a.cols + col));
     else h = linear_act(a.act, h);
     linear_store(a, n, col, h);
   }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, kWalkCtas<NT>) linear_walk_
         if (gated) u += part[buf][w][n * 16 + 8 + r];
       }
       h += linear_bias(a, col);
-      if (gated) h = silu(h) * (u + linear_bias(a, a.cols + col));
+      if (gated) h = linear_silu(h) * (u + linear_bias(a, a.cols + col));
       else h = linear_act(a.act, h);
       linear_store(a, n, col, h);
     }
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(32 * kStreamWarps, 1) linear_wide_kernel(const
     // (gated: of every 16 rows, 8 gates and their ups)
     const int at = n * ROWS + (gated ? 16 * (r >> 3) + (r & 7) : r);
     float h = sum[at] + linear_bias(a, col);
-    if (gated) h = silu(h) * (sum[at + 8] + linear_bias(a, a.cols + col));
+    if (gated) h = linear_silu(h) * (sum[at + 8] + linear_bias(a, a.cols + col));
     else h = linear_act(a.act, h);
     linear_store(a, tok, col, h);
   }

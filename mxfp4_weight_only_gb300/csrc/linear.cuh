@@ -97,9 +97,16 @@ __device__ __forceinline__ float gelu(float h) {
   return h > 8.f ? h : fmaf(-a, q, fmaxf(h, 0.f));  // (h > 8: |h| q is below half a step; infinity)
 }
 
+// h / (1 + e^-h) by the exponential of -|h|, which neither overflows nor, in CUDA's own expf, loses bits with its
+// size (the fast one's argument rounds at |h| 2^-24): 2^-20 of the result, as float32 arithmetic gives.
+__device__ __forceinline__ float linear_silu(float h) {
+  const float e = expf(-fabsf(h));
+  return __fdividef(h > 0.f ? h : h * e, 1.f + e);
+}
+
 // The activation of one value (not the gated one).
 __device__ __forceinline__ float linear_act(int act, float h) {
-  if (act == LINEAR_ACT_SILU) return silu(h);
+  if (act == LINEAR_ACT_SILU) return linear_silu(h);
   if (act == LINEAR_ACT_GELU) return gelu(h);
   return h;
 }

@@ -257,7 +257,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int row, float bias,
     for (int k = 0; k < kChunk / 2; ++k) {
       const float x0 = __uint_as_float(v[2 * k]) + bias, x1 = __uint_as_float(v[2 * k + 1]) + bias;
       const float theirs = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 16);
-      h[k] = silu(up ? theirs : x0) * (up ? x1 : theirs);
+      h[k] = linear_silu(up ? theirs : x0) * (up ? x1 : theirs);
     }
     if constexpr (RES) {
 #pragma unroll
@@ -271,7 +271,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int row, float bias,
     for (int k = 0; k < kChunk; ++k) h[k] = __uint_as_float(v[k]) + bias;
     if (a.act == LINEAR_ACT_SILU) {
 #pragma unroll
-      for (int k = 0; k < kChunk; ++k) h[k] = silu(h[k]);
+      for (int k = 0; k < kChunk; ++k) h[k] = linear_silu(h[k]);
     } else if (a.act == LINEAR_ACT_GELU) {
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) h[k] = linear_act(LINEAR_ACT_GELU, h[k]);
