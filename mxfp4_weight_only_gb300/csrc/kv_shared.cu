@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
   if (tok < q.qb || tok - q.qb >= q.ql) return;  // (none's, or past max_q_len)
   const bool some = ml.y != 0.f && a.seq_lens[lo] >= 0;  // (NaN too; a negative length: an empty place in the batch)
   const int E0 = some ? __float_as_int(ml.z) : -100000;
-  const int E = __reduce_max_sync(0xffffffffu, E0);
+  // (a part's sums may just fit its own unit: those of up to 32 parts take 2^5 of it)
+  const int E = __reduce_max_sync(0xffffffffu, E0) + 5;
   float M = some ? ml.x : -INFINITY;
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
   float l = some ? w * ml.y : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (some && E0 != E) w *= exp2f((float)max(E0 - E, -300));
+  if (some) w *= exp2f((float)max(E0 - E, -300));
   const uint32_t there = __ballot_sync(0xffffffffu, some);
   float o[V];
 #pragma unroll
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     o[k] *= inv;
-    if (l != 0.f && E != 127) {  // two factors: either alone may leave the range
+    if (l != 0.f) {  // two factors: either alone may leave the range
       const int e = min(max(E - 127, -252), 252), h = e >> 1;
       o[k] = o[k] * exp2_int(h) * exp2_int(e - h);
     }
