@@ -166,6 +166,18 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   q.first = q.n - (max(end, q.qb) - q.qb);
   return q;
 }
+// Does a call with a shared prefix write the rows of token ``tok``?  Not those of an empty place of the batch, past
+// max_q_len or in no request.
+__device__ inline bool kv_row_counts(const KvAttnArgs& a, int tok) {
+  int lo = 0, hi = a.R;  // the last request that begins at or before it
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.query_start[mid] <= tok) lo = mid;
+    else hi = mid;
+  }
+  const KvRequest q = kv_request<true>(a, lo);
+  return a.seq_lens[lo] >= 0 && tok >= q.qb && tok - q.qb < q.ql;
+}
 // Page and place in it of key ``key`` of request r.
 template <bool SHARED>
 __device__ __forceinline__ int kv_page(const KvAttnArgs& a, const KvRequest& q, int r, int key) {

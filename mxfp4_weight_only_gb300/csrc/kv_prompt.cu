@@ -331,7 +331,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       const int e = kv_query_exp(range.most());
       const float fs = fabsf(a.scale) * kLog2e;
       f = mul_pow2(fs, e);
-      if (!(f < 0x1p100f)) p.odd[r] = 1;  // (f itself may have overflowed)
+      bool held = f < 0x1p100f && kv_query_finite(range.most());  // (f itself may have overflowed)
       // 2^-e in two factors (either alone may leave the range); none where the scores are all 0
       float e0 = exp2_int((-e) >> 1), e1 = exp2_int(-e - ((-e) >> 1));
       if (f == 0.f) {
@@ -345,9 +345,13 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
           const float v = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src) + c) << 16) * e0 * e1;
           rest += fabsf(v - f16_lo(f32x2_to_f16x2(v, 0.f)));
         }
-        if (kv_key_top(rest, fs, e) < kTopScale) p.odd[r] = 1;
+        held = held && kv_key_top(rest, fs, e) >= kTopScale;
       }
-      if (!kv_query_finite(range.most())) e0 = __uint_as_float(0x7FC00000u);
+      // a row that f16 does not hold is NaN, which marks the request at the end
+      if (!held) {
+        f = 1.f;
+        e0 = __uint_as_float(0x7FC00000u);
+      }
       const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
       uint8_t* dst = smem + x * C::kQBytes + trow * 128;
 #pragma unroll
@@ -507,7 +511,8 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         ok = false;
       }
       if (ok) {
-        if (l != l) p.odd[r] = 1;  // beyond kFarScore on the way (or NaN)
+        // beyond kFarScore on the way, not held or NaN (a slice of a shared prefix: only for rows whose results are used)
+        if (l != l && real && (!SHARED || r < a.R || kv_row_counts(a, i))) p.odd[r] = 1;
         tc_after();
         if constexpr (SHARED) {
           const size_t to = (size_t)rq.part * a.N * a.Hq + (size_t)(qb + i) * a.Hq + hq;
