@@ -379,6 +379,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
         break;
       }
     }
+    // the second CTA: its pair's MMAs are done before its shared and tensor memory go away, too.  (Asked once its tiles have
+    // come: from the start on, as by its idle MMA warp, the limit of this wait would be one of the whole call.)
+    if (rank == 1 && warp == 0) mbar_wait_warp(&sh.drain, 0, a.status, limit);
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- converters: thread = row of the weight
     const int group = (warp - kConvWarp) >> 2, i = (tid - 32 * kConvWarp) & 127;
@@ -589,8 +592,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
     // all issued MMAs are done before shared and tensor memory go away
     if (elect_one()) pair_commit(&sh.drain, both);
     __syncwarp();
-    mbar_wait_warp(&sh.drain, 0, a.status, limit);
-  } else {
     mbar_wait_warp(&sh.drain, 0, a.status, limit);
   }
   if (warp > kMmaWarp) cluster_wait();
