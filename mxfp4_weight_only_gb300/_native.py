@@ -110,6 +110,13 @@ SIGNATURES = {
     "moe_abi_version": (ctypes.c_int, []),
 }
 
+
+def int32(v: int) -> int:
+    """``v`` as an int32 argument.  Where it does not fit (ctypes keeps the low 32 bits), the nearest that does, which the
+    library takes or refuses as it would ``v``."""
+    return v if -0x80000000 <= v <= 0x7FFFFFFF else 0x7FFFFFFF if v > 0 else -0x80000000
+
+
 _libs = {}
 _use_checked = False
 

@@ -18,7 +18,7 @@ import ctypes
 import torch
 
 from . import _native
-from ._native import KvAttnStruct, KvRopeStruct, LinearStruct
+from ._native import KvAttnStruct, KvRopeStruct, LinearStruct, int32
 from .kv_cache import KvCacheMxfp4, _empty, _flat, _i32, _need, _queries, _rows, _stream
 
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
@@ -28,7 +28,7 @@ _BF16, _OUT = (torch.bfloat16,), (torch.bfloat16, torch.float32)
 
 def linear_workspace_bytes(T: int, N: int, K: int) -> int:
     """Bytes of workspace for ``linear_a16w4_mxfp4`` calls of these sizes."""
-    d = LinearStruct(T, K, N, 0, 0, -(-K // 8) * 8, N, N)
+    d = LinearStruct(int32(T), int32(K), int32(N), 0, 0, -(-K // 8) * 8, N, N)
     return int(_native.load().linear_mxfp4_workspace_bytes(ctypes.byref(d)))
 
 
@@ -72,6 +72,8 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
     if code is None:
         raise ValueError(f"act must be one of {tuple(_ACTS)}, got {act!r}")
     (T, K), N = xs, ws[0]
+    if N + K > 0x7FFFFFFF:  # (an int32 each in the C ABI; T: more than memory holds)
+        raise ValueError(f"the weight is too large: {N} rows of {K}")
     cols = N
     if code == 3:
         if N % 2:
@@ -162,8 +164,8 @@ def kv_append_rope_mxfp4(cache: KvCacheMxfp4, q, k, v, positions, slots, cos_sin
             _need(q_out, "q_out", _bf16, (N, Hq, D), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    r = KvRopeStruct(N, Hq, 1 if k.dtype == torch.float32 else 0, cos_sin.shape[1], 1 if interleaved else 0,
-                     min(cos_sin.shape[0], 2 ** 31 - 1), position_offset, qs, ks, vs)
+    r = KvRopeStruct(int32(N), Hq, 1 if k.dtype == torch.float32 else 0, cos_sin.shape[1], 1 if interleaved else 0,
+                     int32(cos_sin.shape[0]), int32(position_offset), qs, ks, vs)
     rc = _native.load().kv_mxfp4_append_rope(
         cache._ref, ctypes.byref(r), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
         positions.data_ptr(), slots.data_ptr(), cos_sin.data_ptr(), None if q_out is None else q_out.data_ptr(),
@@ -177,8 +179,8 @@ def attention_shared_workspace_bytes(cache: KvCacheMxfp4, R: int, N: int, Hq: in
                                      shared_blocks: int) -> int:
     """Bytes of workspace for ``attention_kv_mxfp4_shared`` calls of these sizes, or of fewer requests and rows."""
     D = cache.head_dim
-    a = KvAttnStruct(R, N, Hq, max_blocks, max_q_len, 1, 0, Hq * D, 1.0)
-    return int(_native.load().kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ctypes.byref(a), shared_blocks))
+    a = KvAttnStruct(int32(R), int32(N), int32(Hq), int32(max_blocks), int32(max_q_len), 1, 0, Hq * D, 1.0)
+    return int(_native.load().kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ctypes.byref(a), int32(shared_blocks)))
 
 
 def attention_kv_mxfp4_shared(q, cache: KvCacheMxfp4, shared_table, shared_len, block_table, seq_lens, query_start,
@@ -212,7 +214,8 @@ def attention_kv_mxfp4_shared(q, cache: KvCacheMxfp4, shared_table, shared_len, 
         _need(out, "out", torch.bfloat16, (N, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
-    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, 0, qs, D ** -0.5 if scale is None else scale)
+    sb = int32(sb)
+    a = KvAttnStruct(int32(R), N, Hq, int32(mb), int32(max_q_len), 1 if causal else 0, 0, qs, D ** -0.5 if scale is None else scale)
     lib, ref = _native.load(), ctypes.byref(a)
     if workspace is None:
         workspace = _empty(max(256, lib.kv_mxfp4_attention_shared_workspace_bytes(cache._ref, ref, sb)), torch.uint8, dev, stream)

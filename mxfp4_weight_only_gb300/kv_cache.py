@@ -18,7 +18,7 @@ from typing import NamedTuple
 import torch
 
 from . import _native
-from ._native import KvAttnStruct, KvCacheStruct
+from ._native import KvAttnStruct, KvCacheStruct, int32
 
 _i32 = torch.int32
 
@@ -217,7 +217,7 @@ def kv_gather_mxfp4(cache: KvCacheMxfp4, slots, k_out=None, v_out=None, stream=N
 def attention_workspace_bytes(cache: KvCacheMxfp4, R: int, N: int, Hq: int, max_blocks: int, max_q_len: int) -> int:
     """Bytes of workspace for ``attention_kv_mxfp4`` calls of at most these sizes' kind."""
     D = cache.head_dim
-    a = KvAttnStruct(R, N, Hq, max_blocks, max_q_len, 1, 0, Hq * D, 1.0)
+    a = KvAttnStruct(int32(R), int32(N), int32(Hq), int32(max_blocks), int32(max_q_len), 1, 0, Hq * D, 1.0)
     return int(_native.load().kv_mxfp4_attention_workspace_bytes(cache._ref, ctypes.byref(a)))
 
 
@@ -252,7 +252,7 @@ def attention_kv_mxfp4(q, cache: KvCacheMxfp4, block_table, seq_lens, query_star
     if lse is not None:
         _need(lse, "lse", torch.float32, (N, Hq), dev)
     # (a window past the C ABI's int hides nothing: no request has that many keys)
-    a = KvAttnStruct(R, N, Hq, mb, max_q_len, 1 if causal else 0, min(window, 2 ** 31 - 1), q_stride,
+    a = KvAttnStruct(int32(R), N, Hq, int32(mb), int32(max_q_len), 1 if causal else 0, int32(window), q_stride,
                      D ** -0.5 if scale is None else scale)
     lib = _native.load()
     ref = ctypes.byref(a)
