@@ -91,11 +91,9 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
     if bias is not None:
         if not isinstance(bias, _T) or bias.dtype is not _bf16 or bias.shape != (N,) or not bias.is_contiguous() or bias.get_device() != i:
             _need(bias, "bias", _bf16, (N,), x.device)
-        bias = bias.data_ptr()
     rs = cols
     if residual is not None:
         rs = _matrix(residual, "residual", _BF16, T, cols, x.device)
-        residual = residual.data_ptr()
     if out is None:
         if out_dtype not in _OUT:
             raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
@@ -112,8 +110,10 @@ def linear_a16w4_mxfp4(x, w, w_scale, bias=None, act=None, residual=None, out=No
         workspace = _empty(max(256, lib.linear_mxfp4_workspace_bytes(ref)), torch.uint8, x.device, stream)
     elif workspace.dtype is not _u8 or workspace.get_device() != i or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {x.device}")
-    rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(), bias, residual, out.data_ptr(),
-                                workspace.data_ptr(), workspace.numel(), _stream(stream, x))
+    # (arguments keep their tensors to here: one that only this call holds would give its memory to ``out`` or the workspace)
+    rc = lib.linear_a16w4_mxfp4(ref, x.data_ptr(), w.data_ptr(), w_scale.data_ptr(), None if bias is None else bias.data_ptr(),
+                                None if residual is None else residual.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                                workspace.numel(), _stream(stream, x))
     if rc:
         _native.check("linear_a16w4_mxfp4", rc)
     return out
