@@ -65,6 +65,10 @@ int linear_a16w4_mxfp4(const linear_mxfp4_t* d, const void* x, const uint8_t* w,
                        const void* bias, const void* residual, void* out, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* How a call of these sizes runs on the current device: 0, MMAs from registers; n >= 1, on
+ * the tensor cores with K split in n (1: not split).  Or a negative MOE_ERR_* code. */
+int linear_mxfp4_splits(const linear_mxfp4_t* d);
+
 /* Copy the status word (MOE_STATUS_*) of a linear layer's workspace to *status and
  * clear it.  Synchronises ``stream``. */
 int linear_mxfp4_read_status(void* workspace, uint32_t* status, void* stream);
@@ -139,6 +143,10 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
                               const int32_t* shared_table, const int32_t* shared_len, const int32_t* block_table,
                               const int32_t* seq_lens, const int32_t* query_start, void* out, float* lse, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/* How a call of these sizes runs: 0, the prefix is streamed; n >= 1, on the tensor cores, cut into
+ * n slices (fewer where the workspace is one of a larger batch).  Or a negative MOE_ERR_* code. */
+int kv_mxfp4_attention_shared_slices(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks);
 
 #ifdef __cplusplus
 }

@@ -102,10 +102,12 @@ SIGNATURES = {
     "kv_mxfp4_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "linear_mxfp4_workspace_bytes": (ctypes.c_size_t, [_LinearP]),
     "linear_a16w4_mxfp4": (ctypes.c_int, [_LinearP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "linear_mxfp4_splits": (ctypes.c_int, [_LinearP]),
     "linear_mxfp4_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]),
     "kv_mxfp4_append_rope": (ctypes.c_int, [_CacheP, _RopeP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "kv_mxfp4_attention_shared_workspace_bytes": (ctypes.c_size_t, [_CacheP, _AttnP, _i32]),
     "kv_mxfp4_attention_shared": (ctypes.c_int, [_CacheP, _AttnP, _i32] + [_vp] * 9 + [ctypes.c_size_t, _vp]),
+    "kv_mxfp4_attention_shared_slices": (ctypes.c_int, [_CacheP, _AttnP, _i32]),
     "moe_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_abi_version": (ctypes.c_int, []),
 }

@@ -18,6 +18,16 @@ bool linear_valid(const linear_mxfp4_t* d) {
          d->res_stride <= most && d->out_stride >= cols && d->out_stride <= most;
 }
 
+// The sizes of a call on a device of ``sms`` SMs.
+LinearArgs linear_sizes(const linear_mxfp4_t* d, int sms) {
+  LinearArgs a{};
+  a.T = d->T; a.K = d->K; a.N = d->N; a.act = d->act; a.f32 = d->out_is_f32 == 1;
+  a.cols = d->act == LINEAR_ACT_SWIGLU ? d->N / 2 : d->N;
+  a.x_stride = d->x_stride; a.res_stride = d->res_stride; a.out_stride = d->out_stride;
+  a.num_sms = sms;
+  return a;
+}
+
 bool shared_valid(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t blocks) {
   return cache_valid(c) && a && attn_valid(c, a) && a->window == 0 && blocks >= 1 &&
          (long long)blocks * c->page_size <= 0x7FFFFFFFll;
@@ -52,18 +62,24 @@ int linear_a16w4_mxfp4(const linear_mxfp4_t* d, const void* x, const uint8_t* w,
   int sms = 0;
   const int rc = check_device(&sms);
   if (rc != MOE_OK) return rc;
-  LinearArgs a{};
-  a.T = d->T; a.K = d->K; a.N = d->N; a.cols = (int)cols; a.act = d->act; a.f32 = d->out_is_f32 == 1;
-  a.x_stride = d->x_stride; a.res_stride = d->res_stride; a.out_stride = d->out_stride;
+  LinearArgs a = linear_sizes(d, sms);
   a.x = reinterpret_cast<const uint16_t*>(x);
   a.w = w; a.ws = w_scale;
   a.bias = reinterpret_cast<const uint16_t*>(bias);
   a.res = reinterpret_cast<const uint16_t*>(residual);
   a.out = out;
   a.status = reinterpret_cast<uint32_t*>(workspace);
-  a.num_sms = sms;
   a.wait = wait;
   return launch_linear(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int linear_mxfp4_splits(const linear_mxfp4_t* d) {
+  if (!d) return MOE_ERR_NULL;
+  if (!linear_valid(d)) return MOE_ERR_BAD_DIMS;
+  int sms = 0, splits = 0;
+  const int rc = check_device(&sms);
+  if (rc != MOE_OK) return rc;
+  return linear_splits(linear_sizes(d, sms), &splits) == cudaSuccess ? splits : MOE_ERR_CUDA;
 }
 
 int linear_mxfp4_read_status(void* workspace, uint32_t* status, void* stream) {
@@ -147,6 +163,13 @@ int kv_mxfp4_attention_shared(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* 
   g.sh.table = shared_table;
   g.sh.len = shared_len;
   return launch_kv_shared(g, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int kv_mxfp4_attention_shared_slices(const kv_mxfp4_cache_t* c, const kv_mxfp4_attn_t* a, int32_t shared_blocks) {
+  if (!c || !a) return MOE_ERR_NULL;
+  if (!shared_valid(c, a, shared_blocks)) return MOE_ERR_BAD_DIMS;
+  const KvSharedPlan plan = kv_shared_plan(view_of(c), a, shared_blocks);
+  return plan.stream ? 0 : plan.splits;
 }
 
 }  // extern "C"

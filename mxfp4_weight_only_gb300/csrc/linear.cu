@@ -499,14 +499,24 @@ cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s) {
   return launch_wide<4>(a, s);
 }
 
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+cudaError_t linear_splits(const LinearArgs& a, int* splits) {
   // 3584 -> 3584: 32 rows 9.2 us, with tcgen05 13.3; more rows take more passes over the weight
   // (in one wave of CTAs: 64 x 3584 -> 2048 9.1 and 13.1, 128 x 8192 -> 1024 15.4 and 19.1, 256 x 512 -> 512
   // 4.4 and 10.2.  In two, of middling depth: 256 x 512 -> 1024 7.8 and 10.2, 1000 x 2048 -> 256 12.0 and 15.2;
   // 96 x 3584 -> 2048 16.6 and 13.6, 64 x 256 -> 4096 7.6 and 6.6.  In three 400 x 1024 -> 1024 12.7 and 12.3.)
   const long long tiles = (long long)wide_tiles(a) * ((a.T + 31) / 32);
-  if (a.T <= 32 || tiles <= (a.K >= 512 && a.K <= 2048 ? 2 : 1) * a.num_sms) return launch_linear_stream(a, s);
-  return launch_linear_tc(a, s);
+  if (a.T <= 32 || tiles <= (a.K >= 512 && a.K <= 2048 ? 2 : 1) * a.num_sms) {
+    *splits = 0;
+    return cudaSuccess;
+  }
+  return linear_tc_splits(a, splits);
+}
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  int splits = 0;
+  const cudaError_t e = linear_splits(a, &splits);
+  if (e != cudaSuccess) return e;
+  return splits ? launch_linear_tc(a, splits, s) : launch_linear_stream(a, s);
 }
 
 }  // namespace moe

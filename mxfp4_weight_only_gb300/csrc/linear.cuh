@@ -26,9 +26,12 @@ struct LinearArgs {
 // Few rows, or few tiles: MMAs from registers (linear.cu).
 cudaError_t launch_linear_stream(const LinearArgs& a, cudaStream_t s);
 
-// Many rows: tensor cores (linear_tc.cu).
-cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s);
+// Many rows: tensor cores (linear_tc.cu), K split in ``splits``.
+cudaError_t linear_tc_splits(const LinearArgs& a, int* splits);
+cudaError_t launch_linear_tc(const LinearArgs& a, int splits, cudaStream_t s);
 
+// 0: launch_linear_stream, else the splits of launch_linear_tc.
+cudaError_t linear_splits(const LinearArgs& a, int* splits);
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -653,6 +653,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) linear_tc_kernel(const __grid_c
   }
 }
 
+int tc_m_tiles(const LinearArgs& a) {
+  const int per = a.act == LINEAR_ACT_SWIGLU ? 128 : 256;
+  return (a.cols + per - 1) / per;
+}
+
 cudaLaunchConfig_t tc_config(int splits, unsigned clusters, cudaLaunchAttribute* attr, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * splits * clusters);
@@ -712,18 +717,25 @@ cudaError_t launch_tc(const LinearArgs& a, int m_tiles, int splits, cudaStream_t
 // 64 x 3584 -> 3584, 14 tiles, 24.0 / 17.2 / 15.0 / 14.5 in 1 / 2 / 3 / 4, and
 // 128 x 3584 -> 4608, 18 tiles, whose 18 clusters of 8 do not fit at once, 24.9 / 18.3 /
 // 17.1 / 29.2; 64 x 512 -> 1024, two quads, 8.8 unsplit and 10.0 in 2).
-cudaError_t launch_linear_tc(const LinearArgs& a, cudaStream_t s) {
-  const int per = a.act == LINEAR_ACT_SWIGLU ? 128 : 256;
-  const int m_tiles = (a.cols + per - 1) / per, quads = (a.K + 255) / 256;
-  const long long tiles = (long long)m_tiles * ((a.T + BN - 1) / BN);
+cudaError_t linear_tc_splits(const LinearArgs& a, int* splits) {
+  const long long tiles = (long long)tc_m_tiles(a) * ((a.T + BN - 1) / BN);
+  const int quads = (a.K + 255) / 256;
   for (int n = 4; n > 1; --n) {
     if (quads < 3 * n || 2 * n * tiles > a.num_sms) continue;
     int fit = 0;
     const cudaError_t e = resident_clusters(n, &fit);
     if (e != cudaSuccess) return e;
-    if (tiles <= fit) return launch_tc<true>(a, m_tiles, n, s);
+    if (tiles <= fit) {
+      *splits = n;
+      return cudaSuccess;
+    }
   }
-  return launch_tc<false>(a, m_tiles, 1, s);
+  *splits = 1;
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_tc(const LinearArgs& a, int splits, cudaStream_t s) {
+  return splits > 1 ? launch_tc<true>(a, tc_m_tiles(a), splits, s) : launch_tc<false>(a, tc_m_tiles(a), 1, s);
 }
 
 }  // namespace moe
