@@ -125,8 +125,8 @@ size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, cons
 
 /*
  * out = softmax over the prefix's keys and the request's own, as kv_mxfp4_attention
- * (its types, formulas, precision and status word; weights of the prefix's keys have
- * 16 bits whatever the rows):
+ * (its types, formulas, precision and status word: weights have 16 bits, in requests of
+ * many rows, prompts, perhaps 11):
  *   shared_table  int32 [shared_blocks]  pages of the prefix; a page id outside the
  *                 cache makes its tokens invisible
  *   shared_len    int32 [1]  keys of the prefix (at most shared_blocks * page_size

@@ -166,6 +166,36 @@ __device__ __forceinline__ KvRequest kv_request(const KvAttnArgs& a, int r) {
   q.first = q.n - (max(end, q.qb) - q.qb);
   return q;
 }
+// The last request that begins at or before token ``tok``, -1 for none: 32 candidates at a time (the whole warp calls it).
+__device__ __forceinline__ int kv_request_at(const KvAttnArgs& a, int tok) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.R;  // it is one of lo .. lo + n - 1, or the token is none's
+  while (n > 1) {
+    const int step = (n + 31) / 32, k = lane * step;
+    const bool begun = k < n && a.query_start[lo + k] <= tok;
+    const int c = __popc(__ballot_sync(0xffffffffu, begun));
+    if (c == 0) return -1;
+    lo += (c - 1) * step;
+    n = min(step, n - (c - 1) * step);
+  }
+  return lo;
+}
+// Is one of the tokens first .. last of a request that is streamed without a prefix, of at most ``limit`` rows (the whole warp
+// calls it)?
+__device__ __forceinline__ bool kv_few_rows_among(const KvAttnArgs& a, int G, int limit, int first, int last) {
+  const int lane = threadIdx.x & 31;
+  for (int r0 = max(kv_request_at(a, first), 0); r0 < a.R; r0 += 32) {
+    bool few = false, past = true;
+    if (r0 + lane < a.R) {
+      const KvRequest q = kv_request<true>(a, r0 + lane);
+      past = q.qb > last;
+      few = !past && q.ql > 0 && q.qb + q.ql > first && (long long)q.ql * G <= limit;
+    }
+    if (__any_sync(0xffffffffu, few)) return true;
+    if (__any_sync(0xffffffffu, past)) return false;
+  }
+  return false;
+}
 // Does a call with a shared prefix write the rows of token ``tok``?  Not those of an empty place of the batch, past
 // max_q_len or in no request.
 __device__ inline bool kv_row_counts(const KvAttnArgs& a, int tok) {

@@ -23,8 +23,8 @@
 // enter as f16 times a power of two per row (exact down to 2^-31 of the row's
 // largest; a row with smaller ones that could tell marks its request: see
 // kQueryExp), weights as f16 of p 2^9 (11 bits down to p = 2^-23 of the reference,
-// multiples of 2^-33 below), in items with few keys and for a shared prefix as two bf16
-// (kFewKeys).
+// multiples of 2^-33 below), in items with few keys and in those of a shared prefix with
+// decoding rows as two bf16 (kFewKeys).
 // While one tile's softmax runs, the tensor core works on the other tile.  Each
 // query tile has an issuing thread of its own: a thread that issues MMAs keeps
 // only a short queue, so its barrier probes and commits (about 100 cycles each)
@@ -56,9 +56,9 @@ constexpr float kSlack = 6.f, kWeightExp = 9.f;
 // in two products.  (64 query and 8 kv heads, 256 keys: 32 requests of 64 tokens 70
 // us, with one f16 weight 64, in the streaming kernel 225; 16 of 256 tokens 115,
 // 105 and 524.)
-// Slices of a shared prefix do so whatever their keys: their rows are all the call's, those
-// of decoding requests among them, whose weights have 16 bits without a prefix too.  (28 / 4
-// heads of 128: 64 requests behind 32,768 tokens 87 us, with one f16 weight 82; 256 behind 8192 93 and 88.)
+// So do row tiles of a shared prefix's slices, whatever their keys, with a row of a request that is streamed without a
+// prefix, where its weights have 16 bits.  (28 / 4 heads of 128: 64 requests behind 32,768 tokens 87 us, with one
+// f16 weight 82; 256 behind 8192 93 and 88.)
 constexpr int kFewKeys = 256;
 // A weight is off by up to a unit in the last place of its row's reference
 // (products S f unrounded, the reference and its sum with kWeightExp rounded): from
@@ -82,6 +82,7 @@ struct PromptParams {
   KvAttnArgs a;
   int G, row_limit;
   int slice_tiles;  // shared prefix: row tiles of a slice at most, 0: its slices are streamed
+  bool few_rows;    // shared prefix: no request has more than row_limit rows
   int32_t* odd;  // [R] set for requests with scales outside the exact range
 };
 
@@ -795,13 +796,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) kv_prompt_kernel(const Prom
     if (SHARED && (int)blockIdx.x < slices) {
       const int of = blockIdx.x / (p.slice_tiles * H), in = blockIdx.x % (p.slice_tiles * H);
       const KvRequest rq = kv_request<SHARED>(a, a.R + of);
-      const long long rows = (long long)rq.ql * p.G;
-      if (lane == 0 && rows > a.sh.row_limit && rows > (long long)(in / H) * 256) {
-        item[0] = a.R + of;
-        item[1] = in % H;
-        item[2] = in / H * 256;
-        item[3] = 1;
-        request = rq;
+      const long long rows = (long long)rq.ql * p.G, row0 = (long long)(in / H) * 256;
+      if (rows > a.sh.row_limit && rows > row0) {
+        const int last = (int)((min(row0 + 256, rows) - 1) / p.G);
+        const bool few = p.few_rows || rq.n <= kFewKeys || kv_few_rows_among(a, p.G, p.row_limit, (int)(row0 / p.G), last);
+        if (lane == 0) {
+          item[0] = a.R + of;
+          item[1] = in % H;
+          item[2] = (int)row0;
+          item[3] = few;
+          request = rq;
+        }
       }
     }
     const long long block = SHARED && (int)blockIdx.x < slices ? -1 : (long long)blockIdx.x - slices;
@@ -893,7 +898,8 @@ cudaError_t launch_kv_prompt(const KvAttnArgs& a, int row_limit, int32_t* odd, c
   if (a.sh.splits > 0) {
     // a slice of a shared prefix has all rows (fewer than the limit are streamed)
     p.slice_tiles = rows > a.sh.row_limit ? (int)((rows + 255) / 256) : 0;
-    if ((long long)a.max_q_len * p.G <= row_limit) grid = 0;  // no request of its own has enough rows
+    p.few_rows = (long long)a.max_q_len * p.G <= row_limit;
+    if (p.few_rows) grid = 0;  // no request of its own has enough rows
     grid += (long long)p.slice_tiles * a.sh.splits * a.cache.heads;
     if (grid == 0) return cudaSuccess;
     return a.cache.D == 128 ? launch_prompt<128, true>(p, (unsigned)grid, s) : launch_prompt<64, true>(p, (unsigned)grid, s);

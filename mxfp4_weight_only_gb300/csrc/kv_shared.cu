@@ -51,17 +51,8 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
   // lane p: part p
   float4 ml = make_float4(-INFINITY, 0.f, 0.f, 0.f);
   if (lane < parts) ml = a.sh.ml[lane * all + row];
-  // the token's request: the last that begins at or before it, 32 candidates at a time
-  const int tok = (int)(row / a.Hq);
-  int lo = 0, n = a.R;  // it is one of lo .. lo + n - 1, or the token is none's
-  while (n > 1) {
-    const int step = (n + 31) / 32, k = lane * step;
-    const bool begun = k < n && a.query_start[lo + k] <= tok;
-    const int c = __popc(__ballot_sync(0xffffffffu, begun));
-    if (c == 0) return;
-    lo += (c - 1) * step;
-    n = min(step, n - (c - 1) * step);
-  }
+  const int tok = (int)(row / a.Hq), lo = kv_request_at(a, tok);
+  if (lo < 0) return;
   const KvRequest q = kv_request<true>(a, lo);
   if (tok < q.qb || tok - q.qb >= q.ql) return;  // (none's, or past max_q_len)
   const bool some = ml.y != 0.f && a.seq_lens[lo] >= 0;  // (NaN too; a negative length: an empty place in the batch)
