@@ -63,18 +63,24 @@ class Layer:
         f = 10000.0 ** (-torch.arange(0, head_dim, 2, device="cuda", dtype=torch.float64) / head_dim)
         angle = torch.arange(positions, device="cuda", dtype=torch.float64)[:, None] * f
         self.cos_sin = torch.cat((angle.cos(), angle.sin()), 1).float()
+        # (its status word says when a wait ran out; the size does not depend on the rows)
+        self.work = torch.zeros(max(m.linear_workspace_bytes(1, w.shape[0], 2 * w.shape[1]) for w in (
+            self.wqkv, self.wo, self.shared13, self.shared2)), dtype=torch.uint8, device="cuda")
+
+    def linear(self, x, w, s, **kw):
+        return m.linear_a16w4_mxfp4(x, w, s, workspace=self.work, **kw)
 
     def project(self, x):
         """Queries, keys and values of x [N, hidden], slices of one [N, heads, head_dim] tensor."""
-        qkv = m.linear_a16w4_mxfp4(x, self.wqkv, self.sqkv, bias=self.bqkv).view(len(x), -1, self.head_dim)
+        qkv = self.linear(x, self.wqkv, self.sqkv, bias=self.bqkv).view(len(x), -1, self.head_dim)
         return qkv, qkv[:, :self.heads], qkv[:, self.heads:-self.kv_heads], qkv[:, -self.kv_heads:]
 
     def experts(self, hidden):
         """The routed experts and the shared one, added to the residual stream."""
         ids, weights = m.moe_router_topk((hidden @ self.router.T).float(), self.topk)
         moe = m.moe_a16w4_mxfp4(hidden, ids, weights, self.w13, self.s13, self.w2, self.s2)
-        gated = m.linear_a16w4_mxfp4(hidden, self.shared13, self.shared_s13, act="swiglu")
-        return m.linear_a16w4_mxfp4(gated, self.shared2, self.shared_s2, residual=hidden + moe), moe, gated
+        gated = self.linear(hidden, self.shared13, self.shared_s13, act="swiglu")
+        return self.linear(gated, self.shared2, self.shared_s2, residual=hidden + moe), moe, gated
 
 
 class Server:
@@ -91,20 +97,24 @@ class Server:
         self.free_ring = torch.arange(first, first + pages, **i32)
         self.ring_state = torch.tensor([0, pages], **i32)
         self.lens = torch.zeros(requests, **i32)
-        self.workspace = torch.zeros(0, dtype=torch.uint8, device="cuda")
+        need = m.attention_workspace_bytes(self.cache, 1, P, layer.heads, first, P)
+        self.workspace = torch.zeros(need, dtype=torch.uint8, device="cuda")
         # the prefix runs as one prompt on its own pages
         _, q, k, v = layer.project(prefix)
         at = torch.arange(P, **i32)
         q = m.kv_append_rope_mxfp4(self.cache, q, k, v, at, at, layer.cos_sin)
         start = torch.tensor([0, P], **i32)
-        attn = m.attention_kv_mxfp4(q, self.cache, self.shared_table[None], self.shared_len, start, P)
-        hidden = m.linear_a16w4_mxfp4(attn.flatten(1), layer.wo, layer.so, residual=prefix)
+        attn = m.attention_kv_mxfp4(q, self.cache, self.shared_table[None], self.shared_len, start, P,
+                                    workspace=self.workspace)
+        hidden = layer.linear(attn.flatten(1), layer.wo, layer.so, residual=prefix)
         self.prefix_out = layer.experts(hidden)[0]  # what the next layer's prefix would be
 
     def check(self):
-        """Raises if a wait of an attention since the last check ran out (its outputs are invalid)."""
-        if self.workspace.numel() and m.attention_read_status(self.workspace):
+        """Raises if a wait of an attention or a linear layer since the last check ran out (its outputs are invalid)."""
+        if m.attention_read_status(self.workspace):
             raise RuntimeError("an attention kernel gave up waiting")
+        if m.linear_read_status(self.layer.work):
+            raise RuntimeError("a linear layer's kernel gave up waiting")
 
     def step(self, x, new_lens, max_q_len):
         """``x`` bf16 [tokens, hidden], the tokens of ``new_lens`` (int32 [requests], -1: finished) in order."""
@@ -121,7 +131,7 @@ class Server:
             self.workspace = torch.zeros(need, dtype=torch.uint8, device="cuda")
         attn = m.attention_kv_mxfp4_shared(q, self.cache, self.shared_table, self.shared_len, self.block_table,
                                            tables.seq_lens, tables.query_start, max_q_len, workspace=self.workspace)
-        hidden = m.linear_a16w4_mxfp4(attn.flatten(1), L.wo, L.so, residual=x)
+        hidden = L.linear(attn.flatten(1), L.wo, L.so, residual=x)
         y, moe, gated = L.experts(hidden)
         # a refused request (-1) keeps its length and pages: the caller gives its tokens again
         self.lens.copy_(torch.where(tables.seq_lens < 0, self.lens, tables.seq_lens))
