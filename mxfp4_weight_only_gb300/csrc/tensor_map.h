@@ -3,6 +3,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "moe_internal.h"
 #ifdef __CUDACC__
 #include "common.cuh"
@@ -15,15 +17,16 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline cudaError_t get_encoder(EncodeTiledFn* fn) {
-  static EncodeTiledFn cached = nullptr;
-  if (!cached) {
+  static std::atomic<EncodeTiledFn> cached{nullptr};  // (host threads may call at once)
+  *fn = cached.load(std::memory_order_acquire);
+  if (!*fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
     cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
     if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr) return e != cudaSuccess ? e : cudaErrorNotSupported;
-    cached = reinterpret_cast<EncodeTiledFn>(ptr);
+    *fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    cached.store(*fn, std::memory_order_release);
   }
-  *fn = cached;
   return cudaSuccess;
 }
 
