@@ -112,6 +112,9 @@ int kv_mxfp4_append_rope(const kv_mxfp4_cache_t* c, const kv_mxfp4_rope_t* r, co
  * Attention of a batch whose requests share a cached prefix, which is read once for
  * all of them.  The prefix has pages of its own, as has what each request holds
  * after it (so a request's own keys begin on a page of their own, numbered from 0).
+ * It is for decoding batches behind a long prefix, from some 200,000 tokens of prefix times
+ * requests on; below, and for prompts, kv_mxfp4_attention with the prefix's pages repeated
+ * in every request's table takes as long or less.
  *   a              as in kv_mxfp4_attention; max_blocks, seq_lens, query_start and
  *                  positions are those of the requests' own tokens; window is 0
  *   shared_blocks  entries of shared_table, >= 1
@@ -135,7 +138,7 @@ size_t kv_mxfp4_attention_shared_workspace_bytes(const kv_mxfp4_cache_t* c, cons
  *                 and keys; every row sees the whole prefix, and its own keys as
  *                 without one.  Length 0: only the prefix.  A negative length: the
  *                 request sees nothing, not the prefix either (an empty place in the
- *                 batch: zeros, lse -inf).
+ *                 batch: zeros, lse -inf, whatever its rows of q hold).
  *   query_start   int32 [R+1], not descending
  * The rest as in kv_mxfp4_attention.
  */

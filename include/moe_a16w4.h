@@ -302,9 +302,10 @@ int moe_read_status(const moe_dims_t* d, void* workspace, uint32_t* status, void
  *   extra_waiters  for tests of the give-up path: the fused decode kernel's
  *                  wait for all of its CTAs' gate_up results expects this many
  *                  CTAs more than it launched, so that wait runs out after
- *                  limit_ns; so do, in kv_mxfp4_attention, the waits for the
- *                  cache's records and for the weights of a tile (0..64; 0 for
- *                  normal use)
+ *                  limit_ns; so do, in kv_mxfp4_attention and its form behind a
+ *                  shared prefix, the waits for the cache's records and for the
+ *                  weights of a tile, in linear_a16w4_mxfp4 those for a stage
+ *                  (0..64; 0 for normal use)
  * Returns MOE_ERR_BAD_DIMS for limit_ns = 0 or extra_waiters outside [0, 64].
  */
 int moe_set_wait_limit(uint64_t limit_ns, int32_t extra_waiters);

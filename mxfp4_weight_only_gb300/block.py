@@ -194,7 +194,9 @@ def attention_kv_mxfp4_shared(q, cache: KvCacheMxfp4, shared_table, shared_len, 
     from 0 (the step's new tokens included); 0: only the prefix, negative: an empty
     place in the batch, whose rows are zeros (lse -inf).  Every row sees the whole prefix.  The rest as
     ``attention_kv_mxfp4``; the workspace's size is ``attention_shared_workspace_bytes``, its status
-    is read by ``attention_read_status``."""
+    is read by ``attention_read_status``.  For decoding batches behind a long prefix (some 200,000 tokens of
+    prefix times requests); for less, and for prompts, ``attention_kv_mxfp4`` with the prefix's pages repeated in
+    every row of ``block_table`` takes as long or less."""
     dev = cache.device
     N, Hq, qs = _queries(q, cache, torch.bfloat16)
     D = cache.head_dim

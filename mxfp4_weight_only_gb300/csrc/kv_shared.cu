@@ -10,10 +10,13 @@
 // streamed; many: tensor cores, one CTA per 256 rows, kv head and slice).  The requests' own
 // keys are parts too.  kv_join_kernel joins a row's parts.
 //
-// Measured, 28 / 4 heads of 128: 64 requests behind 32,768 tokens, up to 2048 own, 76 us: prefix 40
-// (14 tiles of 128 keys a CTA at 2.1 us, 7 us until the first scores, 4 after the last), own keys 20,
-// items cut between CTAs 4, parts joined 6.  4 requests behind 100,003: 54 us, the streaming
-// kernel's issue.
+// Measured, 28 / 4 heads of 128: 64 requests behind 32,768 tokens, up to 2048 own, 81 us: prefix 44
+// (14 tiles of 128 keys a CTA at 2.3 us, 11 us before the first scores and after the last), own keys 20,
+// items cut between CTAs 4, parts joined 6; through attention_kv_mxfp4, the prefix's pages repeated in every
+// request's table, 266.  4 requests behind 100,003: 54 us (60), the streaming kernel's issue.
+// Less than some 200,000 tokens of prefix times requests are not worth it (16 requests behind 10,240
+// tokens 39 us either way, behind 256 32 and 19), nor are prompts, which the tensor cores
+// bound (16 of 512 tokens behind 8192: 972 and 784): part sums and launches more.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -119,9 +122,13 @@ SharedLayout shared_layout(int D, int R, int N, int Hq, int splits) {
 // its pieces, which warps and CTAs share; all SMs work on it.  On the tensor cores, cut into slices: as many as
 // shorten that kernel's waves (a CTA of 256 rows takes about 16 ns a key and some 5 us besides),
 // against what a slice's sums cost to write and read (about 4 bytes a picosecond); 9 us for
-// the launch and its marks.  Measured, streamed and on the tensor cores: 64 requests, 4 x 7 heads of
-// 128: 16 keys 16 and 35 us, 2400 32 and 37, 5000 46 and 39; 12 requests: 10,000 keys 28 and 35;
-// 256 requests: 300 keys 44 and 39; 28 rows, 100,003 keys 54 and 86.
+// the launch and its marks.  The constants are of 128-wide heads; a fit to times of both gives 6.9 ns
+// and 3.6 us, 18 ns and 2 us, and 7 us for the launch, beside what both ways share; what counts is the
+// choice.  Measured with both ways and up to nine cuts each, 351 batches (1 to 256 requests, 16 to 100,352
+// keys, 1 to 8 kv heads of 1 to 16 query heads, 64 and 128 wide): it takes 0.1 % more than the best of them on average,
+// 8 % at most.  Streamed and on the tensor cores, 4 x 7 heads of 128, caches cold: 64 requests 16 keys 24 and 43
+// us, 2560 41 and 44, 5120 55 and 47; 16 requests 10,240 keys 39 and 45, 30,720 68 and 56; 128 requests 256 keys
+// 35 and 41; 28 rows, 100,352 keys 67 and 97.
 KvSharedPlan kv_shared_plan(const KvView& c, const kv_mxfp4_attn_t* a, int blocks) {
   const long long rows = (long long)a->N * (a->Hq / c.heads);
   const long long tiles = (rows + 255) / 256 * c.heads, keys = (long long)blocks << c.page_shift;

@@ -4,7 +4,8 @@
 // Measured: 8192 rows x 3584 -> 2 x 3584 gated 234 us, 1,800 TFLOP/s (92 % of the library's
 // bf16 matrix product; 265 us on data that draws more power), tensor pipe 76 % active: a
 // step's conversions (580 to 690 cycles) are a little longer than its MMAs (512).  250 x 3584 ->
-// 8192 21.2 us: 28 steps of 0.3 us, 6 us to the first MMA and after the last, 4 us of sums handed over.
+// 8192, K split in two, 22 us: by the slope over K 28 steps of 0.31 us and 13 us beside them (unsplit 10.6): launch, first
+// loads and conversion, sums handed over, epilogue.
 //
 //   D[256 rows of the weight][up to BN tokens] += W[256][16] x[tokens][16]^T
 //
