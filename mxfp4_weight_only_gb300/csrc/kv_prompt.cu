@@ -349,10 +349,7 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
         held = held && kv_key_top(rest, fs, e) >= kTopScale;
       }
       // a row that f16 does not hold is NaN, which marks the request at the end
-      if (!held) {
-        f = 1.f;
-        e0 = __uint_as_float(0x7FC00000u);
-      }
+      if (!held) e0 = __uint_as_float(0x7FC00000u);
       const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
       uint8_t* dst = smem + x * C::kQBytes + trow * 128;
 #pragma unroll
@@ -513,7 +510,8 @@ __device__ __forceinline__ void prompt_item(const PromptParams& p, uint8_t* smem
       }
       if (ok) {
         // beyond kFarScore on the way, not held or NaN (a slice of a shared prefix: only for rows whose results are used)
-        if (l != l && real && (!SHARED || r < a.R || kv_row_counts(a, i))) p.odd[r] = 1;
+        if (l != l && (!SHARED || r < a.R || (real && kv_row_counts(a, i)))) p.odd[r] = 1;
+        __syncwarp();  // (the lookup may part the lanes; loads of tensor memory take them together)
         tc_after();
         if constexpr (SHARED) {
           const size_t to = (size_t)rq.part * a.N * a.Hq + (size_t)(qb + i) * a.Hq + hq;
