@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const KvAttnArgs a) {
   float l = some ? w * ml.y : 0.f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (some) w *= exp2f((float)max(E0 - E, -300));
+  if (some) w *= exp2_int(E0 - E);  // (units of 2^0 .. 2^42: -47 at least)
   const uint32_t there = __ballot_sync(0xffffffffu, some);
   float o[V];
 #pragma unroll
